@@ -31,7 +31,8 @@ __all__ = [
     "moe_deq_swiglu_quant", "token_scales_of", "MOE_EPILOGUE_MAX_N", "moe_grouped_gemm_i8",
     "MOE_GEMM_MAX_K", "MOE_GEMM_MAX_N", "MOE_GEMM_MAX_GROUPS", "moe_layout_no_alloc",
     "moe_gemm_swiglu_quant_workspace_bytes", "moe_grouped_gemm_swiglu_quant_i8",
-    "MOE_NO_ALLOC_SCRATCH_BYTES",
+    "MOE_NO_ALLOC_SCRATCH_BYTES", "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MOE_ROUTE_MAX_GROUPS", "moe_route",
+    "moe_route_backward", "moe_combine_backward", "moe_combine_backward_src", "moe_grouped_gemm_deq_i8",
 ]
 
 MOE_BF16, MOE_FP16, MOE_FP32, MOE_INT8_ROWSCALE = 0, 1, 2, 3
@@ -39,6 +40,8 @@ MOE_MAX_EXPERTS, MOE_MAX_HIDDEN, MOE_MAX_TOPK, MOE_MAX_SOURCES = 2048, 16384, 32
 MOE_EPILOGUE_MAX_N = 4096
 MOE_GEMM_MAX_K = MOE_GEMM_MAX_N = MOE_GEMM_MAX_GROUPS = 65536
 MOE_NO_ALLOC_SCRATCH_BYTES = 1 << 20
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_ROUTE_MAX_GROUPS = 64
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe_ep.so")
 
@@ -71,6 +74,16 @@ _SIGS = {
     "moe_gemm_swiglu_quant_workspace_bytes": ([_I32, _I32, ctypes.POINTER(_SZ)], _INT),
     "moe_grouped_gemm_swiglu_quant_i8": ([_P, ctypes.c_int64, _I32, _I32, _P, _I32, _P, _I32, _P, _P,
                                           ctypes.c_int64, _P, _SZ, _P, _SZ, _P], _INT),
+    "moe_route": ([_P, _INT, ctypes.c_int64, _I32, _I32, _I32, _INT, _P, _I32, _I32, _I32, _INT, ctypes.c_float, _P,
+                   _P, _P, _P], _INT),
+    "moe_route_backward": ([_P, _P, _INT, ctypes.c_int64, _P, _I32, _I32, _I32, _INT, _INT, ctypes.c_float, _P,
+                            ctypes.c_int64, _P], _INT),
+    "moe_combine_backward": ([_P, _INT, _P, _INT, _SZ, _I32, _I32, _I32, _P, _P, _P, _P, _P, _I32, _I32, _P, _SZ, _P,
+                              _P], _INT),
+    "moe_combine_backward_src": ([_P, _INT, _P, _INT, _SZ, _I32, _I32, _I32, _P, _P, _P, _P, _P, _I32, _I32, _I32,
+                                  _I32, _P, _SZ, _P, _P], _INT),
+    "moe_grouped_gemm_deq_i8": ([_P, ctypes.c_int64, _I32, _I32, _P, _I32, _P, _I32, _P, _P, ctypes.c_int64, _P, _INT,
+                                 _SZ, _P], _INT),
     "moe_status_str": ([_INT], ctypes.c_char_p),
     "moe_last_hip_error": ([], _INT),
 }
@@ -477,6 +490,145 @@ def moe_grouped_gemm_swiglu_quant_i8(a: torch.Tensor, a_row_bytes: int, rows: in
         _dev(w, "w"), n, _dev(weight_scale, "weight_scale", torch.float32), token_scale.data_ptr(),
         token_scale_stride, _dev(out, "out"), out.numel() * out.element_size(), _dev(workspace, "workspace"),
         workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def _logit_rows(t: torch.Tensor, name: str) -> int:
+    """The row stride, in elements, of [bs, num_experts] logits whose rows are
+    dense (the rows themselves may lie apart)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [bs, num_experts]")
+    bs, e = t.shape
+    if e > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have dense rows")
+    if bs > 1 and t.stride(0) < e:
+        raise ValueError(f"{name}'s rows overlap")
+    return t.stride(0) if bs > 1 else e
+
+
+def moe_route(logits: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor, score: int,
+              bias: Optional[torch.Tensor] = None, num_groups: int = 1, topk_groups: int = 1, group_top: int = 1,
+              renormalize: bool = True, scale: float = 1.0, token_mask: Optional[torch.Tensor] = None,
+              stream=None) -> None:
+    """The router: logits [bs, num_experts] (bf16, fp16 or fp32, rows dense) ->
+    topk_idx int32 and topk_weights float32 [bs, topk].  ``score`` is
+    MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID; ``bias`` float32 [num_experts]
+    counts for the choice alone; of num_groups groups the topk_groups with the
+    largest value (their best expert's, or the sum of their two best scores
+    with group_top 2) keep their experts; token_mask (uint8 or bool [bs])
+    takes a token out where it is 0.  Entries without an eligible expert get
+    id -1 and weight 0."""
+    stride = _logit_rows(logits, "logits")
+    bs, e = logits.shape
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != bs:
+        raise ValueError("topk_idx must be [bs, topk]")
+    topk = topk_idx.shape[1]
+    if topk_weights.shape != topk_idx.shape:
+        raise ValueError("topk_weights must be [bs, topk]")
+    _need(bias, "bias", e)
+    _need(token_mask, "token_mask", bs)
+    if token_mask is not None and token_mask.dtype not in (torch.uint8, torch.bool):
+        raise ValueError("token_mask must be uint8 or bool")
+    _check("moe_route", _lib.moe_route(
+        logits.data_ptr(), dtype_code(logits.dtype), stride, bs, e, topk, score,
+        _dev(bias, "bias", torch.float32, optional=True), num_groups, topk_groups, group_top,
+        1 if renormalize else 0, scale, _dev(token_mask, "token_mask", optional=True),
+        _dev(topk_idx, "topk_idx", torch.int32), _dev(topk_weights, "topk_weights", torch.float32), _stream(stream)))
+
+
+def moe_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_idx: torch.Tensor, score: int,
+                       grad_logits: torch.Tensor, renormalize: bool = True, scale: float = 1.0,
+                       stream=None) -> None:
+    """The router's gradient: grad_weights float32 [bs, topk] -> grad_logits
+    [bs, num_experts] of logits' type, every element written.  topk_idx, score,
+    renormalize and scale as ``moe_route`` gave and had them."""
+    stride, grad_stride = _logit_rows(logits, "logits"), _logit_rows(grad_logits, "grad_logits")
+    bs, e = logits.shape
+    if grad_logits.shape != logits.shape or grad_logits.dtype != logits.dtype:
+        raise ValueError("grad_logits must have logits' shape and type")
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != bs or grad_weights.shape != topk_idx.shape:
+        raise ValueError("topk_idx and grad_weights must be [bs, topk]")
+    _check("moe_route_backward", _lib.moe_route_backward(
+        _dev(grad_weights, "grad_weights", torch.float32), logits.data_ptr(), dtype_code(logits.dtype), stride,
+        _dev(topk_idx, "topk_idx", torch.int32), bs, e, topk_idx.shape[1], score, 1 if renormalize else 0, scale,
+        grad_logits.data_ptr(), grad_stride, _stream(stream)))
+
+
+def _combine_backward_sizes(grad_out, topk_idx, topk_weights, send_token_idx, grad_weights):
+    if grad_out.dim() != 2 or topk_idx.dim() != 2 or grad_out.shape[0] != topk_idx.shape[0]:
+        raise ValueError("grad_out must be [bs, hidden] and topk_idx [bs, topk]")
+    (bs, hidden), topk = grad_out.shape, topk_idx.shape[1]
+    for t, name in ((topk_weights, "topk_weights"), (send_token_idx, "send_token_idx"), (grad_weights, "grad_weights")):
+        _need(t, name, bs * topk)
+    return bs, hidden, topk
+
+
+def moe_combine_backward(grad_out: torch.Tensor, recv_x: torch.Tensor, recv_type: int, topk_idx: torch.Tensor,
+                         topk_weights: torch.Tensor, send_token_idx: torch.Tensor, put_offset: torch.Tensor,
+                         recv_base: torch.Tensor, expert_num_per_rank: int, rank_size: int,
+                         grad_recv: torch.Tensor, grad_weights: torch.Tensor, stream=None) -> None:
+    """The combine's gradient: grad_out [bs, hidden] and the receive buffer
+    combine read (recv_type MOE_BF16 or MOE_FP16) -> grad_recv, the rows'
+    gradients in the rows' places (may be recv_x itself), and grad_weights
+    float32 [bs, topk]."""
+    bs, hidden, topk = _combine_backward_sizes(grad_out, topk_idx, topk_weights, send_token_idx, grad_weights)
+    _need_routes(expert_num_per_rank, rank_size, put_offset, recv_base)
+    _check("moe_combine_backward", _lib.moe_combine_backward(
+        _dev(grad_out, "grad_out"), dtype_code(grad_out.dtype), _dev(recv_x, "recv_x"), recv_type,
+        recv_x.numel() * recv_x.element_size(), bs, hidden, topk, _dev(topk_idx, "topk_idx", torch.int32),
+        _dev(topk_weights, "topk_weights", torch.float32), _dev(send_token_idx, "send_token_idx", torch.int32),
+        _dev(put_offset, "put_offset", torch.int32), _dev(recv_base, "recv_base", torch.int32), expert_num_per_rank,
+        rank_size, _dev(grad_recv, "grad_recv"), grad_recv.numel() * grad_recv.element_size(),
+        _dev(grad_weights, "grad_weights", torch.float32), _stream(stream)))
+
+
+def moe_combine_backward_src(grad_out: torch.Tensor, recv_x: torch.Tensor, recv_type: int, topk_idx: torch.Tensor,
+                             topk_weights: torch.Tensor, send_token_idx: torch.Tensor, put_offset: torch.Tensor,
+                             recv_base: torch.Tensor, expert_num_per_rank: int, rank_size: int, src_rank: int,
+                             grad_recv: torch.Tensor, grad_weights: torch.Tensor, stream=None) -> None:
+    """The combine's gradient for source ``src_rank``; put_offset is [E, num_src]."""
+    if put_offset.dim() != 2:
+        raise ValueError("put_offset must be [E, num_src]")
+    bs, hidden, topk = _combine_backward_sizes(grad_out, topk_idx, topk_weights, send_token_idx, grad_weights)
+    _need_routes(expert_num_per_rank, rank_size, put_offset, recv_base, put_offset.shape[1])
+    _check("moe_combine_backward_src", _lib.moe_combine_backward_src(
+        _dev(grad_out, "grad_out"), dtype_code(grad_out.dtype), _dev(recv_x, "recv_x"), recv_type,
+        recv_x.numel() * recv_x.element_size(), bs, hidden, topk, _dev(topk_idx, "topk_idx", torch.int32),
+        _dev(topk_weights, "topk_weights", torch.float32), _dev(send_token_idx, "send_token_idx", torch.int32),
+        _dev(put_offset, "put_offset", torch.int32), _dev(recv_base, "recv_base", torch.int32), expert_num_per_rank,
+        rank_size, put_offset.shape[1], src_rank, _dev(grad_recv, "grad_recv"),
+        grad_recv.numel() * grad_recv.element_size(), _dev(grad_weights, "grad_weights", torch.float32),
+        _stream(stream)))
+
+
+def moe_grouped_gemm_deq_i8(a: torch.Tensor, a_row_bytes: int, rows: int, k: int, group_count: torch.Tensor,
+                            w: torch.Tensor, weight_scale: torch.Tensor, token_scale: torch.Tensor,
+                            out: torch.Tensor, token_scale_stride: int = 4, stream=None) -> None:
+    """Second expert matmul: ``a``, a_row_bytes, rows, k and group_count as for
+    ``moe_grouped_gemm_i8``; w int8 [groups, n, k]; weight_scale float32
+    [groups, n]; token_scale and token_scale_stride as for
+    ``moe_deq_swiglu_quant``; out [rows, n] of bf16, fp16 or fp32 gets
+    out[m][j] = (float(sum_i a[m][i] * w[g][j][i]) * weight_scale[g][j]) *
+    token_scale_m (rows of no expert are not written)."""
+    if w.dim() != 3 or w.shape[2] != k or w.dtype not in (torch.int8, torch.uint8):
+        raise ValueError("w must be int8 [groups, n, k]")
+    groups, n = w.shape[0], w.shape[1]
+    if group_count.numel() != groups:
+        raise ValueError("group_count must hold one count per group")
+    if weight_scale.numel() != groups * n:
+        raise ValueError("weight_scale must hold groups * n floats")
+    if a.dtype not in (torch.int8, torch.uint8):
+        raise ValueError("a must be a byte buffer")
+    if rows > 0 and a.numel() < (rows - 1) * a_row_bytes + k:
+        raise ValueError("a is smaller than (rows - 1) * a_row_bytes + k bytes")
+    if not token_scale.is_cuda:
+        raise ValueError("token_scale must be a device tensor")
+    _need_scales(token_scale, rows, token_scale_stride)
+    _check("moe_grouped_gemm_deq_i8", _lib.moe_grouped_gemm_deq_i8(
+        _dev(a, "a"), a_row_bytes, rows, k, _dev(group_count, "group_count", torch.int32), groups, _dev(w, "w"), n,
+        _dev(weight_scale, "weight_scale", torch.float32), token_scale.data_ptr(), token_scale_stride,
+        _dev(out, "out"), dtype_code(out.dtype), out.numel() * out.element_size(), _stream(stream)))
 
 
 def token_scales_of(recv_x: torch.Tensor, hidden: int) -> Tuple[torch.Tensor, int]:

@@ -518,6 +518,161 @@ int moe_grouped_gemm_swiglu_quant_i8(const void* a, int64_t a_row_bytes, int32_t
   return hip_status(moe::launch_grouped_gemm_swiglu_quant(g, static_cast<hipStream_t>(stream)));
 }
 
+namespace {
+
+// Checks shared by the router and its gradient.
+int check_router(moe_dtype type, int64_t stride, int32_t bs, int32_t experts, int32_t topk, moe_score score,
+                 int renorm) {
+  if (bs < 0 || experts < 1 || topk < 1 || topk > experts || stride < experts) return MOE_ERR_BAD_SHAPE;
+  if (experts > MOE_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
+  int st = check_tokens(bs, topk);
+  if (st) return st;
+  if (type != MOE_BF16 && type != MOE_FP16 && type != MOE_FP32) return MOE_ERR_BAD_DTYPE;
+  if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return MOE_ERR_BAD_DTYPE;
+  if (renorm != 0 && renorm != 1) return MOE_ERR_BAD_DTYPE;
+  return MOE_OK;
+}
+
+moe::Out float_type(moe_dtype t) {
+  return t == MOE_FP32 ? moe::Out::kF32 : t == MOE_FP16 ? moe::Out::kFp16 : moe::Out::kBf16;
+}
+size_t float_bytes(moe_dtype t) { return t == MOE_FP32 ? 4 : 2; }
+
+}  // namespace
+
+int moe_route(const void* logits, moe_dtype logits_type, int64_t logits_stride, int32_t bs, int32_t num_experts,
+              int32_t topk, moe_score score, const float* bias, int32_t num_groups, int32_t topk_groups,
+              int32_t group_top, int renormalize, float scale, const uint8_t* token_mask, int32_t* topk_idx,
+              float* topk_weights, void* stream) {
+  int st = check_router(logits_type, logits_stride, bs, num_experts, topk, score, renormalize);
+  if (st) return st;
+  if (num_groups < 1 || topk_groups < 1 || topk_groups > num_groups || num_experts % num_groups != 0 ||
+      (group_top != 1 && group_top != 2) || topk > topk_groups * (num_experts / num_groups))
+    return MOE_ERR_BAD_SHAPE;
+  if (num_groups > MOE_ROUTE_MAX_GROUPS) return MOE_ERR_UNSUPPORTED;
+  if (bs == 0) return MOE_OK;
+  if (!logits || !topk_idx || !topk_weights) return MOE_ERR_NULL_PTR;
+  if (!aligned(logits, float_bytes(logits_type)) || !aligned(bias, 4) || !aligned(topk_idx, 4) ||
+      !aligned(topk_weights, 4))
+    return MOE_ERR_BAD_ALIGN;
+  moe::RouterArgs a{};
+  a.logits = logits;
+  a.stride = logits_stride;
+  a.bs = bs;
+  a.num_experts = num_experts;
+  a.k = topk;
+  a.bias = bias;
+  a.groups = num_groups;
+  a.keep = topk_groups;
+  a.group_top = group_top;
+  a.group_size = num_experts / num_groups;
+  a.group_magic = moe::div_magic(a.group_size);
+  a.renorm = renormalize;
+  a.scale = scale;
+  a.token_mask = token_mask;
+  a.topk_idx = topk_idx;
+  a.topk_weights = topk_weights;
+  return hip_status(moe::launch_route(a, float_type(logits_type), score == MOE_SCORE_SIGMOID,
+                                      static_cast<hipStream_t>(stream)));
+}
+
+int moe_route_backward(const float* grad_weights, const void* logits, moe_dtype logits_type, int64_t logits_stride,
+                       const int32_t* topk_idx, int32_t bs, int32_t num_experts, int32_t topk, moe_score score,
+                       int renormalize, float scale, void* grad_logits, int64_t grad_stride, void* stream) {
+  int st = check_router(logits_type, logits_stride, bs, num_experts, topk, score, renormalize);
+  if (st) return st;
+  if (grad_stride < num_experts) return MOE_ERR_BAD_SHAPE;
+  if (bs == 0) return MOE_OK;
+  if (!grad_weights || !logits || !topk_idx || !grad_logits) return MOE_ERR_NULL_PTR;
+  if (!aligned(logits, float_bytes(logits_type)) || !aligned(grad_logits, float_bytes(logits_type)) ||
+      !aligned(topk_idx, 4) || !aligned(grad_weights, 4))
+    return MOE_ERR_BAD_ALIGN;
+  moe::RouterArgs a{};
+  a.logits = logits;
+  a.stride = logits_stride;
+  a.bs = bs;
+  a.num_experts = num_experts;
+  a.k = topk;
+  a.renorm = renormalize;
+  a.scale = scale;
+  a.topk_idx = const_cast<int32_t*>(topk_idx);  // only read by the gradient
+  a.grad_weights = grad_weights;
+  a.grad_logits = grad_logits;
+  a.grad_stride = grad_stride;
+  return hip_status(moe::launch_route_backward(a, float_type(logits_type), score == MOE_SCORE_SIGMOID,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+int moe_combine_backward(const void* grad_out, moe_dtype grad_out_type, const void* recv_x, moe_dtype recv_type,
+                         size_t recv_x_bytes, int32_t bs, int32_t hidden, int32_t topk, const int32_t* topk_idx,
+                         const float* topk_weights, const int32_t* send_token_idx, const int32_t* put_offset,
+                         const int32_t* recv_base, int32_t epr, int32_t ranks, void* grad_recv,
+                         size_t grad_recv_bytes, float* grad_weights, void* stream) {
+  return moe_combine_backward_src(grad_out, grad_out_type, recv_x, recv_type, recv_x_bytes, bs, hidden, topk,
+                                  topk_idx, topk_weights, send_token_idx, put_offset, recv_base, epr, ranks, 1, 0,
+                                  grad_recv, grad_recv_bytes, grad_weights, stream);
+}
+
+int moe_combine_backward_src(const void* grad_out, moe_dtype grad_out_type, const void* recv_x,
+                             moe_dtype recv_type, size_t recv_x_bytes, int32_t bs, int32_t hidden, int32_t topk,
+                             const int32_t* topk_idx, const float* topk_weights, const int32_t* send_token_idx,
+                             const int32_t* put_offset, const int32_t* recv_base, int32_t epr, int32_t ranks,
+                             int32_t num_src, int32_t src_rank, void* grad_recv, size_t grad_recv_bytes,
+                             float* grad_weights, void* stream) {
+  if (recv_type != MOE_BF16 && recv_type != MOE_FP16) return MOE_ERR_BAD_DTYPE;
+  if (grad_out_type != MOE_BF16 && grad_out_type != MOE_FP16 && grad_out_type != MOE_FP32) return MOE_ERR_BAD_DTYPE;
+  moe::RouteArgs r{};
+  // an entry is in range of both buffers, or skipped
+  const size_t bytes = recv_x_bytes < grad_recv_bytes ? recv_x_bytes : grad_recv_bytes;
+  int st = make_route(bs, hidden, topk, topk_idx, send_token_idx, put_offset, recv_base, epr, ranks, num_src,
+                      src_rank, recv_type, bytes, &r);
+  if (st) return st;
+  if (bs == 0) return MOE_OK;
+  if (!grad_out || !recv_x || !topk_weights || !grad_recv || !grad_weights) return MOE_ERR_NULL_PTR;
+  if (!aligned(grad_out, 16) || !aligned(recv_x, 16) || !aligned(grad_recv, 16) || !aligned(topk_weights, 4) ||
+      !aligned(grad_weights, 4))
+    return MOE_ERR_BAD_ALIGN;
+  return hip_status(moe::launch_combine_backward(r, grad_out, float_type(grad_out_type), recv_x,
+                                                 recv_type == MOE_FP16 ? moe::Half::kFp16 : moe::Half::kBf16,
+                                                 topk_weights, grad_recv, grad_weights,
+                                                 static_cast<hipStream_t>(stream)));
+}
+
+int moe_grouped_gemm_deq_i8(const void* a, int64_t a_row_bytes, int32_t rows, int32_t k,
+                            const int32_t* group_count, int32_t groups, const void* w, int32_t n,
+                            const float* weight_scale, const void* token_scale, int64_t token_scale_stride, void* out,
+                            moe_dtype out_type, size_t out_bytes, void* stream) {
+  if (rows < 0 || k < 1 || n < 1 || groups < 1 || a_row_bytes < k || token_scale_stride < 4 ||
+      token_scale_stride % 4 != 0)
+    return MOE_ERR_BAD_SHAPE;
+  if (k % 16 != 0 || k > MOE_GEMM_MAX_K || n > MOE_GEMM_MAX_N || groups > MOE_GEMM_MAX_GROUPS)
+    return MOE_ERR_UNSUPPORTED;
+  if (out_type != MOE_BF16 && out_type != MOE_FP16 && out_type != MOE_FP32) return MOE_ERR_BAD_DTYPE;
+  if (a_row_bytes % 16 != 0) return MOE_ERR_BAD_ALIGN;
+  if (rows == 0) return MOE_OK;
+  if (!a || !group_count || !w || !weight_scale || !token_scale || !out) return MOE_ERR_NULL_PTR;
+  const size_t es = float_bytes(out_type);
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(group_count, 4) || !aligned(weight_scale, 4) ||
+      !aligned(token_scale, 4) || !aligned(out, es))
+    return MOE_ERR_BAD_ALIGN;
+  if (out_bytes / es / static_cast<size_t>(n) < static_cast<size_t>(rows)) return MOE_ERR_BUFFER_TOO_SMALL;
+  if (moe::grouped_gemm_deq_blocks(rows, groups, n, k) > moe::kGemmMaxBlocks) return MOE_ERR_UNSUPPORTED;
+  moe::GemmDeqArgs g{};
+  g.a = static_cast<const int8_t*>(a);
+  g.a_stride = a_row_bytes;
+  g.rows = rows;
+  g.k = k;
+  g.group_count = group_count;
+  g.groups = groups;
+  g.w = static_cast<const int8_t*>(w);
+  g.n = n;
+  g.weight_scale = weight_scale;
+  g.token_scale = static_cast<const uint8_t*>(token_scale);
+  g.ts_stride = token_scale_stride;
+  g.out = out;
+  return hip_status(moe::launch_grouped_gemm_deq(g, float_type(out_type), static_cast<hipStream_t>(stream)));
+}
+
 const char* moe_status_str(int status) {
   switch (status) {
     case MOE_OK: return "ok";

@@ -85,5 +85,9 @@ constexpr int epilogue_shape_index(int n) {
 constexpr int kGemmStageK = 128;
 constexpr bool gemm_k_tail(int k) { return k % kGemmStageK != 0; }
 
+// ---- router and its gradient: logits per lane of a wave ----------------------
+constexpr int kRouterVpl[] = {1, 2, 4, 8, 16, 32};
+constexpr int router_vpl(int experts) { return first_at_least(kRouterVpl, (experts + kLanes - 1) / kLanes); }
+
 }  // namespace select
 }  // namespace moe

@@ -56,6 +56,12 @@ typedef enum {
   MOE_INT8_ROWSCALE = 3  /* int8 codes + float inverse scale per row (receive buffer) */
 } moe_dtype;
 
+/* How the router turns an expert's logit into its score. */
+typedef enum {
+  MOE_SCORE_SOFTMAX = 0, /* softmax over the token's experts */
+  MOE_SCORE_SIGMOID = 1  /* sigmoid of the logit alone */
+} moe_score;
+
 /* Status codes. */
 enum {
   MOE_OK = 0,
@@ -80,6 +86,7 @@ enum {
 #define MOE_GEMM_MAX_K 65536    /* k of the first expert matmul: sums stay below 2^31 */
 #define MOE_GEMM_MAX_N 65536    /* n of the first expert matmul */
 #define MOE_GEMM_MAX_GROUPS 65536 /* experts of one first-expert-matmul call */
+#define MOE_ROUTE_MAX_GROUPS 64 /* expert groups of the router */
 #define MOE_NO_ALLOC_SCRATCH_BYTES (1u << 20) /* moe_layout_no_alloc's static workspace */
 
 /* Bytes of one receive-buffer row for hidden size `hidden` and receive type
@@ -394,6 +401,138 @@ int moe_grouped_gemm_swiglu_quant_i8(const void* a, int64_t aRowBytes, int32_t r
                                      const float* weightScale, const void* tokenScale,
                                      int64_t tokenScaleStride, void* out, size_t outBytes, void* workspace,
                                      size_t workspaceBytes, void* stream);
+
+/* ---- Router, and the gradients of the routed path ------------------------- */
+
+/* The router: each token's topk experts and their weights from its logits.
+ * No counterpart on the pages (they take topkIdx and topkWeights as given);
+ * its outputs are the topkIdx and topkWeights of moe_layout, moe_dispatch and
+ * moe_combine.
+ *
+ * In:  logits       device [bs][numExperts] of logitsType (MOE_BF16, MOE_FP16
+ *                   or MOE_FP32), row t at element t * logitsStride
+ *                   (logitsStride >= numExperts), aligned to its element.
+ *      bias         device float [numExperts] or NULL: added to the scores
+ *                   for the choice alone, never to the weights.  Finite.
+ *      tokenMask    device bytes [bs] or NULL: a token whose byte is 0 gets
+ *                   no expert; what its logits hold is ignored.
+ * An expert with a logit of -inf or NaN is not eligible; +inf counts as the
+ * largest finite binary32.  Over the eligible experts of a token
+ *   s_e = softmax or sigmoid of the logit x_e
+ *   u_e = s_e + bias_e rounded to a multiple of 2^-30, within [-1024, 1024]
+ *   v_e = u_e with a bias, x_e without one (s grows with x)
+ * and, with numGroups > 1, the experts in groups of numExperts / numGroups
+ * consecutive ids: a group's value is its largest v (groupTop 1) or the sum
+ * of its two largest u (groupTop 2; of the only one, if one is eligible), and
+ * the topkGroups groups of largest value keep their experts.  Among those
+ * the topk experts of largest v are chosen.  Equal values go to the lower id,
+ * for groups and experts.
+ * Out: topkIdx      device int32 [bs][topk]: the chosen experts, v descending;
+ *                   -1 (a bad id: no row is sent) where fewer are eligible.
+ *      topkWeights  device float [bs][topk]: scale * s_e, with renormalize
+ *                   scale * s_e / (sum of the chosen s); 0 at -1.  The ratio
+ *                   is taken of scores scaled by the largest chosen one, so
+ *                   it holds where the scores themselves underflow.
+ * The choice is exact for these definitions up to the error of the binary64
+ * scores (below 2^-44); weights are computed in binary32.
+ *
+ * Requires bs >= 0, numExperts >= 1, 1 <= topkGroups <= numGroups, numGroups
+ * a divisor of numExperts, 1 <= topk <= topkGroups * numExperts / numGroups,
+ * groupTop 1 or 2 (else MOE_ERR_BAD_SHAPE); numExperts <= MOE_MAX_EXPERTS,
+ * topk <= MOE_MAX_TOPK, numGroups <= MOE_ROUTE_MAX_GROUPS, bs * topk < 2^31
+ * (else MOE_ERR_UNSUPPORTED); a known score and renormalize 0 or 1 (else
+ * MOE_ERR_BAD_DTYPE).  bs == 0 enqueues nothing.  One launch, no workspace. */
+int moe_route(const void* logits, moe_dtype logitsType, int64_t logitsStride, int32_t bs,
+              int32_t numExperts, int32_t topk, moe_score score, const float* bias, int32_t numGroups,
+              int32_t topkGroups, int32_t groupTop, int renormalize, float scale,
+              const uint8_t* tokenMask, int32_t* topkIdx, float* topkWeights, void* stream);
+
+/* The router's gradient (no counterpart on the pages): the gradient of the
+ * weights carried back to the logits.  The choice is constant, and the bias
+ * has no gradient.  With S the entries of a token whose id lies in [0,
+ * numExperts), Z the sum of their scores and g = gradWeights:
+ *   ds_j = (scale / Z) (g_j - sum over i in S of g_i s_i / Z)  (renormalize)
+ *        = scale g_j                                           (else)
+ *   softmax: dx_e = s_e ((ds_j if e is entry j's expert, else 0) - sum over i in S of ds_i s_i)
+ *   sigmoid: dx_e = ds_j s_e (1 - s_e) if e is entry j's expert, else 0
+ * over the eligible experts (see moe_route); 0 at the others, so that a
+ * masked token (ids all -1) gets a row of zeros whatever its logits hold.
+ * In:  gradWeights  device float [bs][topk]; logits, topkIdx, score,
+ *                   renormalize, scale as moe_route had and gave them (a
+ *                   token's valid ids are distinct).
+ * Out: gradLogits   device [bs][numExperts] of logitsType, row t at element
+ *                   t * gradStride (gradStride >= numExperts); every element
+ *                   of a row is written, computed in binary32 and rounded
+ *                   once.  Must not overlap logits.
+ * Limits and errors as moe_route.  One launch, no workspace. */
+int moe_route_backward(const float* gradWeights, const void* logits, moe_dtype logitsType,
+                       int64_t logitsStride, const int32_t* topkIdx, int32_t bs, int32_t numExperts,
+                       int32_t topk, moe_score score, int renormalize, float scale, void* gradLogits,
+                       int64_t gradStride, void* stream);
+
+/* The gradient of moe_combine (page section 2.6 defines the sum; the pages
+ * have no backward pass) for 16-bit rows: with g = gradOut[t] and y the
+ * receive row of entry (t, j) as moe_combine finds it
+ *   gradRecv row (same place)  = w_tj * g, rounded half-even to recvType
+ *   gradWeights[t][j]          = sum over i of y[i] * g[i]  (binary32 sums)
+ * and gradWeights[t][j] = 0 for an entry that moe_combine skips.  Rows that
+ * no entry of this call owns are not written.  The dispatch's own gradient
+ * (the sum of a token's k row gradients) is moe_combine of gradRecv with unit
+ * weights.
+ * In:  gradOut      device [bs][hidden] of gradOutType (MOE_BF16, MOE_FP16 or
+ *                   MOE_FP32), 16-byte aligned.
+ *      recvX        the receive buffer that moe_combine read, recvType
+ *                   MOE_BF16 or MOE_FP16; other arguments as moe_combine.
+ * Out: gradRecv     device buffer of gradRecvBytes bytes, rows as recvX's;
+ *                   16-byte aligned.  May be recvX itself (the rows are then
+ *                   replaced by their gradients); must not overlap it otherwise.
+ *      gradWeights  device float [bs][topk].
+ * The sums do not depend on scheduling.  gradRecvBytes below bs * topk rows
+ * gives MOE_ERR_BUFFER_TOO_SMALL; an entry whose row falls outside either
+ * buffer is skipped.  One launch, no workspace. */
+int moe_combine_backward(const void* gradOut, moe_dtype gradOutType, const void* recvX, moe_dtype recvType,
+                         size_t recvXBytes, int32_t bs, int32_t hidden, int32_t topk, const int32_t* topkIdx,
+                         const float* topkWeights, const int32_t* sendTokenIdx, const int32_t* putOffset,
+                         const int32_t* recvBase, int32_t expertNumPerRank, int32_t rankSize, void* gradRecv,
+                         size_t gradRecvBytes, float* gradWeights, void* stream);
+
+/* moe_combine_backward (page section 2.6) for source srcRank of numSrc, with
+ * the rows of moe_combine_src.  Calls for different sources write disjoint
+ * rows and may run concurrently. */
+int moe_combine_backward_src(const void* gradOut, moe_dtype gradOutType, const void* recvX,
+                             moe_dtype recvType, size_t recvXBytes, int32_t bs, int32_t hidden, int32_t topk,
+                             const int32_t* topkIdx, const float* topkWeights, const int32_t* sendTokenIdx,
+                             const int32_t* putOffset, const int32_t* recvBase, int32_t expertNumPerRank,
+                             int32_t rankSize, int32_t numSrc, int32_t srcRank, void* gradRecv,
+                             size_t gradRecvBytes, float* gradWeights, void* stream);
+
+/* Second expert matmul (GMM2) with its dequantisation -- page section 4.3
+ * (Fused Deep MoE: GMM2 on the requantised activations, then the combine):
+ * int8 rows times each expert's int8 weights, scaled by token and by output
+ * channel, in the row type that moe_combine reads.  For every row m owned by
+ * expert g (as moe_grouped_gemm_i8 defines ownership) and column j < n
+ *   acc       = sum over i < k of a[m][i] * w[g][j][i]           (exact, int32)
+ *   out[m][j] = (float(acc) * weightScale[g][j]) * tokenScale_m
+ * each operation rounded to binary32, then half-even to outType.  Bit for bit
+ * that definition.
+ *
+ * a, aRowBytes, rows, k, groupCount, groups, w: as moe_grouped_gemm_i8; the
+ *            int8 rows of moe_deq_swiglu_quant and
+ *            moe_grouped_gemm_swiglu_quant_i8 are used in place.
+ * weightScale [groups][n] float, device, 4-byte aligned.
+ * tokenScale, tokenScaleStride: as moe_deq_swiglu_quant (the rows' inverse
+ *            scales in place, or a dense float array).
+ * out        [rows][n] of outType (MOE_BF16, MOE_FP16 or MOE_FP32), device,
+ *            aligned to its element, outBytes >= rows * n elements.  A 16-bit
+ *            out with n = hidden is the receive buffer that moe_combine reads.
+ *            Rows that no expert owns are not written.
+ * Requires as moe_grouped_gemm_i8, tokenScaleStride a multiple of 4 and >= 4
+ * (else MOE_ERR_BAD_SHAPE); another outType gives MOE_ERR_BAD_DTYPE.  rows ==
+ * 0 enqueues nothing.  One launch, no workspace. */
+int moe_grouped_gemm_deq_i8(const void* a, int64_t aRowBytes, int32_t rows, int32_t k,
+                            const int32_t* groupCount, int32_t groups, const void* w, int32_t n,
+                            const float* weightScale, const void* tokenScale, int64_t tokenScaleStride,
+                            void* out, moe_dtype outType, size_t outBytes, void* stream);
 
 /* Diagnostics.  No counterpart on the pages (their operator calls report
  * failure through the framework's own status; section 6.7 does not show it):
