@@ -6,9 +6,26 @@
 // with the sum exact in int32 (below 2^31 for any order) and each later
 // operation rounded to binary32, so the result does not depend on the tiling.
 //
-// One wave per 16 x 16 tile of one expert's output, straight from global
-// memory: in a step of 64 k bytes lane l holds 16 bytes of row (column) l % 16
-// at k offset 16 (l / 16) for v_mfma_i32_16x16x64_i8.
+// The weights are the first operand of v_mfma_i32_16x16x64_i8 and the rows
+// the second: a lane then holds four consecutive columns of one row, which it
+// scales with one token scale and stores together.
+//
+// Two kernels (see the rule at the launcher):
+//
+// stream_kernel, for experts with few rows, where the weights' bytes are the
+// work: a workgroup takes kMI x 16 rows and 64 columns.  The rows lie in LDS
+// in chunks of kKC bytes of k, two buffers; a wave owns 16 columns and loads
+// their weights straight into registers, a chunk ahead, each byte once.  (A
+// fragment load touches 16 rows of 64 bytes, a quarter of a cache line per 16
+// lanes; with the rows' fragments loaded that way too a decode step took 50
+// us, the line accesses of the L1 being the bound.)
+//
+// tile_kernel, for experts with hundreds of rows, where the matrix cores are
+// the work: 256 x 256 tiles of eight waves in two groups, one wave of each
+// per SIMD, half a step apart; while one multiplies the other reads its
+// fragments.  K is walked in stages of 128 bytes that the LDS-destination
+// loads fill (two slots for the rows, three for the weights, all 160 KB).  The
+// schedule is that of the first expert matmul (gemm.hip).
 #include "device_util.h"
 #include "gemm.h"
 #include "router_util.h"
@@ -20,61 +37,417 @@ namespace moe {
 namespace {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-
-constexpr int kTile = 16, kStepK = 64, kWaves = 4;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#define MOE_LDS __attribute__((address_space(3)))
 
 template <Out kOut>
-__global__ __launch_bounds__(kWave* kWaves) void grouped_gemm_deq_kernel(GemmDeqArgs a) {
-  const int lane = threadIdx.x % kWave, wave = uniform(static_cast<int>(threadIdx.x / kWave));
-  const int64_t col_blocks = (a.n + kTile * kWaves - 1) / (kTile * kWaves);
-  const int64_t slot = blockIdx.x / col_blocks;
-  const int col0 = static_cast<int>(blockIdx.x - slot * col_blocks) * kTile * kWaves + wave * kTile;
-  RowSlot rs;
-  if (!find_row_slot<kTile>(a.group_count, a.groups, a.rows, slot, lane, &rs) || col0 >= a.n) return;
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (kOut == Out::kFp16) return f32_to_f16(round_f32(a)) | (f32_to_f16(round_f32(b)) << 16);
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
 
-  const int piece = lane / 16 * 16;
-  const int8_t* pa = a.a + min(rs.row0 + lane % 16, rs.row_end - 1) * a.a_stride;
-  const int col = col0 + lane % 16;
-  const int8_t* pb = a.w + (static_cast<int64_t>(rs.group) * a.n + min(col, a.n - 1)) * a.k;
-  i32x4 acc = {0, 0, 0, 0};
-  for (int k0 = 0; k0 < a.k; k0 += kStepK) {
-    const bool in = k0 + piece < a.k;  // k ends inside the step: the rest of the row of a counts as zero
-    const int at = in ? k0 + piece : 0;
-    i32x4 fa = *reinterpret_cast<const i32x4*>(pa + at);
-    const i32x4 fb = *reinterpret_cast<const i32x4*>(pb + at);
-    if (!in) fa = i32x4{0, 0, 0, 0};
-    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa, fb, acc, 0, 0, 0);
-  }
-  if (col >= a.n) return;
-  const float ws = a.weight_scale[static_cast<int64_t>(rs.group) * a.n + col];
+// kN (4 or 8) consecutive columns of one row.  kVec: the row's start allows
+// vector stores and the columns all exist.
+template <Out kOut, int kN>
+__device__ __forceinline__ void store_columns(const GemmDeqArgs& a, int64_t row, int col, bool vec,
+                                              const float (&v)[kN]) {
+  const int64_t at = row * a.n + col;
+  if (vec) {
+    if constexpr (kOut == Out::kF32) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int row = rs.row0 + lane / 16 * 4 + r;
+      for (int q = 0; q < kN; q += 4)
+        *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at + q) = f32x4{v[q], v[q + 1], v[q + 2], v[q + 3]};
+    } else if constexpr (kN == 8) {
+      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + at) =
+          u32x4{pack2<kOut>(v[0], v[1]), pack2<kOut>(v[2], v[3]), pack2<kOut>(v[4], v[5]), pack2<kOut>(v[6], v[7])};
+    } else {
+      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at) =
+          u32x2{pack2<kOut>(v[0], v[1]), pack2<kOut>(v[2], v[3])};
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < kN; ++q)
+      if (col + q < a.n) store_float<kOut>(a.out, at + q, round_f32(v[q]));
+  }
+}
+
+// Whether every row's multiple of kN columns allows the vector stores above.
+template <Out kOut, int kN>
+__device__ __forceinline__ bool rows_aligned(const GemmDeqArgs& a) {
+  constexpr int kBytes = kOut == Out::kF32 ? 16 : 2 * kN;
+  return a.n % kN == 0 && reinterpret_cast<uintptr_t>(a.out) % kBytes == 0;
+}
+
+// ---- few rows for each expert -----------------------------------------------------
+
+constexpr int kStreamWaves = 4, kStreamCols = 16 * kStreamWaves;
+
+template <Out kOut, int kMI, int kKC>
+__global__ __launch_bounds__(kWave* kStreamWaves) void stream_kernel(GemmDeqArgs a, int64_t slots) {
+  constexpr int kThreads = kWave * kStreamWaves;
+  constexpr int kRowPieces = kKC / 16;
+  constexpr int kSteps = kKC / 64;
+  constexpr int kCopies = kMI * 16 * kRowPieces / kThreads;  // pieces of a chunk's rows that a thread brings
+  static_assert(kRowPieces % 16 == 0 && kCopies * kThreads == kMI * 16 * kRowPieces, "whole chunks");
+  __shared__ __attribute__((aligned(1024))) uint8_t sa0[kMI * 16 * kKC];
+  __shared__ __attribute__((aligned(1024))) uint8_t sa1[kMI * 16 * kKC];
+  const int tid = threadIdx.x, lane = tid % kWave, wave = uniform(tid / kWave);
+  // workgroups of one block of columns lie on one XCD, an expert's slots next to each other
+  const int64_t x = blockIdx.x % 8, y = blockIdx.x / 8;
+  const int64_t slot = y % slots, block = y / slots * 8 + x;
+  if (block * kStreamCols >= a.n) return;
+  RowSlot rs;
+  if (!find_row_slot<kMI * 16>(a.group_count, a.groups, a.rows, slot, lane, &rs)) return;
+
+  const int col0 = static_cast<int>(block) * kStreamCols + wave * 16;
+  const int piece = lane / 16 * 16;
+  const int8_t* pb =
+      a.w + (static_cast<int64_t>(rs.group) * a.n + min(col0 + lane % 16, a.n - 1)) * a.k;
+  const int8_t* pa[kCopies];
+  int ka[kCopies], la[kCopies];
+#pragma unroll
+  for (int q = 0; q < kCopies; ++q) {
+    const int p = q * kThreads + tid, r = p / kRowPieces, c = p % kRowPieces;
+    pa[q] = a.a + min(rs.row0 + r, rs.row_end - 1) * a.a_stride;
+    ka[q] = c * 16;
+    la[q] = r * kKC + (c ^ (r % 16)) * 16;
+  }
+  const int chunks = (a.k + kKC - 1) / kKC;
+  // Past k the rows count as zero, and whatever weights a valid address gives do no harm.
+  auto load_a = [&](int chunk, i32x4 (&v)[kCopies]) {
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q) {
+      const int at = chunk * kKC + ka[q];
+      v[q] = *reinterpret_cast<const i32x4*>(pa[q] + (at < a.k ? at : 0));
+      if (at >= a.k) v[q] = i32x4{0, 0, 0, 0};
+    }
+  };
+  auto put_a = [&](uint8_t* buf, const i32x4 (&v)[kCopies]) {
+#pragma unroll
+    for (int q = 0; q < kCopies; ++q) *reinterpret_cast<i32x4*>(buf + la[q]) = v[q];
+  };
+  auto load_b = [&](int chunk, i32x4 (&v)[kSteps]) {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int at = chunk * kKC + s * 64 + piece;
+      v[s] = *reinterpret_cast<const i32x4*>(pb + (at < a.k ? at : 0));
+    }
+  };
+  i32x4 acc[kMI];
+#pragma unroll
+  for (int i = 0; i < kMI; ++i) acc[i] = i32x4{0, 0, 0, 0};
+  auto multiply = [&](const uint8_t* buf, const i32x4 (&b)[kSteps]) {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+#pragma unroll
+      for (int i = 0; i < kMI; ++i) {
+        const i32x4 f = *reinterpret_cast<const i32x4*>(buf + (i * 16 + lane % 16) * kKC +
+                                                        ((s * 4 + lane / 16) ^ (lane % 16)) * 16);
+        acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[s], f, acc[i], 0, 0, 0);
+      }
+    }
+  };
+
+  i32x4 va[kCopies], b0[kSteps], b1[kSteps];
+  load_a(0, va);
+  load_b(0, b0);
+  put_a(sa0, va);
+  __syncthreads();
+  // A buffer is written again only after the barrier that follows its readers.
+  for (int c = 0; c < chunks; c += 2) {
+    if (c + 1 < chunks) {
+      load_a(c + 1, va);
+      load_b(c + 1, b1);
+    }
+    multiply(sa0, b0);
+    if (c + 1 >= chunks) break;
+    put_a(sa1, va);
+    __syncthreads();
+    if (c + 2 < chunks) {
+      load_a(c + 2, va);
+      load_b(c + 2, b0);
+    }
+    multiply(sa1, b1);
+    if (c + 2 >= chunks) break;
+    put_a(sa0, va);
+    __syncthreads();
+  }
+
+  const int col = col0 + lane / 16 * 4;
+  if (col >= a.n) return;
+  const bool vec = rows_aligned<kOut, 4>(a);
+  const float* ws = a.weight_scale + static_cast<int64_t>(rs.group) * a.n;
+  float w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) w[q] = ws[min(col + q, a.n - 1)];
+#pragma unroll
+  for (int i = 0; i < kMI; ++i) {
+    const int row = rs.row0 + i * 16 + lane % 16;
     if (row < rs.row_end) {
       const float ts = *reinterpret_cast<const float*>(a.token_scale + row * a.ts_stride);
-      store_float<kOut>(a.out, static_cast<int64_t>(row) * a.n + col, round_f32(static_cast<float>(acc[r]) * ws * ts));
+      float v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = static_cast<float>(acc[i][q]) * w[q] * ts;
+      store_columns<kOut, 4>(a, row, col, vec, v);
     }
   }
+}
+
+// ---- many rows for each expert -----------------------------------------------------
+
+constexpr int kTileM = 256, kTileN = 256, kWavesM = 4, kWavesN = 2;
+constexpr int kTileWaves = kWavesM * kWavesN;
+constexpr int kXcdColGroups = 4, kXcdRows = 8;  // the tile order of gemm.hip
+constexpr int kSK = 128;                        // bytes of k per stage
+
+constexpr int vmcnt_wait(int n) { return 0x0f70 | (n & 15) | ((n >> 4) << 14); }
+constexpr int kLgkmWait0 = 0xc07f;
+
+// Position of a 16-byte piece in a stage row: piece p of row r sits at p ^
+// swizzle(r).  The fragments read 16 rows at one piece, rows 16 i + (0 .. 15)
+// of the rows and 32 p + {0-3, 8-11, 16-19, 24-27} (+ 4) of the weights; for
+// both the 16 rows fall into all 16 groups of banks.
+__device__ __forceinline__ int swizzle(int r) { return ((r >> 1) & 7) ^ (((r >> 4) & 1) << 1); }
+
+template <Out kOut, bool kTail>
+__global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) {
+  constexpr int kWaveM = kTileM / kWavesM, kWaveN = kTileN / kWavesN;
+  constexpr int kMI = kWaveM / 16, kNI = kWaveN / 16;
+  constexpr int kRowsPerLoad = kWave / (kSK / 16);
+  constexpr int kLoadsA = kTileM / kRowsPerLoad / kTileWaves, kLoadsB = kTileN / kRowsPerLoad / kTileWaves;
+  __shared__ __attribute__((aligned(1024))) uint8_t sa0[kTileM * kSK];
+  __shared__ __attribute__((aligned(1024))) uint8_t sa1[kTileM * kSK];
+  __shared__ __attribute__((aligned(1024))) uint8_t sb0[kTileN * kSK];
+  __shared__ __attribute__((aligned(1024))) uint8_t sb1[kTileN * kSK];
+  __shared__ __attribute__((aligned(1024))) uint8_t sb2[kTileN * kSK];
+  const int tid = threadIdx.x, lane = tid % kWave, wave = uniform(tid / kWave);
+
+  const int64_t n_tiles = (a.n + kTileN - 1) / kTileN;
+  int64_t slot, col_tile;
+  if (n_tiles % kXcdColGroups == 0) {
+    const int64_t g = blockIdx.x, x = g % 8, l = g / 8;
+    const int64_t cols = n_tiles / kXcdColGroups, per_block = kXcdRows * cols;
+    const int64_t b = 2 * (l / per_block) + x / kXcdColGroups, w = l % per_block;
+    slot = b * kXcdRows + w / cols;
+    col_tile = (x % kXcdColGroups) * cols + w % cols;
+  } else {
+    slot = blockIdx.x / n_tiles;
+    col_tile = blockIdx.x - slot * n_tiles;
+  }
+  RowSlot rs;
+  if (!find_row_slot<kTileM>(a.group_count, a.groups, a.rows, slot, lane, &rs)) return;  // the whole workgroup
+  const int row0 = rs.row0, row_end = rs.row_end;
+  const int col0 = static_cast<int>(col_tile) * kTileN;
+
+  // Load q of this wave fills the stage rows from 8 (q 8 + wave); lane l
+  // fetches the piece that belongs at position l % 8 of row l / 8, the same
+  // piece for every q.
+  const int piece = (lane % 8) ^ swizzle(kRowsPerLoad * wave + lane / 8);
+  const int8_t* src_a[kLoadsA];
+  const int8_t* src_b[kLoadsB];
+#pragma unroll
+  for (int q = 0; q < kLoadsA; ++q) {
+    const int r = kRowsPerLoad * (q * kTileWaves + wave) + lane / 8;
+    src_a[q] = a.a + min(row0 + r, row_end - 1) * a.a_stride + piece * 16;
+  }
+#pragma unroll
+  for (int q = 0; q < kLoadsB; ++q) {
+    const int r = kRowsPerLoad * (q * kTileWaves + wave) + lane / 8;
+    src_b[q] = a.w + (static_cast<int64_t>(rs.group) * a.n + min(col0 + r, a.n - 1)) * a.k + piece * 16;
+  }
+  const int stages = (a.k + kSK - 1) / kSK;
+  // Stages past the last one load it again, into slots that are not read; a
+  // piece past k reads the row's first piece (its row fragments count as zero).
+  auto stage_offset = [&](int s) {
+    const int k0 = min(s, stages - 1) * kSK;
+    if constexpr (kTail) return (k0 + piece * 16 < a.k) ? k0 : -piece * 16;
+    return k0;
+  };
+  auto issue_a = [&](int s, uint8_t* buf) {
+    const int off = stage_offset(s);
+#pragma unroll
+    for (int q = 0; q < kLoadsA; ++q)
+      __builtin_amdgcn_global_load_lds(src_a[q] + off,
+                                       (MOE_LDS void*)(buf + (q * kTileWaves + wave) * kRowsPerLoad * kSK), 16, 0, 0);
+  };
+  auto issue_b = [&](int s, uint8_t* buf) {
+    const int off = stage_offset(s);
+#pragma unroll
+    for (int q = 0; q < kLoadsB; ++q)
+      __builtin_amdgcn_global_load_lds(src_b[q] + off,
+                                       (MOE_LDS void*)(buf + (q * kTileWaves + wave) * kRowsPerLoad * kSK), 16, 0, 0);
+  };
+
+  const int wm = wave / kWavesN, wn = wave % kWavesN;
+  const int l16 = lane % 16;
+  const int frag_a = (wm * kWaveM + l16) * kSK;
+  // pair p, tile t of the weights: row 32 p + 8 (l16 / 4) + 4 t + l16 % 4, so
+  // that a lane ends with 8 consecutive columns in the two tiles
+  const int row_b = 8 * (l16 / 4) + l16 % 4;
+  const int frag_b = (wn * kWaveN + row_b) * kSK;
+  const int swz_a = swizzle(l16), swz_b = swizzle(row_b);
+  i32x4 acc[kMI][kNI];
+#pragma unroll
+  for (int i = 0; i < kMI; ++i)
+#pragma unroll
+    for (int j = 0; j < kNI; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+
+  auto barrier = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto step = [&](int S, int h, const uint8_t* ca, const uint8_t* cb, uint8_t* fill_a, uint8_t* fill_b) {
+    if (h == 0) issue_a(S + 1, fill_a);  // into the slot A(S - 1) used
+    else issue_b(S + 2, fill_b);         // into the slot B(S - 1) used
+    const int p = 4 * h + lane / 16;
+    i32x4 af[kMI], bf[kNI];
+#pragma unroll
+    for (int i = 0; i < kMI; ++i)
+      af[i] = *reinterpret_cast<const i32x4*>(ca + frag_a + i * 16 * kSK + (p ^ swz_a ^ ((i & 1) << 1)) * 16);
+#pragma unroll
+    for (int j = 0; j < kNI; ++j)
+      bf[j] = *reinterpret_cast<const i32x4*>(cb + frag_b + ((j >> 1) * 32 + (j & 1) * 4) * kSK +
+                                              (p ^ swz_b ^ ((j & 1) << 1)) * 16);
+    if constexpr (kTail) {
+      const int keep = S * kSK + p * 16 < a.k ? -1 : 0;
+#pragma unroll
+      for (int i = 0; i < kMI; ++i) af[i] &= keep;
+    }
+    // this wave's loads of A(S + 1) and B(S + 1); those of B(S + 2) may still run
+    if (h == 1) __builtin_amdgcn_s_waitcnt(vmcnt_wait(kLoadsB));
+    __builtin_amdgcn_s_waitcnt(kLgkmWait0);
+    barrier();
+#pragma unroll
+    for (int i = 0; i < kMI; ++i)
+#pragma unroll
+      for (int j = 0; j < kNI; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[j], af[i], acc[i][j], 0, 0, 0);
+    barrier();
+  };
+  auto stage = [&](int S, const uint8_t* ca, const uint8_t* cb, uint8_t* fill_a, uint8_t* fill_b) {
+    step(S, 0, ca, cb, fill_a, fill_b);
+    step(S, 1, ca, cb, fill_a, fill_b);
+  };
+  issue_b(0, sb0);
+  issue_a(0, sa0);
+  issue_b(1, sb1);
+  __builtin_amdgcn_s_waitcnt(vmcnt_wait(kLoadsB));
+  barrier();
+  const int grp = wave / 4;
+  if (grp == 1) barrier();  // the second group runs half a step behind
+  const int rounds = stages / 6;
+  for (int r = 0; r < rounds; ++r) {
+    stage(6 * r, sa0, sb0, sa1, sb2);
+    stage(6 * r + 1, sa1, sb1, sa0, sb0);
+    stage(6 * r + 2, sa0, sb2, sa1, sb1);
+    stage(6 * r + 3, sa1, sb0, sa0, sb2);
+    stage(6 * r + 4, sa0, sb1, sa1, sb0);
+    stage(6 * r + 5, sa1, sb2, sa0, sb1);
+  }
+  {
+    const int rest = stages - rounds * 6;
+    if (rest > 0) stage(6 * rounds, sa0, sb0, sa1, sb2);
+    if (rest > 1) stage(6 * rounds + 1, sa1, sb1, sa0, sb0);
+    if (rest > 2) stage(6 * rounds + 2, sa0, sb2, sa1, sb1);
+    if (rest > 3) stage(6 * rounds + 3, sa1, sb0, sa0, sb2);
+    if (rest > 4) stage(6 * rounds + 4, sa0, sb1, sa1, sb0);
+  }
+  if (grp == 0) barrier();  // every wave passes the same number of barriers
+  // no load may still be writing this workgroup's LDS when it exits
+  __builtin_amdgcn_s_waitcnt(vmcnt_wait(0));
+
+  const bool vec = rows_aligned<kOut, 8>(a);
+  const float* ws = a.weight_scale + static_cast<int64_t>(rs.group) * a.n;
+  const int col_base = col0 + wn * kWaveN + 8 * (lane / 16);
+  float ts[kMI];
+#pragma unroll
+  for (int i = 0; i < kMI; ++i)
+    ts[i] = *reinterpret_cast<const float*>(a.token_scale +
+                                            min(row0 + wm * kWaveM + i * 16 + l16, row_end - 1) * a.ts_stride);
+#pragma unroll
+  for (int p = 0; p < kNI / 2; ++p) {
+    const int col = col_base + p * 32;
+    if (col >= a.n) continue;
+    float w[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) w[q] = ws[min(col + q, a.n - 1)];
+#pragma unroll
+    for (int i = 0; i < kMI; ++i) {
+      const int row = row0 + wm * kWaveM + i * 16 + l16;
+      if (row >= row_end) continue;
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = static_cast<float>(acc[i][2 * p + q / 4][q % 4]) * w[q] * ts[i];
+      store_columns<kOut, 8>(a, row, col, vec, v);
+    }
+  }
+}
+
+// ---- the rule ------------------------------------------------------------------------
+
+// Rows of the tile that a call's experts take: the rows are spread over at
+// most `groups` experts, so rows / groups is what an expert has on average
+// when all have some.
+int tile_rows(int32_t rows, int32_t groups) {
+  const int64_t mean = (static_cast<int64_t>(rows) + groups - 1) / groups;
+  return mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : mean <= 160 ? 128 : kTileM;
+}
+
+int64_t tile_slots(int32_t rows, int32_t groups, int64_t n_tiles) {
+  int64_t slots = row_slots(rows, groups, kTileM);
+  if (n_tiles % kXcdColGroups == 0) slots = (slots + 2 * kXcdRows - 1) / (2 * kXcdRows) * (2 * kXcdRows);
+  return slots;
+}
+
+template <Out kOut>
+hipError_t launch_out(const GemmDeqArgs& a, hipStream_t stream) {
+  const dim3 grid(static_cast<uint32_t>(grouped_gemm_deq_blocks(a.rows, a.groups, a.n, a.k)));
+  const int tm = tile_rows(a.rows, a.groups);
+  if (tm == kTileM) {
+    if (a.k % kSK != 0) tile_kernel<kOut, true><<<grid, dim3(kWave * kTileWaves), 0, stream>>>(a);
+    else tile_kernel<kOut, false><<<grid, dim3(kWave * kTileWaves), 0, stream>>>(a);
+    return hipGetLastError();
+  }
+  const int64_t slots = row_slots(a.rows, a.groups, tm);
+  const dim3 block(kWave * kStreamWaves);
+  switch (tm) {
+    case 16: stream_kernel<kOut, 1, 512><<<grid, block, 0, stream>>>(a, slots); break;
+    case 32: stream_kernel<kOut, 2, 512><<<grid, block, 0, stream>>>(a, slots); break;
+    case 64: stream_kernel<kOut, 4, 512><<<grid, block, 0, stream>>>(a, slots); break;
+    default: stream_kernel<kOut, 8, 256><<<grid, block, 0, stream>>>(a, slots); break;
+  }
+  return hipGetLastError();
 }
 
 }  // namespace
 
 int64_t grouped_gemm_deq_blocks(int32_t rows, int32_t groups, int32_t n, int32_t k) {
   (void)k;
-  return row_slots(rows, groups, kTile) * ((static_cast<int64_t>(n) + kTile * kWaves - 1) / (kTile * kWaves));
+  const int tm = tile_rows(rows, groups);
+  if (tm == kTileM) {
+    const int64_t n_tiles = (static_cast<int64_t>(n) + kTileN - 1) / kTileN;
+    return tile_slots(rows, groups, n_tiles) * n_tiles;
+  }
+  const int64_t blocks = (static_cast<int64_t>(n) + kStreamCols - 1) / kStreamCols;
+  return row_slots(rows, groups, tm) * ((blocks + 7) / 8 * 8);
 }
 
 hipError_t launch_grouped_gemm_deq(const GemmDeqArgs& a, Out out_type, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
-  const int64_t blocks = grouped_gemm_deq_blocks(a.rows, a.groups, a.n, a.k);
-  if (blocks > kGemmMaxBlocks) return hipErrorInvalidValue;
-  const dim3 grid(static_cast<uint32_t>(blocks)), block(kWave * kWaves);
+  if (grouped_gemm_deq_blocks(a.rows, a.groups, a.n, a.k) > kGemmMaxBlocks) return hipErrorInvalidValue;
   switch (out_type) {
-    case Out::kBf16: grouped_gemm_deq_kernel<Out::kBf16><<<grid, block, 0, stream>>>(a); break;
-    case Out::kFp16: grouped_gemm_deq_kernel<Out::kFp16><<<grid, block, 0, stream>>>(a); break;
-    case Out::kF32: grouped_gemm_deq_kernel<Out::kF32><<<grid, block, 0, stream>>>(a); break;
+    case Out::kBf16: return launch_out<Out::kBf16>(a, stream);
+    case Out::kFp16: return launch_out<Out::kFp16>(a, stream);
+    case Out::kF32: return launch_out<Out::kF32>(a, stream);
   }
-  return hipGetLastError();
+  return hipErrorInvalidValue;
 }
 
 }  // namespace moe
