@@ -65,7 +65,7 @@ struct GemmDeqArgs {
   void* out;                   // [rows][n]
 };
 // Workgroups of one launch.
-int64_t grouped_gemm_deq_blocks(int32_t rows, int32_t groups, int32_t n, int32_t k);
+int64_t grouped_gemm_deq_blocks(int32_t rows, int32_t groups, int32_t n);
 hipError_t launch_grouped_gemm_deq(const GemmDeqArgs& a, Out out_type, hipStream_t stream);
 
 }  // namespace moe

@@ -10,22 +10,36 @@
 // the second: a lane then holds four consecutive columns of one row, which it
 // scales with one token scale and stores together.
 //
-// Two kernels (see the rule at the launcher):
+// Two kernels (select.h has the rule):
 //
 // stream_kernel, for experts with few rows, where the weights' bytes are the
 // work: a workgroup takes kMI x 16 rows and 64 columns.  The rows lie in LDS
 // in chunks of kKC bytes of k, two buffers; a wave owns 16 columns and loads
 // their weights straight into registers, a chunk ahead, each byte once.  (A
-// fragment load touches 16 rows of 64 bytes, a quarter of a cache line per 16
-// lanes; with the rows' fragments loaded that way too a decode step took 50
-// us, the line accesses of the L1 being the bound.)
+// fragment load touches 16 rows at 64 bytes each; with the rows' fragments
+// loaded that way too, a decode step took 50 us instead of 44.)  24 rows over
+// 16 experts, k 2048, n 7168: 44 us = 5.35 TB/s, which is what a large copy
+// reaches on this card.
 //
-// tile_kernel, for experts with hundreds of rows, where the matrix cores are
-// the work: 256 x 256 tiles of eight waves in two groups, one wave of each
-// per SIMD, half a step apart; while one multiplies the other reads its
-// fragments.  K is walked in stages of 128 bytes that the LDS-destination
-// loads fill (two slots for the rows, three for the weights, all 160 KB).  The
-// schedule is that of the first expert matmul (gemm.hip).
+// tile_kernel, for experts with more rows: eight waves in two groups, one wave
+// of each per SIMD, half a step apart; while one multiplies, the other reads
+// its fragments.  K is walked in stages of 128 bytes that the LDS-destination
+// loads fill, whole cache lines (two slots for the rows, three for the
+// weights); the schedule is that of the first expert matmul (gemm.hip), with
+// its reasons.  The tiles of 64 x 128 and 128 x 128 take at most 80 KB of LDS,
+// so two workgroups share a CU and one's start and stores run under the
+// other's products; the tile of 256 x 256 takes all of it and moves half the
+// bytes from L2 per product.  Tiles are dealt to the XCDs by the number that
+// the counts give, not by the launch's bound: an eighth each, in an order in
+// which an XCD's L2 holds the weights of 1024 columns while the rows pass.
+// (Dealt by the bound, XCDs with empty slots idled: 16384 rows over 64
+// experts, k and n 2048, took 132 us instead of 112.)  32768 rows over 16
+// experts, k 2048, n 7168: 498 us = 1.93 POP/s, bound by LDS reads beside the
+// matrix cores (a wave reads 12 KB for 32 products of 8 cycles) at the clock
+// that the chip holds under this load; a large library product reaches 2.09
+// POP/s.  Not faster there: loads left out past the last stage (the accumulators
+// spill where the paths meet), token scales loaded before the loop,
+// non-temporal stores, groups of 512 columns; groups of 2048 are 7 % slower.
 #include "device_util.h"
 #include "gemm.h"
 #include "router_util.h"
@@ -50,22 +64,26 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
 }
 
-// kN (4 or 8) consecutive columns of one row.  kVec: the row's start allows
-// vector stores and the columns all exist.
+// Stores at any element's address: a row of an odd n starts anywhere, and one
+// unaligned store of 16 bytes costs far less than eight stores.
+typedef f32x4 f32x4_u __attribute__((aligned(4)));
+typedef u32x2 u32x2_u __attribute__((aligned(2)));
+typedef u32x4 u32x4_u __attribute__((aligned(2)));
+
+// kN (4 or 8) consecutive columns of one row, as far as the row goes.
 template <Out kOut, int kN>
-__device__ __forceinline__ void store_columns(const GemmDeqArgs& a, int64_t row, int col, bool vec,
-                                              const float (&v)[kN]) {
+__device__ __forceinline__ void store_columns(const GemmDeqArgs& a, int64_t row, int col, const float (&v)[kN]) {
   const int64_t at = row * a.n + col;
-  if (vec) {
+  if (col + kN <= a.n) {
     if constexpr (kOut == Out::kF32) {
 #pragma unroll
       for (int q = 0; q < kN; q += 4)
-        *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at + q) = f32x4{v[q], v[q + 1], v[q + 2], v[q + 3]};
+        *reinterpret_cast<f32x4_u*>(static_cast<float*>(a.out) + at + q) = f32x4{v[q], v[q + 1], v[q + 2], v[q + 3]};
     } else if constexpr (kN == 8) {
-      *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + at) =
+      *reinterpret_cast<u32x4_u*>(static_cast<uint16_t*>(a.out) + at) =
           u32x4{pack2<kOut>(v[0], v[1]), pack2<kOut>(v[2], v[3]), pack2<kOut>(v[4], v[5]), pack2<kOut>(v[6], v[7])};
     } else {
-      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + at) =
+      *reinterpret_cast<u32x2_u*>(static_cast<uint16_t*>(a.out) + at) =
           u32x2{pack2<kOut>(v[0], v[1]), pack2<kOut>(v[2], v[3])};
     }
   } else {
@@ -75,20 +93,11 @@ __device__ __forceinline__ void store_columns(const GemmDeqArgs& a, int64_t row,
   }
 }
 
-// Whether every row's multiple of kN columns allows the vector stores above.
-template <Out kOut, int kN>
-__device__ __forceinline__ bool rows_aligned(const GemmDeqArgs& a) {
-  constexpr int kBytes = kOut == Out::kF32 ? 16 : 2 * kN;
-  return a.n % kN == 0 && reinterpret_cast<uintptr_t>(a.out) % kBytes == 0;
-}
-
 // ---- few rows for each expert -----------------------------------------------------
 
-constexpr int kStreamWaves = 4, kStreamCols = 16 * kStreamWaves;
-
-template <Out kOut, int kMI, int kKC>
-__global__ __launch_bounds__(kWave* kStreamWaves) void stream_kernel(GemmDeqArgs a, int64_t slots) {
-  constexpr int kThreads = kWave * kStreamWaves;
+template <Out kOut, int kMI, int kNI, int kWaves, int kKC>
+__global__ __launch_bounds__(kWave* kWaves) void stream_kernel(GemmDeqArgs a, int64_t slots) {
+  constexpr int kThreads = kWave * kWaves, kCols = 16 * kNI * kWaves;
   constexpr int kRowPieces = kKC / 16;
   constexpr int kSteps = kKC / 64;
   constexpr int kCopies = kMI * 16 * kRowPieces / kThreads;  // pieces of a chunk's rows that a thread brings
@@ -99,14 +108,16 @@ __global__ __launch_bounds__(kWave* kStreamWaves) void stream_kernel(GemmDeqArgs
   // workgroups of one block of columns lie on one XCD, an expert's slots next to each other
   const int64_t x = blockIdx.x % 8, y = blockIdx.x / 8;
   const int64_t slot = y % slots, block = y / slots * 8 + x;
-  if (block * kStreamCols >= a.n) return;
+  if (block * kCols >= a.n) return;
   RowSlot rs;
   if (!find_row_slot<kMI * 16>(a.group_count, a.groups, a.rows, slot, lane, &rs)) return;
 
-  const int col0 = static_cast<int>(block) * kStreamCols + wave * 16;
+  const int col0 = static_cast<int>(block) * kCols + wave * 16 * kNI;
   const int piece = lane / 16 * 16;
-  const int8_t* pb =
-      a.w + (static_cast<int64_t>(rs.group) * a.n + min(col0 + lane % 16, a.n - 1)) * a.k;
+  const int8_t* pb[kNI];
+#pragma unroll
+  for (int j = 0; j < kNI; ++j)
+    pb[j] = a.w + (static_cast<int64_t>(rs.group) * a.n + min(col0 + j * 16 + lane % 16, a.n - 1)) * a.k;
   const int8_t* pa[kCopies];
   int ka[kCopies], la[kCopies];
 #pragma unroll
@@ -130,29 +141,34 @@ __global__ __launch_bounds__(kWave* kStreamWaves) void stream_kernel(GemmDeqArgs
 #pragma unroll
     for (int q = 0; q < kCopies; ++q) *reinterpret_cast<i32x4*>(buf + la[q]) = v[q];
   };
-  auto load_b = [&](int chunk, i32x4 (&v)[kSteps]) {
+  auto load_b = [&](int chunk, i32x4 (&v)[kSteps][kNI]) {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const int at = chunk * kKC + s * 64 + piece;
-      v[s] = *reinterpret_cast<const i32x4*>(pb + (at < a.k ? at : 0));
+#pragma unroll
+      for (int j = 0; j < kNI; ++j) v[s][j] = *reinterpret_cast<const i32x4*>(pb[j] + (at < a.k ? at : 0));
     }
   };
-  i32x4 acc[kMI];
+  i32x4 acc[kMI][kNI];
 #pragma unroll
-  for (int i = 0; i < kMI; ++i) acc[i] = i32x4{0, 0, 0, 0};
-  auto multiply = [&](const uint8_t* buf, const i32x4 (&b)[kSteps]) {
+  for (int i = 0; i < kMI; ++i)
+#pragma unroll
+    for (int j = 0; j < kNI; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  auto multiply = [&](const uint8_t* buf, const i32x4 (&b)[kSteps][kNI]) {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
 #pragma unroll
       for (int i = 0; i < kMI; ++i) {
         const i32x4 f = *reinterpret_cast<const i32x4*>(buf + (i * 16 + lane % 16) * kKC +
                                                         ((s * 4 + lane / 16) ^ (lane % 16)) * 16);
-        acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[s], f, acc[i], 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < kNI; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[s][j], f, acc[i][j], 0, 0, 0);
       }
     }
   };
 
-  i32x4 va[kCopies], b0[kSteps], b1[kSteps];
+  i32x4 va[kCopies], b0[kSteps][kNI], b1[kSteps][kNI];
   load_a(0, va);
   load_b(0, b0);
   put_a(sa0, va);
@@ -177,32 +193,45 @@ __global__ __launch_bounds__(kWave* kStreamWaves) void stream_kernel(GemmDeqArgs
     __syncthreads();
   }
 
-  const int col = col0 + lane / 16 * 4;
-  if (col >= a.n) return;
-  const bool vec = rows_aligned<kOut, 4>(a);
   const float* ws = a.weight_scale + static_cast<int64_t>(rs.group) * a.n;
-  float w[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) w[q] = ws[min(col + q, a.n - 1)];
+  for (int j = 0; j < kNI; ++j) {
+    const int col = col0 + j * 16 + lane / 16 * 4;
+    if (col >= a.n) continue;
+    float w[4];
 #pragma unroll
-  for (int i = 0; i < kMI; ++i) {
-    const int row = rs.row0 + i * 16 + lane % 16;
-    if (row < rs.row_end) {
-      const float ts = *reinterpret_cast<const float*>(a.token_scale + row * a.ts_stride);
-      float v[4];
+    for (int q = 0; q < 4; ++q) w[q] = ws[min(col + q, a.n - 1)];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = static_cast<float>(acc[i][q]) * w[q] * ts;
-      store_columns<kOut, 4>(a, row, col, vec, v);
+    for (int i = 0; i < kMI; ++i) {
+      const int row = rs.row0 + i * 16 + lane % 16;
+      if (row < rs.row_end) {
+        const float ts = *reinterpret_cast<const float*>(a.token_scale + row * a.ts_stride);
+        float v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = static_cast<float>(acc[i][j][q]) * w[q] * ts;
+        store_columns<kOut, 4>(a, row, col, v);
+      }
     }
   }
 }
 
+int64_t stream_blocks(int32_t rows, int32_t groups, int32_t n, int tile_m, int tile_n) {
+  return row_slots(rows, groups, tile_m) * (((static_cast<int64_t>(n) + tile_n - 1) / tile_n + 7) / 8 * 8);
+}
+
+template <Out kOut, int kMI, int kNI, int kWaves, int kKC>
+hipError_t launch_stream(const GemmDeqArgs& a, hipStream_t stream) {
+  const dim3 grid(static_cast<uint32_t>(stream_blocks(a.rows, a.groups, a.n, kMI * 16, 16 * kNI * kWaves)));
+  stream_kernel<kOut, kMI, kNI, kWaves, kKC>
+      <<<grid, dim3(kWave * kWaves), 0, stream>>>(a, row_slots(a.rows, a.groups, kMI * 16));
+  return hipGetLastError();
+}
+
 // ---- many rows for each expert -----------------------------------------------------
 
-constexpr int kTileM = 256, kTileN = 256, kWavesM = 4, kWavesN = 2;
-constexpr int kTileWaves = kWavesM * kWavesN;
-constexpr int kXcdColGroups = 4, kXcdRows = 8;  // the tile order of gemm.hip
-constexpr int kSK = 128;                        // bytes of k per stage
+constexpr int kTileWaves = 8;
+constexpr int kSK = 128;         // bytes of k per stage
+constexpr int kGroupCols = 1024;  // columns of a group of column tiles
 
 constexpr int vmcnt_wait(int n) { return 0x0f70 | (n & 15) | ((n >> 4) << 14); }
 constexpr int kLgkmWait0 = 0xc07f;
@@ -213,8 +242,9 @@ constexpr int kLgkmWait0 = 0xc07f;
 // both the 16 rows fall into all 16 groups of banks.
 __device__ __forceinline__ int swizzle(int r) { return ((r >> 1) & 7) ^ (((r >> 4) & 1) << 1); }
 
-template <Out kOut, bool kTail>
+template <Out kOut, int kTileM, int kTileN, int kWavesM, bool kTail>
 __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) {
+  constexpr int kWavesN = kTileWaves / kWavesM;
   constexpr int kWaveM = kTileM / kWavesM, kWaveN = kTileN / kWavesN;
   constexpr int kMI = kWaveM / 16, kNI = kWaveN / 16;
   constexpr int kRowsPerLoad = kWave / (kSK / 16);
@@ -226,20 +256,23 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) 
   __shared__ __attribute__((aligned(1024))) uint8_t sb2[kTileN * kSK];
   const int tid = threadIdx.x, lane = tid % kWave, wave = uniform(tid / kWave);
 
+  // Tiles in order: groups of column tiles, the row slots of a group, its
+  // columns; XCD x (workgroups x, x + 8, ...) takes the x-th eighth of the
+  // tiles that the counts give.
+  constexpr int kGroup = kGroupCols / kTileN;
   const int64_t n_tiles = (a.n + kTileN - 1) / kTileN;
-  int64_t slot, col_tile;
-  if (n_tiles % kXcdColGroups == 0) {
-    const int64_t g = blockIdx.x, x = g % 8, l = g / 8;
-    const int64_t cols = n_tiles / kXcdColGroups, per_block = kXcdRows * cols;
-    const int64_t b = 2 * (l / per_block) + x / kXcdColGroups, w = l % per_block;
-    slot = b * kXcdRows + w / cols;
-    col_tile = (x % kXcdColGroups) * cols + w % cols;
-  } else {
-    slot = blockIdx.x / n_tiles;
-    col_tile = blockIdx.x - slot * n_tiles;
-  }
+  int64_t col_tile = 0;
+  const auto pick = [&](int64_t slots) -> int64_t {
+    const int64_t tiles = n_tiles * slots, per_xcd = (tiles + 7) / 8;
+    const int64_t l = blockIdx.x / 8, t = blockIdx.x % 8 * per_xcd + l;
+    if (l >= per_xcd || t >= tiles) return -1;
+    const int64_t group = t / (slots * kGroup), within = t - group * slots * kGroup;
+    const int64_t width = min(n_tiles - group * kGroup, static_cast<int64_t>(kGroup));
+    col_tile = group * kGroup + within % width;
+    return within / width;
+  };
   RowSlot rs;
-  if (!find_row_slot<kTileM>(a.group_count, a.groups, a.rows, slot, lane, &rs)) return;  // the whole workgroup
+  if (!place_row_slot<kTileM>(a.group_count, a.groups, a.rows, lane, pick, &rs)) return;  // the whole workgroup
   const int row0 = rs.row0, row_end = rs.row_end;
   const int col0 = static_cast<int>(col_tile) * kTileN;
 
@@ -270,16 +303,20 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) 
   auto issue_a = [&](int s, uint8_t* buf) {
     const int off = stage_offset(s);
 #pragma unroll
-    for (int q = 0; q < kLoadsA; ++q)
-      __builtin_amdgcn_global_load_lds(src_a[q] + off,
-                                       (MOE_LDS void*)(buf + (q * kTileWaves + wave) * kRowsPerLoad * kSK), 16, 0, 0);
+    for (int q = 0; q < kLoadsA; ++q) {
+      const int8_t* src = src_a[q] + off;
+      __builtin_amdgcn_global_load_lds(src, (MOE_LDS void*)(buf + (q * kTileWaves + wave) * kRowsPerLoad * kSK), 16, 0,
+                                       0);
+    }
   };
   auto issue_b = [&](int s, uint8_t* buf) {
     const int off = stage_offset(s);
 #pragma unroll
-    for (int q = 0; q < kLoadsB; ++q)
-      __builtin_amdgcn_global_load_lds(src_b[q] + off,
-                                       (MOE_LDS void*)(buf + (q * kTileWaves + wave) * kRowsPerLoad * kSK), 16, 0, 0);
+    for (int q = 0; q < kLoadsB; ++q) {
+      const int8_t* src = src_b[q] + off;
+      __builtin_amdgcn_global_load_lds(src, (MOE_LDS void*)(buf + (q * kTileWaves + wave) * kRowsPerLoad * kSK), 16, 0,
+                                       0);
+    }
   };
 
   const int wm = wave / kWavesN, wn = wave % kWavesN;
@@ -363,7 +400,6 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) 
   // no load may still be writing this workgroup's LDS when it exits
   __builtin_amdgcn_s_waitcnt(vmcnt_wait(0));
 
-  const bool vec = rows_aligned<kOut, 8>(a);
   const float* ws = a.weight_scale + static_cast<int64_t>(rs.group) * a.n;
   const int col_base = col0 + wn * kWaveN + 8 * (lane / 16);
   float ts[kMI];
@@ -385,63 +421,52 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) 
       float v[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) v[q] = static_cast<float>(acc[i][2 * p + q / 4][q % 4]) * w[q] * ts[i];
-      store_columns<kOut, 8>(a, row, col, vec, v);
+      store_columns<kOut, 8>(a, row, col, v);
     }
   }
 }
 
-// ---- the rule ------------------------------------------------------------------------
-
-// Rows of the tile that a call's experts take: the rows are spread over at
-// most `groups` experts, so rows / groups is what an expert has on average
-// when all have some.
-int tile_rows(int32_t rows, int32_t groups) {
-  const int64_t mean = (static_cast<int64_t>(rows) + groups - 1) / groups;
-  return mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : mean <= 160 ? 128 : kTileM;
+int64_t tile_blocks(int32_t rows, int32_t groups, int32_t n, int tile_m, int tile_n) {
+  return (row_slots(rows, groups, tile_m) * ((static_cast<int64_t>(n) + tile_n - 1) / tile_n) + 7) / 8 * 8;
 }
 
-int64_t tile_slots(int32_t rows, int32_t groups, int64_t n_tiles) {
-  int64_t slots = row_slots(rows, groups, kTileM);
-  if (n_tiles % kXcdColGroups == 0) slots = (slots + 2 * kXcdRows - 1) / (2 * kXcdRows) * (2 * kXcdRows);
-  return slots;
+template <Out kOut, int kTileM, int kTileN, int kWavesM>
+hipError_t launch_tile(const GemmDeqArgs& a, hipStream_t stream) {
+  const dim3 grid(static_cast<uint32_t>(tile_blocks(a.rows, a.groups, a.n, kTileM, kTileN))), block(kWave * kTileWaves);
+  if (a.k % kSK != 0) tile_kernel<kOut, kTileM, kTileN, kWavesM, true><<<grid, block, 0, stream>>>(a);
+  else tile_kernel<kOut, kTileM, kTileN, kWavesM, false><<<grid, block, 0, stream>>>(a);
+  return hipGetLastError();
 }
 
+// One case for each tile of select::gemm_deq_kind.
 template <Out kOut>
 hipError_t launch_out(const GemmDeqArgs& a, hipStream_t stream) {
-  const dim3 grid(static_cast<uint32_t>(grouped_gemm_deq_blocks(a.rows, a.groups, a.n, a.k)));
-  const int tm = tile_rows(a.rows, a.groups);
-  if (tm == kTileM) {
-    if (a.k % kSK != 0) tile_kernel<kOut, true><<<grid, dim3(kWave * kTileWaves), 0, stream>>>(a);
-    else tile_kernel<kOut, false><<<grid, dim3(kWave * kTileWaves), 0, stream>>>(a);
-    return hipGetLastError();
+  switch (select::gemm_deq_kind(a.rows, a.groups, a.n)) {
+    case select::GemmDeqKind::kStream16: return launch_stream<kOut, 1, 1, 4, 512>(a, stream);
+    case select::GemmDeqKind::kStream32: return launch_stream<kOut, 2, 1, 4, 512>(a, stream);
+    case select::GemmDeqKind::kTile64: return launch_tile<kOut, 64, 128, 2>(a, stream);
+    case select::GemmDeqKind::kTile128: return launch_tile<kOut, 128, 128, 2>(a, stream);
+    case select::GemmDeqKind::kTile256: return launch_tile<kOut, 256, 256, 4>(a, stream);
   }
-  const int64_t slots = row_slots(a.rows, a.groups, tm);
-  const dim3 block(kWave * kStreamWaves);
-  switch (tm) {
-    case 16: stream_kernel<kOut, 1, 512><<<grid, block, 0, stream>>>(a, slots); break;
-    case 32: stream_kernel<kOut, 2, 512><<<grid, block, 0, stream>>>(a, slots); break;
-    case 64: stream_kernel<kOut, 4, 512><<<grid, block, 0, stream>>>(a, slots); break;
-    default: stream_kernel<kOut, 8, 256><<<grid, block, 0, stream>>>(a, slots); break;
-  }
-  return hipGetLastError();
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-int64_t grouped_gemm_deq_blocks(int32_t rows, int32_t groups, int32_t n, int32_t k) {
-  (void)k;
-  const int tm = tile_rows(rows, groups);
-  if (tm == kTileM) {
-    const int64_t n_tiles = (static_cast<int64_t>(n) + kTileN - 1) / kTileN;
-    return tile_slots(rows, groups, n_tiles) * n_tiles;
+int64_t grouped_gemm_deq_blocks(int32_t rows, int32_t groups, int32_t n) {
+  switch (select::gemm_deq_kind(rows, groups, n)) {
+    case select::GemmDeqKind::kStream16: return stream_blocks(rows, groups, n, 16, 64);
+    case select::GemmDeqKind::kStream32: return stream_blocks(rows, groups, n, 32, 64);
+    case select::GemmDeqKind::kTile64: return tile_blocks(rows, groups, n, 64, 128);
+    case select::GemmDeqKind::kTile128: return tile_blocks(rows, groups, n, 128, 128);
+    case select::GemmDeqKind::kTile256: return tile_blocks(rows, groups, n, 256, 256);
   }
-  const int64_t blocks = (static_cast<int64_t>(n) + kStreamCols - 1) / kStreamCols;
-  return row_slots(rows, groups, tm) * ((blocks + 7) / 8 * 8);
+  return 0;
 }
 
 hipError_t launch_grouped_gemm_deq(const GemmDeqArgs& a, Out out_type, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
-  if (grouped_gemm_deq_blocks(a.rows, a.groups, a.n, a.k) > kGemmMaxBlocks) return hipErrorInvalidValue;
+  if (grouped_gemm_deq_blocks(a.rows, a.groups, a.n) > kGemmMaxBlocks) return hipErrorInvalidValue;
   switch (out_type) {
     case Out::kBf16: return launch_out<Out::kBf16>(a, stream);
     case Out::kFp16: return launch_out<Out::kFp16>(a, stream);

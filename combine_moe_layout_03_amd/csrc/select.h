@@ -85,9 +85,49 @@ constexpr int epilogue_shape_index(int n) {
 constexpr int kGemmStageK = 128;
 constexpr bool gemm_k_tail(int k) { return k % kGemmStageK != 0; }
 
-// ---- router and its gradient: logits per lane of a wave ----------------------
-constexpr int kRouterVpl[] = {1, 2, 4, 8, 16, 32};
-constexpr int router_vpl(int experts) { return first_at_least(kRouterVpl, (experts + kLanes - 1) / kLanes); }
+// ---- second expert matmul: kernel and tile ----------------------------------
+// The kernel and tile of a call.  The rows an expert has on average (when all
+// have some) decide how many rows a tile takes, measured at k 2048, n 7168, 16
+// experts whose counts fall as rank^-1/2 (us; stream16, stream32, tile64,
+// tile128, tile256):
+//   24 rows: 44, 45, 47, 49, 59      200: 51, 49, 48, 51, 60
+//   400: 69, 55, 51, 54, 64          1000: 129, 88, 66, 61, 72
+//   2500: 289, 175, 101, 83, 79      5000: 554, 319, 162, 129, 107
+// Fewer than about half as many workgroups as there are CUs leave the chip
+// idle, and then the next smaller tile is the faster one (777 rows, k 1040, n
+// 1001, 7 experts: 22 us with tile256, 16, 11, 8.6 with stream32; 1000 rows, k
+// 4096, n 1024, 8 experts: 38, 22, 19 with tile64, 30 with stream32).
+enum class GemmDeqKind { kStream16, kStream32, kTile64, kTile128, kTile256 };
+
+// Workgroups to expect: every other expert ends inside a tile.
+constexpr int64_t gemm_deq_workgroups(int32_t rows, int32_t groups, int32_t n, int tile_m, int tile_n) {
+  return (rows / tile_m + (int64_t(groups) + 1) / 2) * ((int64_t(n) + tile_n - 1) / tile_n);
+}
+constexpr GemmDeqKind gemm_deq_kind(int32_t rows, int32_t groups, int32_t n) {
+  constexpr int64_t kFewWorkgroups = 128;
+  const int64_t mean = (int64_t(rows) + groups - 1) / groups;
+  if (mean <= 4) return GemmDeqKind::kStream16;
+  if (mean <= 16) return GemmDeqKind::kStream32;
+  if (mean > 128 && gemm_deq_workgroups(rows, groups, n, 256, 256) >= kFewWorkgroups) return GemmDeqKind::kTile256;
+  if (mean > 48 && gemm_deq_workgroups(rows, groups, n, 128, 128) >= kFewWorkgroups) return GemmDeqKind::kTile128;
+  return gemm_deq_workgroups(rows, groups, n, 64, 128) >= kFewWorkgroups ? GemmDeqKind::kTile64 : GemmDeqKind::kStream32;
+}
+
+// ---- router and its gradient: (lanes of a token, experts of a lane) -----------
+// 16 lanes a token, four tokens a wave, where a row of 16 holds the experts
+// and the entries and the batch gives every SIMD a wave that way; else a wave.
+struct RouterShape {
+  int lanes, vpl;
+};
+constexpr RouterShape kRouterShapes[] = {{16, 1}, {16, 2}, {16, 4}, {16, 8}, {16, 16}, {64, 1},
+                                         {64, 2}, {64, 4}, {64, 8}, {64, 16}, {64, 32}};
+constexpr int kRouterRowTokens = 4096;  // 1024 SIMDs, four tokens each
+constexpr RouterShape router_shape(int bs, int experts, int topk) {
+  const int lanes = topk <= 16 && experts <= 256 && bs >= kRouterRowTokens ? 16 : 64;
+  for (const RouterShape s : kRouterShapes)
+    if (s.lanes == lanes && s.lanes * s.vpl >= experts) return s;
+  return RouterShape{0, 0};
+}
 
 }  // namespace select
 }  // namespace moe

@@ -8,6 +8,7 @@ import torch
 import combine_moe_layout_03_amd as M
 import router_ref as R
 from gpu_util import align32, int8_row_bytes, log
+from instance_cases_deq import TILED
 
 pytestmark = pytest.mark.gpu
 TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
@@ -187,3 +188,22 @@ def test_gemm_deq_graph_replays():
         assert np.array_equal(got[own >= 0], want[own >= 0]) and (got[own < 0] == -3.0).all()
         M.moe_grouped_gemm_deq_i8(ta.view(-1), k, rows, k, tc, tw, tws, tts, other)
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("tile", TILED)
+@pytest.mark.parametrize("k", [16, 128, 208, 256, 384, 528, 640, 768, 912, 1024, 1152])
+def test_gemm_deq_every_tile(tile, k):
+    """Every tile at every number of stages that its loop's rounds can leave."""
+    rows, n, counts = TILED[tile]
+    kind = ("bf16", "fp16", "fp32")[k // 16 % 3]
+    log(f"gemm_deq {tile} k {k} {kind}")
+    check(np.random.default_rng(k), rows, k, n, counts, kind)
+
+
+@pytest.mark.parametrize("tile", TILED)
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+def test_gemm_deq_every_tile_and_type(tile, kind):
+    rows, n, counts = TILED[tile]
+    log(f"gemm_deq {tile} {kind}")
+    for k in (144, 256):
+        check(np.random.default_rng(k), rows, k, n, counts, kind)
