@@ -43,15 +43,153 @@ __device__ __forceinline__ float router_logit(float v) {
   return (x < FLT_MAX ? x : FLT_MAX) + 0.0f;
 }
 
-__device__ __forceinline__ float wave_sum_f32(float v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d, kWave);
+// ---- a token's lanes ------------------------------------------------------------
+// A token is the work of kL lanes, 16 (a DPP row; four tokens a wave) or 64;
+// lane l holds the kVpl experts from l * kVpl.  All of a wave's lanes stay
+// active: the reductions read their neighbours.
+
+// Exchanges that pair the lanes of a row so that four steps reach all 16:
+// lane ^ 1, lane ^ 2, then the mirrors of 8 and of 16 lanes (after the steps
+// before them every lane of the other half holds the same value).
+constexpr int kDppXor1 = 0xb1, kDppXor2 = 0x4e, kDppMirror8 = 0x141, kDppMirror16 = 0x140;
+
+template <int kCtrl>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xf, 0xf, true));
+}
+template <int kCtrl>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = static_cast<uint32_t>(
+      __builtin_amdgcn_update_dpp(0, static_cast<int>(b & 0xffffffffu), kCtrl, 0xf, 0xf, true));
+  const uint32_t hi =
+      static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), kCtrl, 0xf, 0xf, true));
+  return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+}
+__device__ __forceinline__ float lane_value(float v, int q) { return lane_float(v, q); }
+__device__ __forceinline__ double lane_value(double v, int q) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(b & 0xffffffffu), q));
+  const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(b >> 32), q));
+  return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+}
+
+// op over the token's lanes, in every one of them (the same order for each).
+template <int kL, typename T, typename Op>
+__device__ __forceinline__ T token_reduce(T v, Op op) {
+  static_assert(kL == 16 || kL == 64, "a row or the wave");
+  v = op(v, dpp<kDppXor1>(v));
+  v = op(v, dpp<kDppXor2>(v));
+  v = op(v, dpp<kDppMirror8>(v));
+  v = op(v, dpp<kDppMirror16>(v));
+  if constexpr (kL == 64)
+    v = op(op(lane_value(v, 0), lane_value(v, 16)), op(lane_value(v, 32), lane_value(v, 48)));
   return v;
 }
-__device__ __forceinline__ float wave_max_f32(float v) {
+template <int kL, typename T>
+__device__ __forceinline__ T token_sum(T v) {
+  return token_reduce<kL>(v, [](T a, T b) { return a + b; });
+}
+template <int kL>
+__device__ __forceinline__ float token_max(float v) {
+  return token_reduce<kL>(v, [](float a, float b) { return __builtin_fmaxf(a, b); });
+}
+template <int kL>
+__device__ __forceinline__ double token_max(double v) {
+  return token_reduce<kL>(v, [](double a, double b) { return __builtin_fmax(a, b); });
+}
+
+// Orders this wave's LDS writes before its later LDS reads of other lanes' data.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// One logit, of a type known at run time (the same for the whole launch).
+__device__ __forceinline__ float load_logit(const void* base, Out type, int64_t i) {
+  if (type == Out::kF32) return load_float<Out::kF32>(base, i);
+  return type == Out::kFp16 ? load_float<Out::kFp16>(base, i) : load_float<Out::kBf16>(base, i);
+}
+
+// The logits from element i on, kN of them (of which `have` exist; the others
+// read as -inf), as the router reads them.  Rows start at any element, so the
+// vector loads and stores here are unaligned ones.
+typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(2)));
+
+template <int kN>
+__device__ __forceinline__ void load_logits(const void* base, Out type, int64_t i, int have, float (&x)[kN]) {
+  if (kN % 4 == 0 && have >= kN) {
+    if (type == Out::kF32) {
 #pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) v = __builtin_fmaxf(v, __shfl_xor(v, d, kWave));
-  return v;
+      for (int q = 0; q < kN / 4; ++q) {
+        const f32x4_u v = *reinterpret_cast<const f32x4_u*>(static_cast<const float*>(base) + i + 4 * q);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[4 * q + r] = v[r];
+      }
+    } else {
+      uint32_t w[kN / 2 > 0 ? kN / 2 : 1];
+      const uint16_t* p = static_cast<const uint16_t*>(base) + i;
+      if constexpr (kN % 8 == 0) {
+#pragma unroll
+        for (int q = 0; q < kN / 8; ++q) {
+          const u32x4_u v = *reinterpret_cast<const u32x4_u*>(p + 8 * q);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) w[4 * q + r] = v[r];
+        }
+      } else if constexpr (kN % 4 == 0) {
+        const u32x2_u v = *reinterpret_cast<const u32x2_u*>(p);
+        w[0] = v[0], w[1] = v[1];
+      }
+#pragma unroll
+      for (int q = 0; q < kN; ++q) {
+        const uint32_t b = (q & 1) ? w[q / 2] >> 16 : w[q / 2] & 0xffffu;
+        x[q] = type == Out::kFp16 ? f16_to_f32(b) : bf16_to_f32(b);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kN; ++q) x[q] = router_logit(x[q]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < kN; ++q)
+      x[q] = q < have ? router_logit(load_logit(base, type, i + q)) : -__builtin_inff();
+  }
+}
+
+template <int kN>
+__device__ __forceinline__ void store_logits(void* base, Out type, int64_t i, int have, const float (&x)[kN]) {
+  if (kN % 4 == 0 && have >= kN) {
+    if (type == Out::kF32) {
+#pragma unroll
+      for (int q = 0; q < kN / 4; ++q)
+        *reinterpret_cast<f32x4_u*>(static_cast<float*>(base) + i + 4 * q) =
+            f32x4_u{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+      return;
+    }
+    uint32_t w[kN / 2 > 0 ? kN / 2 : 1];
+#pragma unroll
+    for (int q = 0; q < kN / 2; ++q)
+      w[q] = type == Out::kFp16 ? f32_to_f16(round_f32(x[2 * q])) | (f32_to_f16(round_f32(x[2 * q + 1])) << 16)
+                                : f32_to_bf16(x[2 * q]) | (f32_to_bf16(x[2 * q + 1]) << 16);
+    uint16_t* p = static_cast<uint16_t*>(base) + i;
+    if constexpr (kN % 8 == 0) {
+#pragma unroll
+      for (int q = 0; q < kN / 8; ++q)
+        *reinterpret_cast<u32x4_u*>(p + 8 * q) = u32x4_u{w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]};
+    } else if constexpr (kN % 4 == 0) {
+      *reinterpret_cast<u32x2_u*>(p) = u32x2_u{w[0], w[1]};
+    }
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < kN; ++q) {
+    if (q >= have) continue;
+    if (type == Out::kF32) store_float<Out::kF32>(base, i + q, x[q]);
+    else if (type == Out::kFp16) store_float<Out::kFp16>(base, i + q, round_f32(x[q]));
+    else store_float<Out::kBf16>(base, i + q, x[q]);
+  }
 }
 
 // 1 / (1 + e^-x) without an overflow on either side.

@@ -69,6 +69,28 @@ def test_route_shapes(shape, sigmoid):
                         keep=keep, group_top=top, renorm=renorm, scale=2.5)
 
 
+# Batches that take four tokens a wave: E, k, groups, keep, group_top, bias
+LARGE = [(8, 2, 1, 1, 1, False), (16, 8, 4, 2, 1, True), (16, 16, 1, 1, 1, True), (30, 3, 5, 2, 2, False), (64, 6, 8, 3, 2, True),
+         (100, 7, 4, 2, 2, True), (128, 8, 1, 1, 1, True), (160, 6, 8, 3, 1, False), (256, 8, 8, 4, 2, True),
+         (256, 16, 64, 9, 2, True), (256, 1, 2, 1, 2, False)]
+
+
+@pytest.mark.parametrize("shape", LARGE, ids=lambda s: "-".join(map(str, s)))
+@pytest.mark.parametrize("sigmoid", [False, True], ids=["softmax", "sigmoid"])
+def test_route_large_batches(shape, sigmoid):
+    e, k, groups, keep, top, biased = shape
+    rng = np.random.default_rng(e + k)
+    kind = ("bf16", "fp16", "fp32")[(e + k) % 3]
+    x = R.logits(rng, 4101, e, kind)
+    x[5], x[6, : e // 2], x[4100] = -np.inf, np.nan, 0.0
+    mask = (rng.random(4101) > 0.1).astype(np.uint8)
+    bias = (rng.standard_normal(e) * 0.05).astype(np.float32) if biased else None
+    for renorm in (True, False):
+        log(f"route large {shape} {kind} sigmoid={sigmoid} renorm={renorm}")
+        check_route(x, kind, k, sigmoid, bias, mask, stride=e + 3, groups=groups, keep=keep, group_top=top,
+                    renorm=renorm, scale=1.5)
+
+
 @pytest.mark.parametrize("sigmoid", [False, True], ids=["softmax", "sigmoid"])
 @pytest.mark.parametrize("biased", [False, True])
 def test_route_ties_go_to_the_lower_id(sigmoid, biased):
@@ -181,6 +203,19 @@ def test_route_backward(bs, e, k, sigmoid, renorm):
         idx = np.stack([rng.permutation(e)[:k] for _ in range(bs)]).astype(np.int32)
         log(f"route_backward {bs} {e} {k} {kind} sigmoid={sigmoid} renorm={renorm}")
         check_backward(x, kind, idx, sigmoid, renorm, seed=k)
+
+
+@pytest.mark.parametrize("e,k", [(8, 2), (17, 16), (60, 5), (100, 7), (128, 8), (256, 8)])
+@pytest.mark.parametrize("sigmoid", [False, True], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_backward_large_batches(e, k, sigmoid, renorm):
+    rng = np.random.default_rng(e * k)
+    kind = ("bf16", "fp16", "fp32")[(e + k) % 3]
+    x = R.logits(rng, 4101, e, kind)
+    idx = np.argsort(rng.random((4101, e)), axis=1)[:, :k].astype(np.int32)
+    x[7], idx[7], idx[4100, 1:] = np.nan, -1, -1
+    log(f"route_backward large {e} {k} {kind} sigmoid={sigmoid} renorm={renorm}")
+    check_backward(x, kind, idx, sigmoid, renorm, stride=e + 5)
 
 
 @pytest.mark.parametrize("sigmoid", [False, True], ids=["softmax", "sigmoid"])
