@@ -138,7 +138,8 @@ def dtype_code(dtype: torch.dtype) -> int:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # current_stream().cuda_stream without the Stream object (0.2 instead of 2.9 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)

@@ -17,6 +17,13 @@
 //
 // Scores for the choice are computed in binary64 (exp64 below; the error of a
 // score is below 2^-44, far below the grid), weights in binary32.
+//
+// Bound by the vector ALU: some 1100 instructions for four tokens of 256
+// experts, 450 of them the sigmoids (binary64 runs at the rate of binary32
+// here).  16384 tokens x 256 experts, 8 groups, fp32: 13.6 us, where the bytes
+// alone take 3.4.  A choice in 32 bits, with this one behind it for the waves
+// in which values lie too close, was not faster (18 us: one token in 250 is
+// such, and a launch waits for its slowest wave).
 #include "device_util.h"
 #include "launch.h"
 #include "router_util.h"
@@ -24,11 +31,21 @@
 namespace moe {
 namespace {
 
-constexpr int kWaves = 4;
-constexpr double kNone = -__builtin_inf();  // the key of an expert that cannot be chosen
+// Waves of a workgroup: its tokens' LDS stays within 48 KB.
+constexpr int route_waves(int lanes, int vpl) { return lanes * vpl > 512 ? 2 : 4; }
+// The value and the key of an expert that cannot be chosen: any number below
+// kNone (see unless()).
+constexpr double kNone = -1e30;
 constexpr int kIdBits = 11;
 constexpr double kIdSpan = 1 << kIdBits;
 static_assert(MOE_MAX_EXPERTS <= (1 << kIdBits) && MOE_ROUTE_MAX_GROUPS <= kWave, "ids fit below the value");
+
+// v, or if `none` a number below kNone: one select, of the upper word.
+__device__ __forceinline__ double unless(bool none, double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint64_t hi = none ? uint64_t(0xc7e00000) : b >> 32;  // about -2^127
+  return __builtin_bit_cast(double, (hi << 32) | (b & 0xffffffffu));
+}
 
 __device__ __forceinline__ double make_key(double value, int id) {
   return __builtin_fma(value, kIdSpan, static_cast<double>((1 << kIdBits) - 1 - id));  // exact
@@ -47,33 +64,38 @@ __device__ __forceinline__ double logit_value(float x) {
 }
 
 // e^x for |x| <= 64: x = n ln 2 + r, |r| <= ln(2) / 2, the Taylor polynomial
-// of degree 11 (its remainder is below r^12 / 12! e^r < 2^-46 of the result),
-// times 2^n.
-__device__ __forceinline__ double exp64(double x) {
-  const double n = __builtin_rint(x * 1.4426950408889634);
-  const double r = __builtin_fma(n, -0.6931471805599453, x);
-  double p = 1.0 / 39916800.0;
-  p = __builtin_fma(p, r, 1.0 / 3628800.0);
-  p = __builtin_fma(p, r, 1.0 / 362880.0);
-  p = __builtin_fma(p, r, 1.0 / 40320.0);
-  p = __builtin_fma(p, r, 1.0 / 5040.0);
-  p = __builtin_fma(p, r, 1.0 / 720.0);
-  p = __builtin_fma(p, r, 1.0 / 120.0);
-  p = __builtin_fma(p, r, 1.0 / 24.0);
-  p = __builtin_fma(p, r, 1.0 / 6.0);
-  p = __builtin_fma(p, r, 0.5);
-  p = __builtin_fma(p, r, 1.0);
-  p = __builtin_fma(p, r, 1.0);
-  return __builtin_amdgcn_ldexp(p, static_cast<int>(n));
-}
-// 1 / d for 1 <= d: the hardware's estimate and two Newton steps.
+// of degree 10 (its remainder is below r^11 / 11! e^r < 2^-41 of the result),
+// times 2^n.  The coefficients are kept out of the compiler's sight: for ones
+// that it knows, each v_fmac_f64 gets two moves.
+struct Exp64 {
+  double c[8];
+  __device__ __forceinline__ Exp64() : c{1.0 / 3628800.0, 1.0 / 362880.0, 1.0 / 40320.0, 1.0 / 5040.0,
+                                         1.0 / 720.0, 1.0 / 120.0, 1.0 / 24.0, 1.0 / 6.0} {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm("" : "+v"(c[i]));
+  }
+  __device__ __forceinline__ double operator()(double x) const {
+    const double n = __builtin_rint(x * 1.4426950408889634);
+    const double r = __builtin_fma(n, -0.6931471805599453, x);
+    double p = __builtin_fma(c[0], r, c[1]);
+#pragma unroll
+    for (int i = 2; i < 8; ++i) p = __builtin_fma(p, r, c[i]);
+    p = __builtin_fma(p, r, 0.5);
+    p = __builtin_fma(p, r, 1.0);
+    p = __builtin_fma(p, r, 1.0);
+    return __builtin_amdgcn_ldexp(p, static_cast<int>(n));
+  }
+};
+// 1 / d for 1 <= d: the hardware's estimate (2^-24) and a Newton step.
 __device__ __forceinline__ double reciprocal(double d) {
-  double y = __builtin_amdgcn_rcp(d);
-  y = __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+  const double y = __builtin_amdgcn_rcp(d);
   return __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
 }
 
 // Descending sort of kN (a power of two) keys: Batcher's odd-even merge sort.
+__device__ __forceinline__ double larger(double a, double b) { return __builtin_fmax(a, b); }
+__device__ __forceinline__ double smaller(double a, double b) { return __builtin_fmin(a, b); }
+
 template <int kN>
 __device__ __forceinline__ void sort_keys(double (&v)[kN]) {
 #pragma unroll
@@ -86,8 +108,8 @@ __device__ __forceinline__ void sort_keys(double (&v)[kN]) {
         for (int i = 0; i < q; ++i)
           if (i + j + q < kN && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
             const double a = v[i + j], b = v[i + j + q];
-            v[i + j] = __builtin_fmax(a, b);
-            v[i + j + q] = __builtin_fmin(a, b);
+            v[i + j] = larger(a, b);
+            v[i + j + q] = smaller(a, b);
           }
 }
 
@@ -97,23 +119,214 @@ constexpr bool lane_groups(int group_size, int vpl) {
   return group_size % vpl == 0 && lanes <= 16 && (lanes & (lanes - 1)) == 0;
 }
 
+// The selection values of a lane's experts as whole numbers: `u` the grid
+// values of the scores with their bias.
 template <bool kSigmoid, int kL, int kVpl>
-__global__ __launch_bounds__(kWaves* kWave) void route_kernel(RouterArgs a, Out type) {
+__device__ __forceinline__ void grid_values(const RouterArgs& a, const float (&x)[kVpl], const float (&bias)[kVpl],
+                                            float top, double (&u)[kVpl]) {
+  constexpr double kGrid = 1073741824.0, kClip = 1024.0 * kGrid;
+  const Exp64 exp64;
+  double share = kGrid;
+  if constexpr (kSigmoid) {
+#pragma unroll
+    for (int i = 0; i < kVpl; ++i) {
+      const float c = __builtin_amdgcn_fmed3f(x[i], -64.0f, 64.0f);  // past that s is 0 or 1 on the grid
+      u[i] = reciprocal(1.0 + exp64(-static_cast<double>(c)));
+    }
+  } else {
+    double z = 0.0;
+#pragma unroll
+    for (int i = 0; i < kVpl; ++i) {
+      // (below e^-64 a score is 0 on the grid, and the sum does not feel it)
+      u[i] = exp64(__builtin_fmax(static_cast<double>(x[i]) - static_cast<double>(top), -64.0));
+      z += x[i] > -__builtin_inff() ? u[i] : 0.0;
+    }
+    share = kGrid * reciprocal(__builtin_fmax(token_sum<kL>(z), 1.0));
+  }
+  bool clip = false;
+#pragma unroll
+  for (int i = 0; i < kVpl; ++i) {
+    u[i] = __builtin_rint(__builtin_fma(u[i], share, static_cast<double>(bias[i]) * kGrid));
+    clip |= __builtin_fabsf(bias[i]) > 1000.0f;
+  }
+  if (__any(clip)) {
+#pragma unroll
+    for (int i = 0; i < kVpl; ++i) u[i] = __builtin_fmin(__builtin_fmax(u[i], -kClip), kClip);
+  }
+#pragma unroll
+  for (int i = 0; i < kVpl; ++i) u[i] = unless(!(x[i] > -__builtin_inff()), u[i]);
+}
+
+// The two largest of `v` and of what other lanes of the group pass to merge().
+struct TwoLargest {
+  double first = 2 * kNone, second = 2 * kNone;
+  template <int kN>
+  __device__ __forceinline__ void take(const double (&v)[kN]) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) add(v[i]);
+  }
+  __device__ __forceinline__ void add(double q) {
+    second = __builtin_fmax(second, __builtin_fmin(first, q));
+    first = __builtin_fmax(first, q);
+  }
+  template <int kCtrl>
+  __device__ __forceinline__ void merge() {
+    const double o1 = dpp<kCtrl>(first), o2 = dpp<kCtrl>(second);
+    second = __builtin_fmax(__builtin_fmax(second, o2), __builtin_fmin(first, o1));
+    first = __builtin_fmax(first, o1);
+  }
+  // The group's value; below kNone where it has no eligible expert.
+  __device__ __forceinline__ double value(int group_top) const {
+    return group_top == 2 && second > kNone ? first + second : first;
+  }
+};
+
+// Takes the experts of all groups but the best ones out of `v`.  `rank`: the
+// values the groups are ranked by.  `values`: LDS for the token's experts, used
+// where groups are not whole lanes.
+template <int kL, int kVpl>
+__device__ __forceinline__ void keep_groups(const RouterArgs& a, const double (&rank)[kVpl], int lane, double* values,
+                                            double (&v)[kVpl]) {
+  const int e0 = lane * kVpl;
+  if (lane_groups(a.group_size, kVpl)) {
+    const int lanes_log2 = __builtin_ctz(a.group_size / kVpl);
+    TwoLargest best;
+    best.take(rank);
+    if (lanes_log2 > 0) best.merge<kDppXor1>();
+    if (lanes_log2 > 1) best.merge<kDppXor2>();
+    if (lanes_log2 > 2) best.merge<kDppMirror8>();
+    if (lanes_log2 > 3) best.merge<kDppMirror16>();
+    const int g = lane >> lanes_log2;
+    double key = make_key(best.value(a.group_top), g);
+    bool keep = false;
+    for (int j = 0; j < a.keep; ++j)
+      if (key == token_max<kL>(key)) keep = true, key = 2 * kNone;  // all of the group's lanes
+#pragma unroll
+    for (int i = 0; i < kVpl; ++i) v[i] = unless(!keep, v[i]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kVpl; ++i)
+    if (e0 + i < a.num_experts) values[e0 + i] = rank[i];
+  wave_lds_sync();
+  constexpr int kRounds = MOE_ROUTE_MAX_GROUPS / kL;
+  double key[kRounds];
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int g = r * kL + lane;
+    TwoLargest best;
+    if (g < a.groups)
+      for (int m = 0; m < a.group_size; ++m) best.add(values[g * a.group_size + m]);
+    key[r] = make_key(best.value(a.group_top), g);
+  }
+  uint64_t kept = 0;
+  for (int j = 0; j < a.keep; ++j) {
+    double best = key[0];
+#pragma unroll
+    for (int r = 1; r < kRounds; ++r) best = __builtin_fmax(best, key[r]);
+    best = token_max<kL>(best);
+    if (best > kNone) kept |= uint64_t(1) << key_id(best);
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+      if (key[r] == best) key[r] = 2 * kNone;
+  }
+#pragma unroll
+  for (int i = 0; i < kVpl; ++i) {
+    const int g = static_cast<int>((static_cast<uint64_t>(e0 + i) * a.group_magic) >> 32);
+    v[i] = unless(!((kept >> (g & 63)) & 1), v[i]);
+  }
+}
+
+// Lane j's result is the j-th largest key of the token's lanes (j < k).
+template <int kL, int kVpl>
+__device__ __forceinline__ double largest_keys(double (&v)[kVpl], int k, int lane) {
+  sort_keys<kVpl>(v);
+  double mine = 2 * kNone;
+  if constexpr (kL == 16 && kVpl >= 8) {
+    if (k <= 8) {
+      // The lanes' lists join: of two sorted lists of 8, the larger ones of the
+      // first and the reversed second are the 8 largest, as a bitonic sequence
+      // that three rounds sort; after four exchanges every lane has the
+      // token's 8 largest keys (some 220 instructions; the loop below takes 45
+      // a round).
+      double w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = v[i];
+      const auto join = [&](auto other) {
+        double h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = larger(w[i], other(w[7 - i]));
+#pragma unroll
+        for (int d = 4; d >= 1; d >>= 1)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if ((i & d) == 0) {
+              const double p = h[i], q = h[i + d];
+              h[i] = larger(p, q);
+              h[i + d] = smaller(p, q);
+            }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = h[i];
+      };
+      join([](double q) { return dpp<kDppXor1>(q); });
+      join([](double q) { return dpp<kDppXor2>(q); });
+      join([](double q) { return dpp<kDppMirror8>(q); });
+      join([](double q) { return dpp<kDppMirror16>(q); });
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (lane == i && i < k) mine = w[i];
+      return mine;
+    }
+  }
+  for (int j = 0; j < k; ++j) {
+    const double best = token_max<kL>(v[0]);
+    if (lane == j) mine = best;
+    if (v[0] == best) {
+#pragma unroll
+      for (int i = 0; i + 1 < kVpl; ++i) v[i] = v[i + 1];
+      v[kVpl - 1] = 2 * kNone;
+    }
+  }
+  return mine;
+}
+
+template <bool kSigmoid, int kL, int kVpl>
+__global__ __launch_bounds__(kWave* route_waves(kL, kVpl)) void route_kernel(RouterArgs a, Out type) {
+  constexpr int kWaves = route_waves(kL, kVpl);
   extern __shared__ __attribute__((aligned(16))) double lds[];  // [tokens][E], if groups are not whole lanes
   constexpr int kTokens = kWave / kL;
+  __shared__ __attribute__((aligned(16))) float logits[kWaves * kTokens][kL * kVpl];  // for the chosen ones
   const int lane = threadIdx.x % kL, sub = threadIdx.x / kL;  // lane of the token, token of the workgroup
   const int64_t token = static_cast<int64_t>(blockIdx.x) * (kTokens * kWaves) + sub;
   const bool active = token < a.bs;
   const int64_t t = active ? token : a.bs - 1;  // lanes past the batch work on its last token and store nothing
   const int e0 = lane * kVpl;
+  double* values = lds + sub * a.num_experts;
   const bool masked = a.token_mask != nullptr && a.token_mask[t] == 0;
 
-  float x[kVpl];
+  float x[kVpl], bias[kVpl];
   load_logits<kVpl>(a.logits, type, t * a.stride + e0, a.num_experts - e0, x);
+#pragma unroll
+  for (int i = 0; i < kVpl; ++i) bias[i] = 0.0f;
+  if (a.bias != nullptr) {
+    if (kVpl % 4 == 0 && e0 + kVpl <= a.num_experts) {
+#pragma unroll
+      for (int i = 0; i < kVpl; i += 4) {
+        const f32x4_u b = *reinterpret_cast<const f32x4_u*>(a.bias + e0 + i);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) bias[i + q] = b[q];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVpl; ++i) bias[i] = a.bias[min(e0 + i, a.num_experts - 1)];
+    }
+  }
   if (masked) {
 #pragma unroll
     for (int i = 0; i < kVpl; ++i) x[i] = -__builtin_inff();
   }
+#pragma unroll
+  for (int i = 0; i < kVpl; ++i) logits[sub][e0 + i] = x[i];
 
   // the whole row's softmax statistics, where the scores need them
   const bool scored = a.bias != nullptr || (a.groups > 1 && a.group_top == 2);
@@ -130,128 +343,28 @@ __global__ __launch_bounds__(kWaves* kWave) void route_kernel(RouterArgs a, Out 
   }
 
   double v[kVpl];  // selection values as whole numbers, then keys
+  if (a.bias != nullptr) {
+    grid_values<kSigmoid, kL, kVpl>(a, x, bias, top, v);
+    if (a.groups > 1) keep_groups<kL, kVpl>(a, v, lane, values, v);
+  } else {
 #pragma unroll
-  for (int i = 0; i < kVpl; ++i) v[i] = x[i] > -__builtin_inff() ? logit_value(x[i]) : kNone;
-  double best2 = kNone, best1 = kNone;  // the largest values of this lane's experts, for their group
-  if (scored) {
-    double u[kVpl], z = 0.0;
-#pragma unroll
-    for (int i = 0; i < kVpl; ++i) {
-      const bool ok = x[i] > -__builtin_inff();
-      if constexpr (kSigmoid) {
-        const float c = __builtin_amdgcn_fmed3f(ok ? x[i] : 0.0f, -64.0f, 64.0f);  // past that s is 0 or 1 on the grid
-        u[i] = reciprocal(1.0 + exp64(-static_cast<double>(c)));
-      } else {
-        const double d = ok ? static_cast<double>(x[i]) - static_cast<double>(top) : 0.0;
-        u[i] = ok ? exp64(__builtin_fmax(d, -64.0)) : 0.0;
-        z += u[i];
-      }
-    }
-    const double share = kSigmoid ? 1.0 : reciprocal(__builtin_fmax(token_sum<kL>(z), 1.0));
-#pragma unroll
-    for (int i = 0; i < kVpl; ++i) {
-      double s = kSigmoid ? u[i] : u[i] * share;
-      if (a.bias != nullptr) s += static_cast<double>(a.bias[min(e0 + i, a.num_experts - 1)]);
-      u[i] = v[i] > kNone ? __builtin_rint(__builtin_fmin(__builtin_fmax(s, -1024.0), 1024.0) * 1073741824.0) : kNone;
-      if (a.bias != nullptr) v[i] = u[i];
-      best2 = __builtin_fmax(best2, __builtin_fmin(best1, u[i]));
-      best1 = __builtin_fmax(best1, u[i]);
-    }
-    if (a.groups > 1 && a.group_top == 2 && !lane_groups(a.group_size, kVpl)) {
-#pragma unroll
-      for (int i = 0; i < kVpl; ++i)
-        if (e0 + i < a.num_experts) lds[sub * a.num_experts + e0 + i] = u[i];
+    for (int i = 0; i < kVpl; ++i) v[i] = unless(!(x[i] > -__builtin_inff()), logit_value(x[i]));
+    if (a.groups > 1 && a.group_top == 2) {
+      double u[kVpl];
+      grid_values<kSigmoid, kL, kVpl>(a, x, bias, top, u);
+      keep_groups<kL, kVpl>(a, u, lane, values, v);
+    } else if (a.groups > 1) {
+      keep_groups<kL, kVpl>(a, v, lane, values, v);
     }
   }
-
-  if (a.groups > 1) {
-    if (a.group_top == 1) {
-      best1 = v[0];
+  const double base = static_cast<double>((1 << kIdBits) - 1 - e0);
 #pragma unroll
-      for (int i = 1; i < kVpl; ++i) best1 = __builtin_fmax(best1, v[i]);
-    }
-    uint64_t kept = 0;
-    if (lane_groups(a.group_size, kVpl)) {
-      const int lanes = a.group_size / kVpl;
-      // best1, best2 over the group's lanes: of two lanes' pairs, the two largest
-      const auto merge = [&](double o1, double o2) {
-        best2 = __builtin_fmax(__builtin_fmax(best2, o2), __builtin_fmin(best1, o1));
-        best1 = __builtin_fmax(best1, o1);
-      };
-      if (lanes > 1) merge(dpp<kDppXor1>(best1), dpp<kDppXor1>(best2));
-      if (lanes > 2) merge(dpp<kDppXor2>(best1), dpp<kDppXor2>(best2));
-      if (lanes > 4) merge(dpp<kDppMirror8>(best1), dpp<kDppMirror8>(best2));
-      if (lanes > 8) merge(dpp<kDppMirror16>(best1), dpp<kDppMirror16>(best2));
-      const int g = lane / lanes;
-      if (a.group_top == 2 && best2 > kNone) best1 += best2;
-      double key = g < a.groups && best1 > kNone ? make_key(best1, g) : kNone;
-      bool keep = false;
-      for (int j = 0; j < a.keep; ++j) {
-        const double best = token_max<kL>(key);
-        if (key == best) keep = true, key = kNone;  // all of its lanes (or none is left)
-      }
-#pragma unroll
-      for (int i = 0; i < kVpl; ++i)
-        if (!keep) v[i] = kNone;
-    } else {
-      double* values = lds + sub * a.num_experts;
-      if (a.group_top == 1) {
-#pragma unroll
-        for (int i = 0; i < kVpl; ++i)
-          if (e0 + i < a.num_experts) values[e0 + i] = v[i];
-      }
-      wave_lds_sync();
-      constexpr int kRounds = MOE_ROUTE_MAX_GROUPS / kL;
-      double key[kRounds];
-#pragma unroll
-      for (int r = 0; r < kRounds; ++r) {
-        const int g = r * kL + lane;
-        double first = kNone, second = kNone;
-        if (g < a.groups) {
-          for (int m = 0; m < a.group_size; ++m) {
-            const double q = values[g * a.group_size + m];
-            second = __builtin_fmax(second, __builtin_fmin(first, q));
-            first = __builtin_fmax(first, q);
-          }
-        }
-        if (a.group_top == 2 && second > kNone) first += second;
-        key[r] = first > kNone ? make_key(first, g) : kNone;
-      }
-      for (int j = 0; j < a.keep; ++j) {
-        double best = key[0];
-#pragma unroll
-        for (int r = 1; r < kRounds; ++r) best = __builtin_fmax(best, key[r]);
-        best = token_max<kL>(best);
-        if (best > kNone) kept |= uint64_t(1) << key_id(best);
-#pragma unroll
-        for (int r = 0; r < kRounds; ++r)
-          if (key[r] == best) key[r] = kNone;
-      }
-#pragma unroll
-      for (int i = 0; i < kVpl; ++i) {
-        const int g = static_cast<int>((static_cast<uint64_t>(e0 + i) * a.group_magic) >> 32);
-        if (!((kept >> (g & 63)) & 1)) v[i] = kNone;
-      }
-    }
-  }
-
-#pragma unroll
-  for (int i = 0; i < kVpl; ++i)
-    if (v[i] > kNone) v[i] = make_key(v[i], e0 + i);
-  sort_keys<kVpl>(v);
-  double mine = kNone;  // lane j: the key of entry j
-  for (int j = 0; j < a.k; ++j) {
-    const double best = token_max<kL>(v[0]);
-    if (lane == j) mine = best;
-    if (v[0] == best) {
-#pragma unroll
-      for (int i = 0; i + 1 < kVpl; ++i) v[i] = v[i + 1];
-      v[kVpl - 1] = kNone;
-    }
-  }
+  for (int i = 0; i < kVpl; ++i) v[i] = __builtin_fma(v[i], kIdSpan, base) - static_cast<double>(i);
+  const double mine = largest_keys<kL, kVpl>(v, a.k, lane);
   const int id = mine > kNone ? key_id(mine) : -1;
 
-  const float xm = id >= 0 ? router_logit(load_logit(a.logits, type, t * a.stride + id)) : -__builtin_inff();
+  wave_lds_sync();
+  const float xm = id >= 0 ? logits[sub][id] : -__builtin_inff();
   float w = 0.0f;
   if (a.renorm) {
     const float m = token_max<kL>(xm);
@@ -270,9 +383,8 @@ __global__ __launch_bounds__(kWaves* kWave) void route_kernel(RouterArgs a, Out 
 
 template <bool kSigmoid, int kL, int kVpl>
 hipError_t launch_shape(const RouterArgs& a, Out type, hipStream_t stream) {
-  constexpr int kTokens = kWave / kL * kWaves;
+  constexpr int kWaves = route_waves(kL, kVpl), kTokens = kWave / kL * kWaves;
   const dim3 grid(static_cast<unsigned>((a.bs + kTokens - 1) / kTokens)), block(kWaves * kWave);
-  // at most 16 tokens x 256 experts or 4 x 2048, 64 KB
   const size_t lds = a.groups > 1 && !lane_groups(a.group_size, kVpl) ? sizeof(double) * kTokens * a.num_experts : 0;
   hipLaunchKernelGGL((route_kernel<kSigmoid, kL, kVpl>), grid, block, lds, stream, a, type);
   return hipGetLastError();

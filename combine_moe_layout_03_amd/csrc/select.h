@@ -95,8 +95,10 @@ constexpr bool gemm_k_tail(int k) { return k % kGemmStageK != 0; }
 //   2500: 289, 175, 101, 83, 79      5000: 554, 319, 162, 129, 107
 // Fewer than about half as many workgroups as there are CUs leave the chip
 // idle, and then the next smaller tile is the faster one (777 rows, k 1040, n
-// 1001, 7 experts: 22 us with tile256, 16, 11, 8.6 with stream32; 1000 rows, k
-// 4096, n 1024, 8 experts: 38, 22, 19 with tile64, 30 with stream32).
+// 1001, 7 experts, 128 workgroups of tile64 by the estimate below: 22 us with
+// tile256, 16, 11, 8.6 with stream32; 1000 rows, k 4096, n 1024, 8 experts, 152
+// of tile64: 38, 22, 19 with tile64, 30 with stream32; 8000 such rows, 140 of
+// tile256: 44 with tile256, 53 with tile128).
 enum class GemmDeqKind { kStream16, kStream32, kTile64, kTile128, kTile256 };
 
 // Workgroups to expect: every other expert ends inside a tile.
@@ -104,24 +106,26 @@ constexpr int64_t gemm_deq_workgroups(int32_t rows, int32_t groups, int32_t n, i
   return (rows / tile_m + (int64_t(groups) + 1) / 2) * ((int64_t(n) + tile_n - 1) / tile_n);
 }
 constexpr GemmDeqKind gemm_deq_kind(int32_t rows, int32_t groups, int32_t n) {
-  constexpr int64_t kFewWorkgroups = 128;
+  constexpr int64_t kFewWorkgroups = 128, kFewTile64 = 144;
   const int64_t mean = (int64_t(rows) + groups - 1) / groups;
   if (mean <= 4) return GemmDeqKind::kStream16;
   if (mean <= 16) return GemmDeqKind::kStream32;
   if (mean > 128 && gemm_deq_workgroups(rows, groups, n, 256, 256) >= kFewWorkgroups) return GemmDeqKind::kTile256;
   if (mean > 48 && gemm_deq_workgroups(rows, groups, n, 128, 128) >= kFewWorkgroups) return GemmDeqKind::kTile128;
-  return gemm_deq_workgroups(rows, groups, n, 64, 128) >= kFewWorkgroups ? GemmDeqKind::kTile64 : GemmDeqKind::kStream32;
+  return gemm_deq_workgroups(rows, groups, n, 64, 128) >= kFewTile64 ? GemmDeqKind::kTile64 : GemmDeqKind::kStream32;
 }
 
 // ---- router and its gradient: (lanes of a token, experts of a lane) -----------
 // 16 lanes a token, four tokens a wave, where a row of 16 holds the experts
-// and the entries and the batch gives every SIMD a wave that way; else a wave.
+// and the entries and the batch is large (the choice among 256 experts by
+// either: 1024 tokens 5.1 and, a wave each, 4.7 us; 2048: 5.2, 5.6; 4096: 5.2,
+// 7.8; 16384: 13.6, 23.8); else a wave.
 struct RouterShape {
   int lanes, vpl;
 };
 constexpr RouterShape kRouterShapes[] = {{16, 1}, {16, 2}, {16, 4}, {16, 8}, {16, 16}, {64, 1},
                                          {64, 2}, {64, 4}, {64, 8}, {64, 16}, {64, 32}};
-constexpr int kRouterRowTokens = 4096;  // 1024 SIMDs, four tokens each
+constexpr int kRouterRowTokens = 2048;
 constexpr RouterShape router_shape(int bs, int experts, int topk) {
   const int lanes = topk <= 16 && experts <= 256 && bs >= kRouterRowTokens ? 16 : 64;
   for (const RouterShape s : kRouterShapes)

@@ -53,6 +53,7 @@ SHAPES = [
     (13, 128, 32, 4, 4, 1, True), (6, 512, 8, 8, 4, 2, True), (3, 513, 7, 27, 9, 1, True), (2, 1000, 10, 1, 1, 1, True),
     (2, 2048, 32, 64, 8, 2, True), (3, 2048, 16, 1, 1, 1, False), (4, 64, 8, 64, 8, 1, True), (4, 96, 8, 48, 8, 2, True),
     (257, 16, 2, 1, 1, 1, False), (5, 320, 9, 2, 1, 2, False), (130, 8, 2, 4, 1, 2, True),
+    (2, 2040, 9, 24, 5, 2, True), (3, 900, 5, 12, 4, 1, True),
 ]
 
 
