@@ -88,6 +88,36 @@ def test_combine_backward(bs, h, k, epr, ranks, kind, grad, inplace):
     assert (gw.cpu().numpy()[row < 0] == 0).all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp16"])
+@pytest.mark.parametrize("grad", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("inplace", [False, True], ids=["", "inplace"])
+def test_combine_backward_many_rows(kind, grad, inplace):
+    """More bytes of rows than the caches keep (their stores are another instance), against torch on the device."""
+    bs, h, k, epr, ranks = 460, 16384, 7, 4, 4  # 105 MB of rows
+    rng = np.random.default_rng(17)
+    idx, slot, put, base, row = routes(rng, bs, k, epr, ranks, bad=0.02)
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    g = torch.randn((bs, h), device="cuda", generator=gen).to(TYPES[grad])
+    y = torch.randn((bs * k, h), device="cuda", generator=gen).to(TYPES[kind])
+    w = torch.rand((bs, k), device="cuda", generator=gen)
+    recv = y.clone()
+    out = recv if inplace else torch.full_like(y, FILL)
+    gw = torch.full((bs, k), float("nan"), device="cuda")
+    log(f"combine_backward many rows {kind} grad {grad} inplace={inplace}")
+    M.moe_combine_backward(g, recv, M.dtype_code(TYPES[kind]), i32(idx), w, i32(slot), i32(put), i32(base), epr, ranks,
+                           out, gw)
+    torch.cuda.synchronize()
+    want = y.clone() if inplace else torch.full_like(y, FILL)
+    for j in range(k):
+        ok = torch.from_numpy(row[:, j] >= 0).cuda()
+        at = torch.from_numpy(row[:, j]).cuda()[ok]
+        want[at] = (w[ok, j, None] * g[ok].float()).to(TYPES[kind])
+        prod = y[at].double() * g[ok].double()
+        assert ((gw[ok, j] - prod.sum(1)).abs() <= (8 * -(-h // 512) + 16) * R.U * prod.abs().sum(1)).all()
+        assert (gw[~ok, j] == 0).all()
+    assert torch.equal(out, want)
+
+
 def test_combine_backward_skips_rows_outside_the_buffers():
     """Slots that point past the buffer are skipped, and infinities or NaN in other tokens' rows stay there."""
     rng = np.random.default_rng(5)
