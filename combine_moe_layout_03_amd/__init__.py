@@ -136,10 +136,13 @@ def dtype_code(dtype: torch.dtype) -> int:
         raise ValueError(f"unsupported dtype {dtype}") from None
 
 
+_raw_stream, _raw_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
         # current_stream().cuda_stream without the Stream object (0.2 instead of 2.9 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _raw_stream(_raw_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -150,20 +153,20 @@ def _dev(t: Optional[torch.Tensor], name: str, dtype=None, optional: bool = Fals
         if optional:
             return None
         raise ValueError(f"{name} is required")
+    if isinstance(t, torch.Tensor) and t.is_cuda and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _need(t: Optional[torch.Tensor], name: str, count: int) -> None:
     """Raise unless ``t`` (if given) holds at least ``count`` elements: the
     library takes bare pointers, so an undersized tensor would be written or
     read past its end."""
-    if isinstance(t, torch.Tensor) and t.numel() < count:
+    if t is not None and isinstance(t, torch.Tensor) and t.numel() < count:
         raise ValueError(f"{name} holds {t.numel()} elements, the call needs {count}")
 
 
@@ -493,19 +496,22 @@ def moe_grouped_gemm_swiglu_quant_i8(a: torch.Tensor, a_row_bytes: int, rows: in
         workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
-def _logit_rows(t: torch.Tensor, name: str) -> int:
-    """The row stride, in elements, of [bs, num_experts] logits whose rows are
+def _logit_rows(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
+    """(bs, num_experts, row stride in elements) of logits whose rows are
     dense (the rows themselves may lie apart)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must be [bs, num_experts]")
     bs, e = t.shape
-    if e > 1 and t.stride(1) != 1:
+    if t.is_contiguous():
+        return bs, e, e
+    stride, inner = t.stride()
+    if e > 1 and inner != 1:
         raise ValueError(f"{name} must have dense rows")
-    if bs > 1 and t.stride(0) < e:
+    if bs > 1 and stride < e:
         raise ValueError(f"{name}'s rows overlap")
-    return t.stride(0) if bs > 1 else e
+    return bs, e, stride if bs > 1 else e
 
 
 def moe_route(logits: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor, score: int,
@@ -520,17 +526,18 @@ def moe_route(logits: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.
     with group_top 2) keep their experts; token_mask (uint8 or bool [bs])
     takes a token out where it is 0.  Entries without an eligible expert get
     id -1 and weight 0."""
-    stride = _logit_rows(logits, "logits")
-    bs, e = logits.shape
-    if topk_idx.dim() != 2 or topk_idx.shape[0] != bs:
+    bs, e, stride = _logit_rows(logits, "logits")
+    shape = topk_idx.shape
+    if len(shape) != 2 or shape[0] != bs:
         raise ValueError("topk_idx must be [bs, topk]")
-    topk = topk_idx.shape[1]
-    if topk_weights.shape != topk_idx.shape:
+    topk = shape[1]
+    if topk_weights.shape != shape:
         raise ValueError("topk_weights must be [bs, topk]")
     _need(bias, "bias", e)
-    _need(token_mask, "token_mask", bs)
-    if token_mask is not None and token_mask.dtype not in (torch.uint8, torch.bool):
-        raise ValueError("token_mask must be uint8 or bool")
+    if token_mask is not None:
+        _need(token_mask, "token_mask", bs)
+        if token_mask.dtype is not torch.uint8 and token_mask.dtype is not torch.bool:
+            raise ValueError("token_mask must be uint8 or bool")
     _check("moe_route", _lib.moe_route(
         logits.data_ptr(), dtype_code(logits.dtype), stride, bs, e, topk, score,
         _dev(bias, "bias", torch.float32, optional=True), num_groups, topk_groups, group_top,
@@ -544,25 +551,28 @@ def moe_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, topk_id
     """The router's gradient: grad_weights float32 [bs, topk] -> grad_logits
     [bs, num_experts] of logits' type, every element written.  topk_idx, score,
     renormalize and scale as ``moe_route`` gave and had them."""
-    stride, grad_stride = _logit_rows(logits, "logits"), _logit_rows(grad_logits, "grad_logits")
-    bs, e = logits.shape
-    if grad_logits.shape != logits.shape or grad_logits.dtype != logits.dtype:
+    bs, e, stride = _logit_rows(logits, "logits")
+    grad_bs, grad_e, grad_stride = _logit_rows(grad_logits, "grad_logits")
+    if grad_bs != bs or grad_e != e or grad_logits.dtype is not logits.dtype:
         raise ValueError("grad_logits must have logits' shape and type")
-    if topk_idx.dim() != 2 or topk_idx.shape[0] != bs or grad_weights.shape != topk_idx.shape:
+    shape = topk_idx.shape
+    if len(shape) != 2 or shape[0] != bs or grad_weights.shape != shape:
         raise ValueError("topk_idx and grad_weights must be [bs, topk]")
     _check("moe_route_backward", _lib.moe_route_backward(
         _dev(grad_weights, "grad_weights", torch.float32), logits.data_ptr(), dtype_code(logits.dtype), stride,
-        _dev(topk_idx, "topk_idx", torch.int32), bs, e, topk_idx.shape[1], score, 1 if renormalize else 0, scale,
+        _dev(topk_idx, "topk_idx", torch.int32), bs, e, shape[1], score, 1 if renormalize else 0, scale,
         grad_logits.data_ptr(), grad_stride, _stream(stream)))
 
 
 def _combine_backward_sizes(grad_out, topk_idx, topk_weights, send_token_idx, grad_weights):
-    if grad_out.dim() != 2 or topk_idx.dim() != 2 or grad_out.shape[0] != topk_idx.shape[0]:
+    shape, entries = grad_out.shape, topk_idx.shape
+    if len(shape) != 2 or len(entries) != 2 or shape[0] != entries[0]:
         raise ValueError("grad_out must be [bs, hidden] and topk_idx [bs, topk]")
-    (bs, hidden), topk = grad_out.shape, topk_idx.shape[1]
-    for t, name in ((topk_weights, "topk_weights"), (send_token_idx, "send_token_idx"), (grad_weights, "grad_weights")):
-        _need(t, name, bs * topk)
-    return bs, hidden, topk
+    count = entries[0] * entries[1]
+    _need(topk_weights, "topk_weights", count)
+    _need(send_token_idx, "send_token_idx", count)
+    _need(grad_weights, "grad_weights", count)
+    return shape[0], shape[1], entries[1]
 
 
 def moe_combine_backward(grad_out: torch.Tensor, recv_x: torch.Tensor, recv_type: int, topk_idx: torch.Tensor,
@@ -612,9 +622,10 @@ def moe_grouped_gemm_deq_i8(a: torch.Tensor, a_row_bytes: int, rows: int, k: int
     ``moe_deq_swiglu_quant``; out [rows, n] of bf16, fp16 or fp32 gets
     out[m][j] = (float(sum_i a[m][i] * w[g][j][i]) * weight_scale[g][j]) *
     token_scale_m (rows of no expert are not written)."""
-    if w.dim() != 3 or w.shape[2] != k or w.dtype not in (torch.int8, torch.uint8):
+    shape = w.shape
+    if len(shape) != 3 or shape[2] != k or w.dtype not in (torch.int8, torch.uint8):
         raise ValueError("w must be int8 [groups, n, k]")
-    groups, n = w.shape[0], w.shape[1]
+    groups, n, _ = shape
     if group_count.numel() != groups:
         raise ValueError("group_count must hold one count per group")
     if weight_scale.numel() != groups * n:

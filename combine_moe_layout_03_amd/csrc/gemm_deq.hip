@@ -15,7 +15,7 @@
 // stream_kernel, for experts with few rows, where the weights' bytes are the
 // work: a workgroup takes kMI x 16 rows and 64 columns.  The rows lie in LDS
 // in chunks of kKC bytes of k, two buffers; a wave owns 16 columns and loads
-// their weights straight into registers, a chunk ahead, each byte once.  (A
+// their weights straight into registers, two chunks ahead, each byte once.  (A
 // fragment load touches 16 rows at 64 bytes each; with the rows' fragments
 // loaded that way too, a decode step took 50 us instead of 44.)  24 rows over
 // 16 experts, k 2048, n 7168: 44 us = 5.35 TB/s, which is what a large copy
@@ -127,6 +127,15 @@ __global__ __launch_bounds__(kWave* kWaves) void stream_kernel(GemmDeqArgs a, in
     ka[q] = c * 16;
     la[q] = r * kKC + (c ^ (r % 16)) * 16;
   }
+  float w[kNI][4], ts[kMI];
+  const float* ws = a.weight_scale + static_cast<int64_t>(rs.group) * a.n;
+#pragma unroll
+  for (int j = 0; j < kNI; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) w[j][q] = ws[min(col0 + j * 16 + lane / 16 * 4 + q, a.n - 1)];
+#pragma unroll
+  for (int i = 0; i < kMI; ++i)
+    ts[i] = *reinterpret_cast<const float*>(a.token_scale + min(rs.row0 + i * 16 + lane % 16, rs.row_end - 1) * a.ts_stride);
   const int chunks = (a.k + kKC - 1) / kKC;
   // Past k the rows count as zero, and whatever weights a valid address gives do no harm.
   auto load_a = [&](int chunk, i32x4 (&v)[kCopies]) {
@@ -168,47 +177,46 @@ __global__ __launch_bounds__(kWave* kWaves) void stream_kernel(GemmDeqArgs a, in
     }
   };
 
-  i32x4 va[kCopies], b0[kSteps][kNI], b1[kSteps][kNI];
-  load_a(0, va);
+  i32x4 va0[kCopies], va1[kCopies], b0[kSteps][kNI], b1[kSteps][kNI];
+  load_a(0, va0);
   load_b(0, b0);
-  put_a(sa0, va);
+  if (chunks > 1) {
+    load_a(1, va1);
+    load_b(1, b1);
+  }
+  put_a(sa0, va0);
   __syncthreads();
   // A buffer is written again only after the barrier that follows its readers.
-  for (int c = 0; c < chunks; c += 2) {
-    if (c + 1 < chunks) {
-      load_a(c + 1, va);
-      load_b(c + 1, b1);
-    }
+  for (int c = 0;; c += 2) {
     multiply(sa0, b0);
     if (c + 1 >= chunks) break;
-    put_a(sa1, va);
-    __syncthreads();
     if (c + 2 < chunks) {
-      load_a(c + 2, va);
+      load_a(c + 2, va0);
       load_b(c + 2, b0);
     }
+    put_a(sa1, va1);
+    __syncthreads();
     multiply(sa1, b1);
     if (c + 2 >= chunks) break;
-    put_a(sa0, va);
+    if (c + 3 < chunks) {
+      load_a(c + 3, va1);
+      load_b(c + 3, b1);
+    }
+    put_a(sa0, va0);
     __syncthreads();
   }
 
-  const float* ws = a.weight_scale + static_cast<int64_t>(rs.group) * a.n;
 #pragma unroll
   for (int j = 0; j < kNI; ++j) {
     const int col = col0 + j * 16 + lane / 16 * 4;
     if (col >= a.n) continue;
-    float w[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) w[q] = ws[min(col + q, a.n - 1)];
 #pragma unroll
     for (int i = 0; i < kMI; ++i) {
       const int row = rs.row0 + i * 16 + lane % 16;
       if (row < rs.row_end) {
-        const float ts = *reinterpret_cast<const float*>(a.token_scale + row * a.ts_stride);
         float v[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = static_cast<float>(acc[i][j][q]) * w[q] * ts;
+        for (int q = 0; q < 4; ++q) v[q] = static_cast<float>(acc[i][j][q]) * w[j][q] * ts[i];
         store_columns<kOut, 4>(a, row, col, v);
       }
     }
@@ -292,6 +300,24 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) 
     const int r = kRowsPerLoad * (q * kTileWaves + wave) + lane / 8;
     src_b[q] = a.w + (static_cast<int64_t>(rs.group) * a.n + min(col0 + r, a.n - 1)) * a.k + piece * 16;
   }
+  // The scales before the loop where the registers allow it (2 % at 1000 rows).
+  const int wm = wave / kWavesN, wn = wave % kWavesN;
+  const int l16 = lane % 16;
+  const int col_base = col0 + wn * kWaveN + 8 * (lane / 16);
+  constexpr bool kEarlyScales = kMI * kNI <= 16;
+  float ts[kMI], w[kNI / 2][8];
+  const auto load_scales = [&]() {
+    const float* ws = a.weight_scale + static_cast<int64_t>(rs.group) * a.n;
+#pragma unroll
+    for (int i = 0; i < kMI; ++i)
+      ts[i] = *reinterpret_cast<const float*>(a.token_scale +
+                                              min(row0 + wm * kWaveM + i * 16 + l16, row_end - 1) * a.ts_stride);
+#pragma unroll
+    for (int p = 0; p < kNI / 2; ++p)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) w[p][q] = ws[min(col_base + p * 32 + q, a.n - 1)];
+  };
+  if constexpr (kEarlyScales) load_scales();
   const int stages = (a.k + kSK - 1) / kSK;
   // Stages past the last one load it again, into slots that are not read; a
   // piece past k reads the row's first piece (its row fragments count as zero).
@@ -319,8 +345,6 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) 
     }
   };
 
-  const int wm = wave / kWavesN, wn = wave % kWavesN;
-  const int l16 = lane % 16;
   const int frag_a = (wm * kWaveM + l16) * kSK;
   // pair p, tile t of the weights: row 32 p + 8 (l16 / 4) + 4 t + l16 % 4, so
   // that a lane ends with 8 consecutive columns in the two tiles
@@ -400,27 +424,18 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) 
   // no load may still be writing this workgroup's LDS when it exits
   __builtin_amdgcn_s_waitcnt(vmcnt_wait(0));
 
-  const float* ws = a.weight_scale + static_cast<int64_t>(rs.group) * a.n;
-  const int col_base = col0 + wn * kWaveN + 8 * (lane / 16);
-  float ts[kMI];
-#pragma unroll
-  for (int i = 0; i < kMI; ++i)
-    ts[i] = *reinterpret_cast<const float*>(a.token_scale +
-                                            min(row0 + wm * kWaveM + i * 16 + l16, row_end - 1) * a.ts_stride);
+  if constexpr (!kEarlyScales) load_scales();
 #pragma unroll
   for (int p = 0; p < kNI / 2; ++p) {
     const int col = col_base + p * 32;
     if (col >= a.n) continue;
-    float w[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) w[q] = ws[min(col + q, a.n - 1)];
 #pragma unroll
     for (int i = 0; i < kMI; ++i) {
       const int row = row0 + wm * kWaveM + i * 16 + l16;
       if (row >= row_end) continue;
       float v[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = static_cast<float>(acc[i][2 * p + q / 4][q % 4]) * w[q] * ts[i];
+      for (int q = 0; q < 8; ++q) v[q] = static_cast<float>(acc[i][2 * p + q / 4][q % 4]) * w[p][q] * ts[i];
       store_columns<kOut, 8>(a, row, col, v);
     }
   }
@@ -443,7 +458,9 @@ template <Out kOut>
 hipError_t launch_out(const GemmDeqArgs& a, hipStream_t stream) {
   switch (select::gemm_deq_kind(a.rows, a.groups, a.n)) {
     case select::GemmDeqKind::kStream16: return launch_stream<kOut, 1, 1, 4, 512>(a, stream);
-    case select::GemmDeqKind::kStream32: return launch_stream<kOut, 2, 1, 4, 512>(a, stream);
+    case select::GemmDeqKind::kStream32:
+      return select::gemm_deq_short_chunks(a.k) ? launch_stream<kOut, 2, 1, 4, 256>(a, stream)
+                                                : launch_stream<kOut, 2, 1, 4, 512>(a, stream);
     case select::GemmDeqKind::kTile64: return launch_tile<kOut, 64, 128, 2>(a, stream);
     case select::GemmDeqKind::kTile128: return launch_tile<kOut, 128, 128, 2>(a, stream);
     case select::GemmDeqKind::kTile256: return launch_tile<kOut, 256, 256, 4>(a, stream);

@@ -115,6 +115,10 @@ constexpr GemmDeqKind gemm_deq_kind(int32_t rows, int32_t groups, int32_t n) {
   return gemm_deq_workgroups(rows, groups, n, 64, 128) >= kFewTile64 ? GemmDeqKind::kTile64 : GemmDeqKind::kStream32;
 }
 
+// stream32's chunks of k: 256 bytes end nearer to a short k, 512 have half the
+// barriers (k 1040: 7.5 and, with 512, 8.4 us; 2048: 48.1, 49.3; 7168: 44.3, 38.3).
+constexpr bool gemm_deq_short_chunks(int32_t k) { return k <= 2048; }
+
 // ---- combine's gradient: how the row gradients are stored --------------------
 // Non-temporally where the rows are more than the caches keep (h 7168, 8
 // entries, bf16, non-temporal and not: 512 tokens, 59 MB of rows: 25.3 and

@@ -51,8 +51,9 @@ def test_compiled_instances():
     if not kernel_remarks.hipcc_available():
         pytest.skip("hipcc not available")
     names = kernel_remarks.demangle(kernel_remarks.kernel_remarks()).values()
-    stream = {m.group(1, 2) for m in (re.search(r"::stream_kernel<\(moe::Out\)(\d), (\d+),", s) for s in names) if m}
+    stream = {m.group(1, 2, 3) for m in
+              (re.search(r"::stream_kernel<\(moe::Out\)(\d), (\d+), \d+, \d+, (\d+)>", s) for s in names) if m}
     tile = {m.group(1, 2, 3) for m in
             (re.search(r"::tile_kernel<\(moe::Out\)(\d), (\d+), \d+, \d+, (\w+)>", s) for s in names) if m}
-    assert stream == {(o, r) for o in "012" for r in "12"}
+    assert stream == {(o, *r) for o in "012" for r in (("1", "512"), ("2", "256"), ("2", "512"))}
     assert tile == {(o, r, t) for o in "012" for r in ("64", "128", "256") for t in ("true", "false")}

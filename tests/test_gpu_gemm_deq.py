@@ -191,7 +191,7 @@ def test_gemm_deq_graph_replays():
 
 
 @pytest.mark.parametrize("tile", TILED)
-@pytest.mark.parametrize("k", [16, 128, 208, 256, 384, 528, 640, 768, 912, 1024, 1152])
+@pytest.mark.parametrize("k", [16, 128, 208, 256, 384, 528, 640, 768, 912, 1024, 1152, 2064, 2560, 3600])
 def test_gemm_deq_every_tile(tile, k):
     """Every tile at every number of stages that its loop's rounds can leave."""
     rows, n, counts = TILED[tile]
@@ -205,5 +205,5 @@ def test_gemm_deq_every_tile(tile, k):
 def test_gemm_deq_every_tile_and_type(tile, kind):
     rows, n, counts = TILED[tile]
     log(f"gemm_deq {tile} {kind}")
-    for k in (144, 256):
+    for k in (144, 256, 2208):
         check(np.random.default_rng(k), rows, k, n, counts, kind)
