@@ -50,11 +50,11 @@ __device__ __forceinline__ double unless(bool none, double v) {
 __device__ __forceinline__ double make_key(double value, int id) {
   return __builtin_fma(value, kIdSpan, static_cast<double>((1 << kIdBits) - 1 - id));  // exact
 }
-// The id below a key: what is left of the key past whole multiples of 2^11
-// (every step exact, also for the sum of two values at their bound).
+// The whole number above a key's id, and the id below it (every step exact,
+// also for the sum of two values at their bound).
+__device__ __forceinline__ double key_value(double key) { return __builtin_floor(key * (1.0 / kIdSpan)); }
 __device__ __forceinline__ int key_id(double key) {
-  const double below = __builtin_fma(__builtin_floor(key * (1.0 / kIdSpan)), -kIdSpan, key);
-  return (1 << kIdBits) - 1 - static_cast<int>(below);
+  return (1 << kIdBits) - 1 - static_cast<int>(__builtin_fma(key_value(key), -kIdSpan, key));
 }
 
 // Whole number of the same order as the (finite) logit.
@@ -92,12 +92,13 @@ __device__ __forceinline__ double reciprocal(double d) {
   return __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
 }
 
-// Descending sort of kN (a power of two) keys: Batcher's odd-even merge sort.
 __device__ __forceinline__ double larger(double a, double b) { return __builtin_fmax(a, b); }
 __device__ __forceinline__ double smaller(double a, double b) { return __builtin_fmin(a, b); }
 
-template <int kN>
-__device__ __forceinline__ void sort_keys(double (&v)[kN]) {
+// Descending sort of kN (a power of two) keys from v[kAt]: Batcher's odd-even
+// merge sort.
+template <int kN, int kAt, int kAll>
+__device__ __forceinline__ void sort_keys(double (&v)[kAll]) {
 #pragma unroll
   for (int p = 1; p < kN; p <<= 1)
 #pragma unroll
@@ -107,10 +108,54 @@ __device__ __forceinline__ void sort_keys(double (&v)[kN]) {
 #pragma unroll
         for (int i = 0; i < q; ++i)
           if (i + j + q < kN && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
-            const double a = v[i + j], b = v[i + j + q];
-            v[i + j] = larger(a, b);
-            v[i + j + q] = smaller(a, b);
+            const double a = v[kAt + i + j], b = v[kAt + i + j + q];
+            v[kAt + i + j] = larger(a, b);
+            v[kAt + i + j + q] = smaller(a, b);
           }
+}
+
+// w, sorted descending, becomes the 8 largest keys of itself and `other`, also
+// sorted: the larger ones of the first list and the reversed second are those,
+// as a bitonic sequence that three rounds sort.
+template <int kAll, typename Other>
+__device__ __forceinline__ void join8(double (&w)[kAll], Other other) {
+  double h[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = larger(w[i], other(7 - i));
+#pragma unroll
+  for (int d = 4; d >= 1; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((i & d) == 0) {
+        const double p = h[i], q = h[i + d];
+        h[i] = larger(p, q);
+        h[i + d] = smaller(p, q);
+      }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = h[i];
+}
+
+// Whether a choice takes lists of 8: every entry may come from one lane.
+template <int kL, int kVpl>
+__device__ __forceinline__ bool lists_of_8(int k) {
+  return kL == 16 && kVpl >= 8 && k <= 8;
+}
+
+// A lane's keys in descending order (its 8 largest, for lists of 8).
+template <int kL, int kVpl>
+__device__ __forceinline__ void sort_lane(double (&v)[kVpl], int k) {
+  if constexpr (kL == 16 && kVpl == 16) {
+    if (lists_of_8<kL, kVpl>(k)) {
+      sort_keys<8, 0>(v);
+      sort_keys<8, 8>(v);
+      double w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = v[8 + i];
+      join8(v, [&](int i) { return w[i]; });
+      return;
+    }
+  }
+  sort_keys<kVpl, 0>(v);
 }
 
 // Whether a group is whole lanes, 1, 2, 4, 8 or 16 of them.
@@ -150,6 +195,7 @@ __device__ __forceinline__ void grid_values(const RouterArgs& a, const float (&x
     clip |= __builtin_fabsf(bias[i]) > 1000.0f;
   }
   if (__any(clip)) {
+    asm volatile("");  // a branch, not selects
 #pragma unroll
     for (int i = 0; i < kVpl; ++i) u[i] = __builtin_fmin(__builtin_fmax(u[i], -kClip), kClip);
   }
@@ -157,14 +203,9 @@ __device__ __forceinline__ void grid_values(const RouterArgs& a, const float (&x
   for (int i = 0; i < kVpl; ++i) u[i] = unless(!(x[i] > -__builtin_inff()), u[i]);
 }
 
-// The two largest of `v` and of what other lanes of the group pass to merge().
+// A group's two largest values, over lanes with merge().
 struct TwoLargest {
   double first = 2 * kNone, second = 2 * kNone;
-  template <int kN>
-  __device__ __forceinline__ void take(const double (&v)[kN]) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) add(v[i]);
-  }
   __device__ __forceinline__ void add(double q) {
     second = __builtin_fmax(second, __builtin_fmin(first, q));
     first = __builtin_fmax(first, q);
@@ -181,34 +222,26 @@ struct TwoLargest {
   }
 };
 
-// Takes the experts of all groups but the best ones out of `v`.  `rank`: the
-// values the groups are ranked by.  `values`: LDS for the token's experts, used
-// where groups are not whole lanes.
+// Whether this lane's group is one of the best, for groups of whole lanes;
+// `best`: the lane's own two largest values.
 template <int kL, int kVpl>
-__device__ __forceinline__ void keep_groups(const RouterArgs& a, const double (&rank)[kVpl], int lane, double* values,
-                                            double (&v)[kVpl]) {
-  const int e0 = lane * kVpl;
-  if (lane_groups(a.group_size, kVpl)) {
-    const int lanes_log2 = __builtin_ctz(a.group_size / kVpl);
-    TwoLargest best;
-    best.take(rank);
-    if (lanes_log2 > 0) best.merge<kDppXor1>();
-    if (lanes_log2 > 1) best.merge<kDppXor2>();
-    if (lanes_log2 > 2) best.merge<kDppMirror8>();
-    if (lanes_log2 > 3) best.merge<kDppMirror16>();
-    const int g = lane >> lanes_log2;
-    double key = make_key(best.value(a.group_top), g);
-    bool keep = false;
-    for (int j = 0; j < a.keep; ++j)
-      if (key == token_max<kL>(key)) keep = true, key = 2 * kNone;  // all of the group's lanes
-#pragma unroll
-    for (int i = 0; i < kVpl; ++i) v[i] = unless(!keep, v[i]);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < kVpl; ++i)
-    if (e0 + i < a.num_experts) values[e0 + i] = rank[i];
-  wave_lds_sync();
+__device__ __forceinline__ bool keep_lane(const RouterArgs& a, TwoLargest best, int lane) {
+  const int lanes_log2 = __builtin_ctz(a.group_size / kVpl);
+  if (lanes_log2 > 0) best.merge<kDppXor1>();
+  if (lanes_log2 > 1) best.merge<kDppXor2>();
+  if (lanes_log2 > 2) best.merge<kDppMirror8>();
+  if (lanes_log2 > 3) best.merge<kDppMirror16>();
+  double key = make_key(best.value(a.group_top), lane >> lanes_log2);
+  bool keep = false;
+  for (int j = 0; j < a.keep; ++j)
+    if (key == token_max<kL>(key)) keep = true, key = 2 * kNone;  // all of the group's lanes
+  return keep;
+}
+
+// The groups that are kept, as bits, for groups of any size; `values`: LDS with
+// the values of the token's experts.
+template <int kL>
+__device__ __forceinline__ uint64_t keep_bits(const RouterArgs& a, int lane, const double* values) {
   constexpr int kRounds = MOE_ROUTE_MAX_GROUPS / kL;
   double key[kRounds];
 #pragma unroll
@@ -230,43 +263,23 @@ __device__ __forceinline__ void keep_groups(const RouterArgs& a, const double (&
     for (int r = 0; r < kRounds; ++r)
       if (key[r] == best) key[r] = 2 * kNone;
   }
-#pragma unroll
-  for (int i = 0; i < kVpl; ++i) {
-    const int g = static_cast<int>((static_cast<uint64_t>(e0 + i) * a.group_magic) >> 32);
-    v[i] = unless(!((kept >> (g & 63)) & 1), v[i]);
-  }
+  return kept;
 }
 
-// Lane j's result is the j-th largest key of the token's lanes (j < k).
+// Lane j's result is the j-th largest key of the token's lanes (j < k); v is
+// sorted.
 template <int kL, int kVpl>
 __device__ __forceinline__ double largest_keys(double (&v)[kVpl], int k, int lane) {
-  sort_keys<kVpl>(v);
   double mine = 2 * kNone;
   if constexpr (kL == 16 && kVpl >= 8) {
-    if (k <= 8) {
-      // The lanes' lists join: of two sorted lists of 8, the larger ones of the
-      // first and the reversed second are the 8 largest, as a bitonic sequence
-      // that three rounds sort; after four exchanges every lane has the
-      // token's 8 largest keys (some 220 instructions; the loop below takes 45
-      // a round).
+    if (lists_of_8<kL, kVpl>(k)) {
+      // After four exchanges every lane has the token's 8 largest keys (some
+      // 240 instructions; the loop below takes 45 a round).
       double w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = v[i];
       const auto join = [&](auto other) {
-        double h[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = larger(w[i], other(w[7 - i]));
-#pragma unroll
-        for (int d = 4; d >= 1; d >>= 1)
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if ((i & d) == 0) {
-              const double p = h[i], q = h[i + d];
-              h[i] = larger(p, q);
-              h[i + d] = smaller(p, q);
-            }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = h[i];
+        for (int i = 0; i < 8; ++i) w[i] = v[i];
+        join8(v, [&](int i) { return other(w[i]); });
       };
       join([](double q) { return dpp<kDppXor1>(q); });
       join([](double q) { return dpp<kDppXor2>(q); });
@@ -274,7 +287,7 @@ __device__ __forceinline__ double largest_keys(double (&v)[kVpl], int k, int lan
       join([](double q) { return dpp<kDppMirror16>(q); });
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (lane == i && i < k) mine = w[i];
+        if (lane == i && i < k) mine = v[i];
       return mine;
     }
   }
@@ -345,21 +358,53 @@ __global__ __launch_bounds__(kWave* route_waves(kL, kVpl)) void route_kernel(Rou
   double v[kVpl];  // selection values as whole numbers, then keys
   if (a.bias != nullptr) {
     grid_values<kSigmoid, kL, kVpl>(a, x, bias, top, v);
-    if (a.groups > 1) keep_groups<kL, kVpl>(a, v, lane, values, v);
   } else {
 #pragma unroll
     for (int i = 0; i < kVpl; ++i) v[i] = unless(!(x[i] > -__builtin_inff()), logit_value(x[i]));
-    if (a.groups > 1 && a.group_top == 2) {
-      double u[kVpl];
+  }
+  // Groups are ranked by these values, or by scores of their own.  A lane of a
+  // group of whole lanes sorts its keys first and has its group's candidates
+  // on top of its list.
+  const bool own_scores = a.groups > 1 && a.group_top == 2 && a.bias == nullptr;
+  const bool whole_lanes = a.groups > 1 && lane_groups(a.group_size, kVpl);
+  TwoLargest best;
+  if (a.groups > 1 && (own_scores || !whole_lanes)) {
+    double u[kVpl];
+    if (own_scores) {
       grid_values<kSigmoid, kL, kVpl>(a, x, bias, top, u);
-      keep_groups<kL, kVpl>(a, u, lane, values, v);
-    } else if (a.groups > 1) {
-      keep_groups<kL, kVpl>(a, v, lane, values, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVpl; ++i) u[i] = v[i];
+    }
+    if (whole_lanes) {
+#pragma unroll
+      for (int i = 0; i < kVpl; ++i) best.add(u[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVpl; ++i)
+        if (e0 + i < a.num_experts) values[e0 + i] = u[i];
+      wave_lds_sync();
+      const uint64_t kept = keep_bits<kL>(a, lane, values);
+#pragma unroll
+      for (int i = 0; i < kVpl; ++i) {
+        const int g = static_cast<int>((static_cast<uint64_t>(e0 + i) * a.group_magic) >> 32);
+        v[i] = unless(!((kept >> (g & 63)) & 1), v[i]);
+      }
     }
   }
   const double base = static_cast<double>((1 << kIdBits) - 1 - e0);
 #pragma unroll
   for (int i = 0; i < kVpl; ++i) v[i] = __builtin_fma(v[i], kIdSpan, base) - static_cast<double>(i);
+  sort_lane<kL, kVpl>(v, a.k);
+  if (whole_lanes) {
+    if (!own_scores) {
+      best.first = key_value(v[0]);
+      if constexpr (kVpl > 1) best.second = key_value(v[1]);
+    }
+    const bool keep = keep_lane<kL, kVpl>(a, best, lane);
+#pragma unroll
+    for (int i = 0; i < kVpl; ++i) v[i] = unless(!keep, v[i]);
+  }
   const double mine = largest_keys<kL, kVpl>(v, a.k, lane);
   const int id = mine > kNone ? key_id(mine) : -1;
 
