@@ -7,10 +7,10 @@
 //   else, softmax: dx_e = p_e (scale g_e - sum_i scale g_i p_i), every expert.
 //
 // A token is the work of 16 lanes or of a wave, as in route.hip: lane j < k
-// works on entry j and puts its value at the expert's place in a row of LDS
-// that the lanes cleared; then lane l reads and writes the kVpl experts from
-// l kVpl.  Bound by the two passes over the logits' bytes (only the softmax
-// without renormalisation reads more of the logits than the chosen ones).
+// works on entry j and puts its value at the expert's place in a row of LDS,
+// which the lanes cleared or, for the last formula, filled.  Bound by the bytes:
+// 16384 tokens x 256 experts, fp32, sigmoid: 5.7 us for 17 MB of gradients and
+// the lines of the chosen logits; the last formula reads all of them.
 #include "device_util.h"
 #include "launch.h"
 #include "router_util.h"
@@ -29,10 +29,13 @@ __global__ __launch_bounds__(kWaves* kWave) void route_backward_kernel(RouterArg
   const bool active = token < a.bs;
   const int64_t t = active ? token : a.bs - 1;  // lanes past the batch work on its last token and store nothing
   const int64_t row = t * a.stride;
-  const int e0 = lane * kVpl;
+  using Row = TokenRow<kL, kVpl>;
   float* place = rows[sub];
+  const bool dense = !kSigmoid && !a.renorm;  // every expert's logit has a gradient
+  float p[kVpl];
 #pragma unroll
-  for (int i = 0; i < kVpl; ++i) place[e0 + i] = 0.0f;
+  for (int i = 0; i < kVpl; ++i) p[i] = 0.0f;
+  if (!dense) Row::put(place, lane, p);
 
   int id = -1;
   float xm = -__builtin_inff(), g = 0.0f;
@@ -45,22 +48,12 @@ __global__ __launch_bounds__(kWaves* kWave) void route_backward_kernel(RouterArg
     else id = -1;
   }
 
-  float ds = 0.0f, dot = 0.0f;
-  float p[kVpl];
-#pragma unroll
-  for (int i = 0; i < kVpl; ++i) p[i] = 0.0f;
-  if (a.renorm) {
-    const float m = token_max<kL>(xm);
-    const float r = id >= 0 ? relative_score<kSigmoid>(xm, m) : 0.0f;
-    const float z = token_sum<kL>(r);
-    const float share = id >= 0 ? r / z : 0.0f;
-    ds = share * (g - token_sum<kL>(g * share));
-    if (kSigmoid) ds *= id >= 0 ? sigmoid_f32(-xm) : 0.0f;
-  } else if (kSigmoid) {
-    if (id >= 0) ds = g * (sigmoid_f32(xm) * sigmoid_f32(-xm));
-  } else {
+  float ds = 0.0f;
+  if (dense) {
     float x[kVpl];
-    load_logits<kVpl>(a.logits, type, row + e0, a.num_experts - e0, x);
+    Row::load(a.logits, type, row, a.num_experts, lane, place);
+    wave_lds_sync();
+    Row::get(place, lane, x);
     float top = x[0], sum = 0.0f;
 #pragma unroll
     for (int i = 1; i < kVpl; ++i) top = __builtin_fmaxf(top, x[i]);
@@ -73,16 +66,25 @@ __global__ __launch_bounds__(kWaves* kWave) void route_backward_kernel(RouterArg
     sum = token_sum<kL>(sum);
     if (sum == 0.0f) sum = 1.0f;  // no eligible expert: p is 0
     ds = id >= 0 ? g * (expf(xm - top) / sum) : 0.0f;
-    dot = token_sum<kL>(ds);
+    const float dot = token_sum<kL>(ds);
 #pragma unroll
     for (int i = 0; i < kVpl; ++i) p[i] = -(p[i] / sum) * dot;
+    wave_lds_sync();
+    Row::put(place, lane, p);
+  } else if (a.renorm) {
+    const float m = token_max<kL>(xm);
+    const float r = id >= 0 ? relative_score<kSigmoid>(xm, m) : 0.0f;
+    const float z = token_sum<kL>(r);
+    const float share = id >= 0 ? r / z : 0.0f;
+    ds = share * (g - token_sum<kL>(g * share));
+    if (kSigmoid) ds *= id >= 0 ? sigmoid_f32(-xm) : 0.0f;
+  } else {
+    if (id >= 0) ds = g * (sigmoid_f32(xm) * sigmoid_f32(-xm));
   }
   wave_lds_sync();
-  if (id >= 0) place[id] = ds;
+  if (id >= 0) place[Row::at(id)] += ds;
   wave_lds_sync();
-#pragma unroll
-  for (int i = 0; i < kVpl; ++i) p[i] += place[e0 + i];
-  if (active) store_logits<kVpl>(a.grad_logits, type, token * a.grad_stride + e0, a.num_experts - e0, p);
+  if (active) Row::store(a.grad_logits, type, token * a.grad_stride, a.num_experts, lane, place);
 }
 
 template <bool kSigmoid, int kL, int kVpl>

@@ -106,26 +106,28 @@ __device__ __forceinline__ void wave_lds_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// One logit, of a type known at run time (the same for the whole launch).
+// Rows start at any element: the vector accesses below are unaligned ones.
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef f32x4 f32x4_u __attribute__((aligned(4)));
+typedef u32x2 u32x2_u __attribute__((aligned(2)));
+typedef u32x4 u32x4_u __attribute__((aligned(2)));
+
 __device__ __forceinline__ float load_logit(const void* base, Out type, int64_t i) {
   if (type == Out::kF32) return load_float<Out::kF32>(base, i);
   return type == Out::kFp16 ? load_float<Out::kFp16>(base, i) : load_float<Out::kBf16>(base, i);
 }
 
 // The logits from element i on, kN of them (of which `have` exist; the others
-// read as -inf), as the router reads them.  Rows start at any element, so the
-// vector loads and stores here are unaligned ones.
-typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
-typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
-typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(2)));
-
+// read as -inf), as the router reads them.
 template <int kN>
 __device__ __forceinline__ void load_logits(const void* base, Out type, int64_t i, int have, float (&x)[kN]) {
   if (kN % 4 == 0 && have >= kN) {
     if (type == Out::kF32) {
 #pragma unroll
       for (int q = 0; q < kN / 4; ++q) {
-        const f32x4_u v = *reinterpret_cast<const f32x4_u*>(static_cast<const float*>(base) + i + 4 * q);
+        const f32x4 v = *reinterpret_cast<const f32x4_u*>(static_cast<const float*>(base) + i + 4 * q);
 #pragma unroll
         for (int r = 0; r < 4; ++r) x[4 * q + r] = v[r];
       }
@@ -135,12 +137,12 @@ __device__ __forceinline__ void load_logits(const void* base, Out type, int64_t 
       if constexpr (kN % 8 == 0) {
 #pragma unroll
         for (int q = 0; q < kN / 8; ++q) {
-          const u32x4_u v = *reinterpret_cast<const u32x4_u*>(p + 8 * q);
+          const u32x4 v = *reinterpret_cast<const u32x4_u*>(p + 8 * q);
 #pragma unroll
           for (int r = 0; r < 4; ++r) w[4 * q + r] = v[r];
         }
       } else if constexpr (kN % 4 == 0) {
-        const u32x2_u v = *reinterpret_cast<const u32x2_u*>(p);
+        const u32x2 v = *reinterpret_cast<const u32x2_u*>(p);
         w[0] = v[0], w[1] = v[1];
       }
 #pragma unroll
@@ -158,39 +160,151 @@ __device__ __forceinline__ void load_logits(const void* base, Out type, int64_t 
   }
 }
 
-template <int kN>
-__device__ __forceinline__ void store_logits(void* base, Out type, int64_t i, int have, const float (&x)[kN]) {
-  if (kN % 4 == 0 && have >= kN) {
+// ---- a token's row through LDS ----------------------------------------------------
+// Global memory is read and written in 16-byte pieces that lie side by side in
+// a wave's lanes; the work is on kVpl neighbours a lane.  LDS is where the two
+// meet: a row of kL kVpl floats.  (Rows of 256 fp32 gradients stored 64 bytes a
+// lane: 10.1 us for 16384 of them; in pieces side by side 6.6, non-temporally
+// 5.7.  The choice, which only reads, is as fast with its loads a lane's own.)
+template <int kL, int kVpl>
+struct TokenRow {
+  static constexpr int kSize = kL * kVpl;
+  // Place of element e: where a lane has 16 neighbours, the four pieces of lanes
+  // 4 apart change places, so that 16 lanes reading one piece each meet all banks.
+  static __device__ __forceinline__ int at(int e) { return kVpl == 16 ? e ^ ((e >> 4) & 12) : e; }
+
+  // Logits of the row from element `row` on, as router_logit() gives them, and
+  // -inf past the experts.
+  static __device__ __forceinline__ void load(const void* base, Out type, int64_t row, int experts, int lane,
+                                              float* lds) {
+    if (type == Out::kF32) {
+      constexpr int kRounds = (kVpl + 3) / 4;
+      f32x4 v[kRounds];
+#pragma unroll
+      for (int q = 0; q < kRounds; ++q) {  // every load before the first use
+        const int e = (q * kL + lane) * 4;
+        if (e + 4 <= experts) {
+          v[q] = *reinterpret_cast<const f32x4_u*>(static_cast<const float*>(base) + row + e);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            v[q][r] = e + r < experts ? load_float<Out::kF32>(base, row + e + r) : -__builtin_inff();
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kRounds; ++q) {
+        const int e = (q * kL + lane) * 4;
+        if (e < kSize) put4(lds, e, v[q]);
+      }
+    } else {
+      constexpr int kRounds = (kVpl + 7) / 8;
+      u32x4 w[kRounds];
+#pragma unroll
+      for (int q = 0; q < kRounds; ++q) {
+        const int e = (q * kL + lane) * 8;
+        const uint16_t* p = static_cast<const uint16_t*>(base) + row + e;
+        if (e + 8 <= experts) {
+          w[q] = *reinterpret_cast<const u32x4_u*>(p);
+        } else {
+          const uint32_t none = type == Out::kFp16 ? 0xfc00u : 0xff80u;  // -inf
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            w[q][r] = (e + 2 * r < experts ? p[2 * r] : none) | ((e + 2 * r + 1 < experts ? p[2 * r + 1] : none) << 16);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < kRounds; ++q) {
+        const int e = (q * kL + lane) * 8;
+        float f[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const uint32_t b = (r & 1) ? w[q][r / 2] >> 16 : w[q][r / 2] & 0xffffu;
+          f[r] = type == Out::kFp16 ? f16_to_f32(b) : bf16_to_f32(b);
+        }
+        if (e < kSize) put4(lds, e, f32x4{f[0], f[1], f[2], f[3]});
+        if (e + 4 < kSize) put4(lds, e + 4, f32x4{f[4], f[5], f[6], f[7]});
+      }
+    }
+  }
+  static __device__ __forceinline__ void put4(float* lds, int e, f32x4 v) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) v[r] = router_logit(v[r]);
+    if (kSize % 4 == 0) {
+      *reinterpret_cast<f32x4*>(lds + at(e)) = v;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (e + r < kSize) lds[e + r] = v[r];
+    }
+  }
+
+  // This lane's neighbours.
+  static __device__ __forceinline__ void get(const float* lds, int lane, float (&x)[kVpl]) {
+    if constexpr (kVpl % 4 == 0) {
+#pragma unroll
+      for (int q = 0; q < kVpl / 4; ++q) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(lds + at(lane * kVpl + 4 * q));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[4 * q + r] = v[r];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVpl; ++i) x[i] = lds[lane * kVpl + i];
+    }
+  }
+  static __device__ __forceinline__ void put(float* lds, int lane, const float (&x)[kVpl]) {
+    if constexpr (kVpl % 4 == 0) {
+#pragma unroll
+      for (int q = 0; q < kVpl / 4; ++q)
+        *reinterpret_cast<f32x4*>(lds + at(lane * kVpl + 4 * q)) =
+            f32x4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVpl; ++i) lds[lane * kVpl + i] = x[i];
+    }
+  }
+
+  // The row's elements, rounded to `type`, to element `row` on.
+  static __device__ __forceinline__ void store(void* base, Out type, int64_t row, int experts, int lane,
+                                               const float* lds) {
     if (type == Out::kF32) {
 #pragma unroll
-      for (int q = 0; q < kN / 4; ++q)
-        *reinterpret_cast<f32x4_u*>(static_cast<float*>(base) + i + 4 * q) =
-            f32x4_u{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
-      return;
+      for (int q = 0; q < (kVpl + 3) / 4; ++q) {
+        const int e = (q * kL + lane) * 4;
+        if (e + 4 <= experts) {
+          f32x4 v;
+          if constexpr (kSize % 4 == 0) v = *reinterpret_cast<const f32x4*>(lds + at(e));
+          __builtin_nontemporal_store(v, reinterpret_cast<f32x4_u*>(static_cast<float*>(base) + row + e));
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (e + r < experts) store_float<Out::kF32>(base, row + e + r, lds[at(e + r)]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < (kVpl + 7) / 8; ++q) {
+        const int e = (q * kL + lane) * 8;
+        uint16_t* p = static_cast<uint16_t*>(base) + row + e;
+        uint32_t h[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const float f = e + r < experts ? lds[at(e + r)] : 0.0f;
+          h[r] = type == Out::kFp16 ? f32_to_f16(round_f32(f)) : f32_to_bf16(f);
+        }
+        if (e + 8 <= experts) {
+          __builtin_nontemporal_store(
+              u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)},
+              reinterpret_cast<u32x4_u*>(p));
+        } else {
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (e + r < experts) p[r] = static_cast<uint16_t>(h[r]);
+        }
+      }
     }
-    uint32_t w[kN / 2 > 0 ? kN / 2 : 1];
-#pragma unroll
-    for (int q = 0; q < kN / 2; ++q)
-      w[q] = type == Out::kFp16 ? f32_to_f16(round_f32(x[2 * q])) | (f32_to_f16(round_f32(x[2 * q + 1])) << 16)
-                                : f32_to_bf16(x[2 * q]) | (f32_to_bf16(x[2 * q + 1]) << 16);
-    uint16_t* p = static_cast<uint16_t*>(base) + i;
-    if constexpr (kN % 8 == 0) {
-#pragma unroll
-      for (int q = 0; q < kN / 8; ++q)
-        *reinterpret_cast<u32x4_u*>(p + 8 * q) = u32x4_u{w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]};
-    } else if constexpr (kN % 4 == 0) {
-      *reinterpret_cast<u32x2_u*>(p) = u32x2_u{w[0], w[1]};
-    }
-    return;
   }
-#pragma unroll
-  for (int q = 0; q < kN; ++q) {
-    if (q >= have) continue;
-    if (type == Out::kF32) store_float<Out::kF32>(base, i + q, x[q]);
-    else if (type == Out::kFp16) store_float<Out::kFp16>(base, i + q, round_f32(x[q]));
-    else store_float<Out::kBf16>(base, i + q, x[q]);
-  }
-}
+};
 
 // 1 / (1 + e^-x) without an overflow on either side.
 __device__ __forceinline__ float sigmoid_f32(float x) {
