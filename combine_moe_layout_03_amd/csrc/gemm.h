@@ -63,9 +63,10 @@ struct GemmDeqArgs {
   const uint8_t* token_scale;  // float of row m at byte m * ts_stride
   int64_t ts_stride;
   void* out;                   // [rows][n]
+  bool nt;                     // set by the launcher: the tiles' results are stored non-temporally
 };
 // Workgroups of one launch.
 int64_t grouped_gemm_deq_blocks(int32_t rows, int32_t groups, int32_t n);
-hipError_t launch_grouped_gemm_deq(const GemmDeqArgs& a, Out out_type, hipStream_t stream);
+hipError_t launch_grouped_gemm_deq(GemmDeqArgs a, Out out_type, hipStream_t stream);
 
 }  // namespace moe

@@ -29,17 +29,23 @@
 // its reasons.  The tiles of 64 x 128 and 128 x 128 take at most 80 KB of LDS,
 // so two workgroups share a CU and one's start and stores run under the
 // other's products; the tile of 256 x 256 takes all of it and moves half the
-// bytes from L2 per product.  Tiles are dealt to the XCDs by the number that
-// the counts give, not by the launch's bound: an eighth each, in an order in
-// which an XCD's L2 holds the weights of 1024 columns while the rows pass.
-// (Dealt by the bound, XCDs with empty slots idled: 16384 rows over 64
-// experts, k and n 2048, took 132 us instead of 112.)  32768 rows over 16
-// experts, k 2048, n 7168: 498 us = 1.93 POP/s, bound by LDS reads beside the
-// matrix cores (a wave reads 12 KB for 32 products of 8 cycles) at the clock
-// that the chip holds under this load; a large library product reaches 2.09
-// POP/s.  Not faster there: loads left out past the last stage (the accumulators
-// spill where the paths meet), token scales loaded before the loop,
-// non-temporal stores, groups of 512 columns; groups of 2048 are 7 % slower.
+// bytes from L2 per product.  Results pass through LDS to whole cache lines.
+// Tiles are dealt to the XCDs by the number that the counts give, not by the
+// launch's bound: an eighth each, in an order in which an XCD's L2 holds the
+// weights of 1024 columns while the rows pass.  (Dealt by the bound, XCDs with
+// empty slots idled: 16384 rows over 64 experts, k and n 2048, took 132 us
+// instead of 112.)  1000 rows over 16 experts, k 2048, n 7168: 54 us = 4.7 TB/s.
+// 32768 rows: 463 us = 2.08 POP/s, which is what a large library product
+// reaches.  A tile there takes 33 us: 3 to find its rows and load its first
+// stages, 24 for 16 stages, 5 for its results.  A stage keeps the matrix cores
+// busy for 2048 cycles and LDS too (192 KB of fragments, 64 KB of loads at 128
+// bytes a cycle), 17 us of the 24 at the clock that the chip holds under this
+// load; they do not overlap fully.  Not faster: one resident workgroup a CU
+// that loads the next tile's first stages before it stores (511 and 486 us), four
+// waves of 128 x 128 (550, 489), weight fragments read a step ahead (the same;
+// the masked instance of 128 x 128 spills), loads left out past the last stage
+// (the accumulators spill where the paths meet), token scales loaded before the
+// loop, groups of 512 columns; groups of 2048 are 7 % slower.
 #include "device_util.h"
 #include "gemm.h"
 #include "router_util.h"
@@ -70,26 +76,45 @@ typedef f32x4 f32x4_u __attribute__((aligned(4)));
 typedef u32x2 u32x2_u __attribute__((aligned(2)));
 typedef u32x4 u32x4_u __attribute__((aligned(2)));
 
-// kN (4 or 8) consecutive columns of one row, as far as the row goes.
-template <Out kOut, int kN>
-__device__ __forceinline__ void store_columns(const GemmDeqArgs& a, int64_t row, int col, const float (&v)[kN]) {
+// Four consecutive columns of one row, as far as the row goes.
+template <Out kOut>
+__device__ __forceinline__ void store_columns(const GemmDeqArgs& a, int64_t row, int col, const float (&v)[4]) {
   const int64_t at = row * a.n + col;
-  if (col + kN <= a.n) {
-    if constexpr (kOut == Out::kF32) {
-#pragma unroll
-      for (int q = 0; q < kN; q += 4)
-        *reinterpret_cast<f32x4_u*>(static_cast<float*>(a.out) + at + q) = f32x4{v[q], v[q + 1], v[q + 2], v[q + 3]};
-    } else if constexpr (kN == 8) {
-      *reinterpret_cast<u32x4_u*>(static_cast<uint16_t*>(a.out) + at) =
-          u32x4{pack2<kOut>(v[0], v[1]), pack2<kOut>(v[2], v[3]), pack2<kOut>(v[4], v[5]), pack2<kOut>(v[6], v[7])};
-    } else {
+  if (col + 4 <= a.n) {
+    if constexpr (kOut == Out::kF32)
+      *reinterpret_cast<f32x4_u*>(static_cast<float*>(a.out) + at) = f32x4{v[0], v[1], v[2], v[3]};
+    else
       *reinterpret_cast<u32x2_u*>(static_cast<uint16_t*>(a.out) + at) =
           u32x2{pack2<kOut>(v[0], v[1]), pack2<kOut>(v[2], v[3])};
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (col + q < a.n) store_float<kOut>(a.out, at + q, round_f32(v[q]));
+  }
+}
+
+// 16 bytes of consecutive columns of one row, as far as the row goes;
+// non-temporally where the call says so.
+template <Out kOut>
+__device__ __forceinline__ void store_piece(const GemmDeqArgs& a, int64_t row, int col, const u32x4& bits) {
+  constexpr int kSize = kOut == Out::kF32 ? 4 : 2, kCols = 16 / kSize;
+  const int64_t at = row * a.n + col;
+  if (col + kCols <= a.n) {
+    u32x4_u* const dst = reinterpret_cast<u32x4_u*>(static_cast<uint8_t*>(a.out) + at * kSize);
+    if (a.nt) {  // the marks keep the compiler from joining the two into one ordinary store
+      asm volatile("; non-temporal");
+      __builtin_nontemporal_store(bits, dst);
+      asm volatile("; non-temporal");
+    } else {
+      *dst = bits;
     }
   } else {
 #pragma unroll
-    for (int q = 0; q < kN; ++q)
-      if (col + q < a.n) store_float<kOut>(a.out, at + q, round_f32(v[q]));
+    for (int q = 0; q < kCols; ++q) {
+      if (col + q >= a.n) continue;
+      if constexpr (kOut == Out::kF32) static_cast<uint32_t*>(a.out)[at + q] = bits[q];
+      else static_cast<uint16_t*>(a.out)[at + q] = static_cast<uint16_t>(bits[q / 2] >> (q % 2 * 16));
+    }
   }
 }
 
@@ -217,7 +242,7 @@ __global__ __launch_bounds__(kWave* kWaves) void stream_kernel(GemmDeqArgs a, in
         float v[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] = static_cast<float>(acc[i][j][q]) * w[j][q] * ts[i];
-        store_columns<kOut, 4>(a, row, col, v);
+        store_columns<kOut>(a, row, col, v);
       }
     }
   }
@@ -421,23 +446,48 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) 
     if (rest > 4) stage(6 * rounds + 4, sa0, sb1, sa1, sb0);
   }
   if (grp == 0) barrier();  // every wave passes the same number of barriers
-  // no load may still be writing this workgroup's LDS when it exits
+  // no load may still be writing this workgroup's LDS
   __builtin_amdgcn_s_waitcnt(vmcnt_wait(0));
 
   if constexpr (!kEarlyScales) load_scales();
+  // 16 rows of results at a time through LDS, so that a store's lanes lie along
+  // rows (whole cache lines; stored from the products' layout, 64 bytes of each
+  // of 16 rows, 32768 rows took 495 us instead of 469).  The weights' slots are
+  // free once every wave's loads have landed and its reads are done.
+  barrier();
+  constexpr int kPieceCols = kOut == Out::kF32 ? 4 : 8;  // columns of a 16-byte piece
+  constexpr int kRowPieces = kWaveN / kPieceCols, kWaveBytes = 16 * kRowPieces * 16;
+  constexpr int kSlotWaves = kTileN * kSK / kWaveBytes < kTileWaves ? kTileN * kSK / kWaveBytes : kTileWaves;
+  static_assert(2 * kSlotWaves >= kTileWaves, "two slots hold every wave's rows");
+  uint8_t* const mine = (wave < kSlotWaves ? sb0 : sb1) + wave % kSlotWaves * kWaveBytes;
+  // piece c of row r lies at c ^ r, so that 16 rows' pieces fall into all banks
+  constexpr int kTurn = (kRowPieces < 16 ? kRowPieces : 16) - 1;
+  const auto place = [&](int r, int c) { return mine + (r * kRowPieces + (c ^ (r & kTurn))) * 16; };
 #pragma unroll
-  for (int p = 0; p < kNI / 2; ++p) {
-    const int col = col_base + p * 32;
-    if (col >= a.n) continue;
+  for (int i = 0; i < kMI; ++i) {
 #pragma unroll
-    for (int i = 0; i < kMI; ++i) {
-      const int row = row0 + wm * kWaveM + i * 16 + l16;
-      if (row >= row_end) continue;
+    for (int p = 0; p < kNI / 2; ++p) {
       float v[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) v[q] = static_cast<float>(acc[i][2 * p + q / 4][q % 4]) * w[p][q] * ts[i];
-      store_columns<kOut, 8>(a, row, col, v);
+      const int c = (p * 4 + lane / 16) * (8 / kPieceCols);
+      if constexpr (kOut == Out::kF32) {
+        *reinterpret_cast<f32x4*>(place(l16, c)) = f32x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f32x4*>(place(l16, c + 1)) = f32x4{v[4], v[5], v[6], v[7]};
+      } else {
+        *reinterpret_cast<u32x4*>(place(l16, c)) =
+            u32x4{pack2<kOut>(v[0], v[1]), pack2<kOut>(v[2], v[3]), pack2<kOut>(v[4], v[5]), pack2<kOut>(v[6], v[7])};
+      }
     }
+    wave_lds_sync();
+#pragma unroll
+    for (int t = 0; t < 16 * kRowPieces / kWave; ++t) {
+      const int r = (t * kWave + lane) / kRowPieces, c = (t * kWave + lane) % kRowPieces;
+      const u32x4 bits = *reinterpret_cast<const u32x4*>(place(r, c));
+      const int row = row0 + wm * kWaveM + i * 16 + r;
+      if (row < row_end) store_piece<kOut>(a, row, col0 + wn * kWaveN + c * kPieceCols, bits);
+    }
+    wave_lds_sync();
   }
 }
 
@@ -456,11 +506,13 @@ hipError_t launch_tile(const GemmDeqArgs& a, hipStream_t stream) {
 // One case for each tile of select::gemm_deq_kind.
 template <Out kOut>
 hipError_t launch_out(const GemmDeqArgs& a, hipStream_t stream) {
-  switch (select::gemm_deq_kind(a.rows, a.groups, a.n)) {
-    case select::GemmDeqKind::kStream16: return launch_stream<kOut, 1, 1, 4, 512>(a, stream);
+  const select::GemmDeqKind kind = select::gemm_deq_kind(a.rows, a.groups, a.n);
+  const bool short_chunks = select::gemm_deq_short_chunks(kind, a.k);
+  switch (kind) {
+    case select::GemmDeqKind::kStream16:
+      return short_chunks ? launch_stream<kOut, 1, 1, 4, 256>(a, stream) : launch_stream<kOut, 1, 1, 4, 512>(a, stream);
     case select::GemmDeqKind::kStream32:
-      return select::gemm_deq_short_chunks(a.k) ? launch_stream<kOut, 2, 1, 4, 256>(a, stream)
-                                                : launch_stream<kOut, 2, 1, 4, 512>(a, stream);
+      return short_chunks ? launch_stream<kOut, 2, 1, 4, 256>(a, stream) : launch_stream<kOut, 2, 1, 4, 512>(a, stream);
     case select::GemmDeqKind::kTile64: return launch_tile<kOut, 64, 128, 2>(a, stream);
     case select::GemmDeqKind::kTile128: return launch_tile<kOut, 128, 128, 2>(a, stream);
     case select::GemmDeqKind::kTile256: return launch_tile<kOut, 256, 256, 4>(a, stream);
@@ -481,9 +533,10 @@ int64_t grouped_gemm_deq_blocks(int32_t rows, int32_t groups, int32_t n) {
   return 0;
 }
 
-hipError_t launch_grouped_gemm_deq(const GemmDeqArgs& a, Out out_type, hipStream_t stream) {
+hipError_t launch_grouped_gemm_deq(GemmDeqArgs a, Out out_type, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
   if (grouped_gemm_deq_blocks(a.rows, a.groups, a.n) > kGemmMaxBlocks) return hipErrorInvalidValue;
+  a.nt = select::gemm_deq_nt(a.rows, a.groups, a.k, a.n, out_type == Out::kF32 ? 4 : 2);
   switch (out_type) {
     case Out::kBf16: return launch_out<Out::kBf16>(a, stream);
     case Out::kFp16: return launch_out<Out::kFp16>(a, stream);

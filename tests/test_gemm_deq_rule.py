@@ -43,7 +43,7 @@ def test_rule_at_its_borders():
     got = kinds([(1, 1, 1), (4, 1, 65536), (5, 1, 65536), (16 * 16, 16, 7168), (17 * 16, 16, 7168), (48 * 16, 16, 7168),
                  (49 * 16, 16, 7168), (128 * 16, 16, 7168), (129 * 16, 16, 7168), (4096, 2, 64), (big, 65536, 65536),
                  (1, 65536, 65536), (big, 1, 1)])
-    assert got == ["stream16", "stream16", "stream32", "stream32", "tile64", "tile64", "tile128", "tile128", "tile256",
+    assert got == ["stream16", "stream16", "tile64", "tile64", "tile64", "tile64", "tile128", "tile128", "tile256",
                    "stream32", "tile256", "stream16", "tile256"]
 
 
@@ -55,5 +55,5 @@ def test_compiled_instances():
               (re.search(r"::stream_kernel<\(moe::Out\)(\d), (\d+), \d+, \d+, (\d+)>", s) for s in names) if m}
     tile = {m.group(1, 2, 3) for m in
             (re.search(r"::tile_kernel<\(moe::Out\)(\d), (\d+), \d+, \d+, (\w+)>", s) for s in names) if m}
-    assert stream == {(o, *r) for o in "012" for r in (("1", "512"), ("2", "256"), ("2", "512"))}
+    assert stream == {(o, *r) for o in "012" for r in (("1", "256"), ("1", "512"), ("2", "256"), ("2", "512"))}
     assert tile == {(o, r, t) for o in "012" for r in ("64", "128", "256") for t in ("true", "false")}

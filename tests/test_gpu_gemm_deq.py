@@ -207,3 +207,11 @@ def test_gemm_deq_every_tile_and_type(tile, kind):
     log(f"gemm_deq {tile} {kind}")
     for k in (144, 256, 2208):
         check(np.random.default_rng(k), rows, k, n, counts, kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+def test_gemm_deq_large_weights(kind):
+    """Weights past what the caches keep (the results are then stored non-temporally), odd rows at odd addresses."""
+    rows, n, counts = TILED["tile64"]
+    log(f"gemm_deq large weights {kind}")
+    check(np.random.default_rng(9), rows, 4112, n - 1, counts, kind)
