@@ -9,6 +9,7 @@
 
 #include "launch.h"
 #include "gemm.h"
+#include "layer.h"
 #include "moe_ep.h"
 
 namespace {

@@ -12,9 +12,9 @@
 // 0.999 GB = 5.2 TB/s, the rate of a large copy.  (A workgroup per token that
 // takes its rows together: 211 us; row by row with g in registers: 193-204.)
 // The rows are loaded non-temporally, and stored so where they are more than
-// the Infinity Cache keeps (select.h).
+// the Infinity Cache keeps (select_layer.h).
 #include "device_util.h"
-#include "launch.h"
+#include "layer.h"
 #include "router_util.h"
 
 #pragma clang fp contract(off)

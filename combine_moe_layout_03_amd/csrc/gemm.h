@@ -5,7 +5,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "launch.h"
 #include "select.h"
 
 namespace moe {
@@ -48,25 +47,5 @@ hipError_t launch_grouped_gemm_i8(const GemmArgs& a, hipStream_t stream);
 // The fused form: clears the row maxima, runs the matmul with the SwiGLU
 // epilogue into the workspace, then quantises the owned rows.
 hipError_t launch_grouped_gemm_swiglu_quant(const GemmArgs& a, hipStream_t stream);
-
-// ---- second expert matmul: int8 products, scaled to 16- or 32-bit floats ----------
-struct GemmDeqArgs {
-  const int8_t* a;             // row m at a + m * a_stride, k int8 codes
-  int64_t a_stride;            // bytes between rows (a multiple of 16)
-  int32_t rows;
-  int32_t k;                   // a multiple of 16
-  const int32_t* group_count;  // [groups]
-  int32_t groups;
-  const int8_t* w;             // [groups][n][k]
-  int32_t n;
-  const float* weight_scale;   // [groups][n]
-  const uint8_t* token_scale;  // float of row m at byte m * ts_stride
-  int64_t ts_stride;
-  void* out;                   // [rows][n]
-  bool nt;                     // set by the launcher: the tiles' results are stored non-temporally
-};
-// Workgroups of one launch.
-int64_t grouped_gemm_deq_blocks(int32_t rows, int32_t groups, int32_t n);
-hipError_t launch_grouped_gemm_deq(GemmDeqArgs a, Out out_type, hipStream_t stream);
 
 }  // namespace moe

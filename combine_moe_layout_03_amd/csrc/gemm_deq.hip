@@ -10,7 +10,7 @@
 // the second: a lane then holds four consecutive columns of one row, which it
 // scales with one token scale and stores together.
 //
-// Two kernels (select.h has the rule):
+// Two kernels (select_layer.h has the rule):
 //
 // stream_kernel, for experts with few rows, where the weights' bytes are the
 // work: a workgroup takes kMI x 16 rows and 64 columns.  The rows lie in LDS
@@ -48,6 +48,7 @@
 // loop, groups of 512 columns; groups of 2048 are 7 % slower.
 #include "device_util.h"
 #include "gemm.h"
+#include "layer.h"
 #include "router_util.h"
 #include "row_slots.h"
 

@@ -121,30 +121,6 @@ constexpr int kEpilogueMaxN = MOE_EPILOGUE_MAX_N;
 
 hipError_t launch_deq_swiglu_quant(const EpilogueArgs& a, hipStream_t stream);
 
-// ---- router and the gradients of the routed path ----------------------------------
-struct RouterArgs {
-  const void* logits;         // row t at element t * stride
-  int64_t stride;
-  int32_t bs, num_experts, k;
-  const float* bias;          // [E] or null
-  int32_t groups, keep, group_top, group_size;
-  uint64_t group_magic;       // div_magic(group_size)
-  int32_t renorm;
-  float scale;
-  const uint8_t* token_mask;  // [bs] or null
-  int32_t* topk_idx;          // [bs, k] (read by the gradient)
-  float* topk_weights;        // [bs, k]
-  // the gradient
-  const float* grad_weights;  // [bs, k]
-  void* grad_logits;          // row t at element t * grad_stride
-  int64_t grad_stride;
-};
-hipError_t launch_route(const RouterArgs& a, Out logits_type, bool sigmoid, hipStream_t stream);
-hipError_t launch_route_backward(const RouterArgs& a, Out logits_type, bool sigmoid, hipStream_t stream);
-hipError_t launch_combine_backward(const RouteArgs& r, const void* grad_out, Out grad_type, const void* recv_x,
-                                   Half recv_type, const float* topk_w, void* grad_recv, float* grad_weights,
-                                   hipStream_t stream);
-
 size_t fused_lds_bytes(int32_t num_experts, int32_t tokens_per_group, int32_t topk, int32_t copies);
 hipError_t launch_fused(const FusedArgs& a, Half x_type, bool quant, int groups, hipStream_t stream);
 

@@ -25,7 +25,7 @@
 // in which values lie too close, was not faster (18 us: one token in 250 is
 // such, and a launch waits for its slowest wave).
 #include "device_util.h"
-#include "launch.h"
+#include "layer.h"
 #include "router_util.h"
 
 namespace moe {

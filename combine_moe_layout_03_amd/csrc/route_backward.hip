@@ -12,7 +12,7 @@
 // 16384 tokens x 256 experts, fp32, sigmoid: 5.7 us for 17 MB of gradients and
 // the lines of the chosen logits; the last formula reads all of them.
 #include "device_util.h"
-#include "launch.h"
+#include "layer.h"
 #include "router_util.h"
 
 namespace moe {

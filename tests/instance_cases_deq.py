@@ -1,6 +1,6 @@
 """Shapes of the scaled int8 expert product that reach every tile (plain data, no torch)."""
 
-# tile: (rows, n, counts), the tile as the launcher's rule picks it (csrc/select.h, gemm_deq_kind); counts that end
+# tile: (rows, n, counts), the tile as the launcher's rule picks it (csrc/select_layer.h, gemm_deq_kind); counts that end
 # inside tiles, experts without rows, and n that ends inside a column tile
 TILED = {
     "stream16": (50, 900, [0, 3, 5, 17, 0, 1, 2, 4, 0, 0, 9, 8, 1, 0]),

@@ -12,7 +12,7 @@ import kernel_remarks
 
 _DRIVER = r"""
 #include <cstdio>
-#include "select.h"
+#include "select_layer.h"
 int main() {
   int rows, groups, n;
   while (std::scanf("%d %d %d", &rows, &groups, &n) == 3)

@@ -11,7 +11,7 @@ import kernel_remarks
 
 _DRIVER = r"""
 #include <cstdio>
-#include "select.h"
+#include "select_layer.h"
 using namespace moe::select;
 int main() {
   for (const RouterShape s : kRouterShapes) std::printf("%d %d ", s.lanes, s.vpl);
