@@ -8,7 +8,7 @@
 // gradient in y's place, so a row may be replaced in place.  A sum is one
 // lane's chunks in order, then the lanes: a fixed order.
 //
-// Bound by the rows' bytes: 4096 tokens x 8 entries, h 7168, bf16, 192 us for
+// Bound by the rows' bytes: 4096 tokens x 8 entries, h 7168, bf16, 194 us for
 // 0.999 GB = 5.2 TB/s, the rate of a large copy.  (A workgroup per token that
 // takes its rows together: 211 us; row by row with g in registers: 193-204.)
 // The rows are loaded non-temporally, and stored so where they are more than

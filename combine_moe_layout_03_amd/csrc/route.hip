@@ -18,10 +18,10 @@
 // Scores for the choice are computed in binary64 (exp64 below; the error of a
 // score is below 2^-44, far below the grid), weights in binary32.
 //
-// Bound by the vector ALU: some 1100 instructions for four tokens of 256
+// Bound by the vector ALU: some 1200 instructions for four tokens of 256
 // experts, 450 of them the sigmoids (binary64 runs at the rate of binary32
-// here).  16384 tokens x 256 experts, 8 groups, fp32: 13.6 us, where the bytes
-// alone take 3.4.  A choice in 32 bits, with this one behind it for the waves
+// here), issued in 75 % of the cycles.  16384 tokens x 256 experts, 8 groups,
+// fp32: 13 us, where the bytes alone take 3.4.  A choice in 32 bits, with this one behind it for the waves
 // in which values lie too close, was not faster (18 us: one token in 250 is
 // such, and a launch waits for its slowest wave).
 #include "device_util.h"

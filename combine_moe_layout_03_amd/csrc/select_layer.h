@@ -69,8 +69,8 @@ constexpr bool combine_backward_nt(int64_t row_bytes) { return row_bytes > kComb
 // ---- router and its gradient: (lanes of a token, experts of a lane) -----------
 // 16 lanes a token, four tokens a wave, where a row of 16 holds the experts
 // and the entries and the batch is large (the choice among 256 experts by
-// either: 1024 tokens 5.1 and, a wave each, 4.7 us; 2048: 5.2, 5.6; 4096: 5.2,
-// 7.8; 16384: 13.6, 23.8); else a wave.
+// either: 1024 tokens 5.0 and, a wave each, 4.8 us; 2048: 5.0, 5.7; 4096: 5.2,
+// 8.1; 16384: 13.2, 23.8); else a wave.
 struct RouterShape {
   int lanes, vpl;
 };
