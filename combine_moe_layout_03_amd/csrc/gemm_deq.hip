@@ -19,7 +19,11 @@
 // fragment load touches 16 rows at 64 bytes each; with the rows' fragments
 // loaded that way too, a decode step took 50 us instead of 44.)  24 rows over
 // 16 experts, k 2048, n 7168: 44 us = 5.35 TB/s, which is what a large copy
-// reaches on this card.
+// reaches on this card.  Where such workgroups would leave most CUs idle, one
+// takes 16 columns only and its four waves a quarter of k each (64 rows over 8
+// experts, k 4096, n 1024: 8.9 us instead of 12.4; the same split within 64
+// columns, 12.8: a CU's loads in flight are the limit there, not the chain of
+// chunks).
 //
 // tile_kernel, for experts with more rows: eight waves in two groups, one wave
 // of each per SIMD, half a step apart; while one multiplies, the other reads
@@ -77,6 +81,15 @@ typedef f32x4 f32x4_u __attribute__((aligned(4)));
 typedef u32x2 u32x2_u __attribute__((aligned(2)));
 typedef u32x4 u32x4_u __attribute__((aligned(2)));
 
+// Where along k a workgroup begins (the sums are exact in any order).  Rows that
+// lie a multiple of 4096 bytes apart fall into few memory channels, and
+// workgroups in step would all ask the same ones (us, begun at 0 and turned: k
+// 4096, n 4096, 16 experts, 24 rows 65 and 51, 200 rows 65, 47, 1000 rows 82,
+// 71; k 8192, n 2048, 1000 rows 79, 72; but k 2048, n 7168, 1000 rows 54.6, 56.0).
+__device__ __forceinline__ int first_turn(int32_t k, int64_t column_block, int group, int turns) {
+  return k % 4096 != 0 ? 0 : static_cast<int>((column_block * 3 + group * int64_t(5)) % turns);
+}
+
 // Four consecutive columns of one row, as far as the row goes.
 template <Out kOut>
 __device__ __forceinline__ void store_columns(const GemmDeqArgs& a, int64_t row, int col, const float (&v)[4]) {
@@ -121,16 +134,20 @@ __device__ __forceinline__ void store_piece(const GemmDeqArgs& a, int64_t row, i
 
 // ---- few rows for each expert -----------------------------------------------------
 
-template <Out kOut, int kMI, int kNI, int kWaves, int kKC>
-__global__ __launch_bounds__(kWave* kWaves) void stream_kernel(GemmDeqArgs a, int64_t slots) {
-  constexpr int kThreads = kWave * kWaves, kCols = 16 * kNI * kWaves;
+template <Out kOut, int kMI, int kNI, int kWaves, int kKC, int kSplit>
+__global__ __launch_bounds__(kWave* kWaves* kSplit) void stream_kernel(GemmDeqArgs a, int64_t slots) {
+  constexpr int kThreads = kWave * kWaves, kCols = 16 * kNI * kWaves;  // of one part
   constexpr int kRowPieces = kKC / 16;
   constexpr int kSteps = kKC / 64;
   constexpr int kCopies = kMI * 16 * kRowPieces / kThreads;  // pieces of a chunk's rows that a thread brings
   static_assert(kRowPieces % 16 == 0 && kCopies * kThreads == kMI * 16 * kRowPieces, "whole chunks");
-  __shared__ __attribute__((aligned(1024))) uint8_t sa0[kMI * 16 * kKC];
-  __shared__ __attribute__((aligned(1024))) uint8_t sa1[kMI * 16 * kKC];
-  const int tid = threadIdx.x, lane = tid % kWave, wave = uniform(tid / kWave);
+  constexpr int kRowsBytes = kMI * 16 * kKC;
+  __shared__ __attribute__((aligned(1024))) uint8_t rows0[kSplit * kRowsBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t rows1[kSplit * kRowsBytes];
+  const int tid = threadIdx.x % kThreads, lane = tid % kWave, wave = uniform(tid / kWave);
+  const int part = kSplit == 1 ? 0 : uniform(threadIdx.x / kThreads);
+  uint8_t* const sa0 = rows0 + part * kRowsBytes;
+  uint8_t* const sa1 = rows1 + part * kRowsBytes;
   // workgroups of one block of columns lie on one XCD, an expert's slots next to each other
   const int64_t x = blockIdx.x % 8, y = blockIdx.x / 8;
   const int64_t slot = y % slots, block = y / slots * 8 + x;
@@ -162,9 +179,12 @@ __global__ __launch_bounds__(kWave* kWaves) void stream_kernel(GemmDeqArgs a, in
 #pragma unroll
   for (int i = 0; i < kMI; ++i)
     ts[i] = *reinterpret_cast<const float*>(a.token_scale + min(rs.row0 + i * 16 + lane % 16, rs.row_end - 1) * a.ts_stride);
-  const int chunks = (a.k + kKC - 1) / kKC;
+  const int rounds = (a.k + kSplit * kKC - 1) / (kSplit * kKC);
+  const int start = first_turn(a.k, block, rs.group, rounds);
+  const auto turn = [&](int r) { return r + start < rounds ? r + start : r + start - rounds; };
   // Past k the rows count as zero, and whatever weights a valid address gives do no harm.
-  auto load_a = [&](int chunk, i32x4 (&v)[kCopies]) {
+  auto load_a = [&](int round, i32x4 (&v)[kCopies]) {
+    const int chunk = turn(round) * kSplit + part;
 #pragma unroll
     for (int q = 0; q < kCopies; ++q) {
       const int at = chunk * kKC + ka[q];
@@ -176,7 +196,8 @@ __global__ __launch_bounds__(kWave* kWaves) void stream_kernel(GemmDeqArgs a, in
 #pragma unroll
     for (int q = 0; q < kCopies; ++q) *reinterpret_cast<i32x4*>(buf + la[q]) = v[q];
   };
-  auto load_b = [&](int chunk, i32x4 (&v)[kSteps][kNI]) {
+  auto load_b = [&](int round, i32x4 (&v)[kSteps][kNI]) {
+    const int chunk = turn(round) * kSplit + part;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const int at = chunk * kKC + s * 64 + piece;
@@ -206,7 +227,7 @@ __global__ __launch_bounds__(kWave* kWaves) void stream_kernel(GemmDeqArgs a, in
   i32x4 va0[kCopies], va1[kCopies], b0[kSteps][kNI], b1[kSteps][kNI];
   load_a(0, va0);
   load_b(0, b0);
-  if (chunks > 1) {
+  if (rounds > 1) {
     load_a(1, va1);
     load_b(1, b1);
   }
@@ -215,21 +236,40 @@ __global__ __launch_bounds__(kWave* kWaves) void stream_kernel(GemmDeqArgs a, in
   // A buffer is written again only after the barrier that follows its readers.
   for (int c = 0;; c += 2) {
     multiply(sa0, b0);
-    if (c + 1 >= chunks) break;
-    if (c + 2 < chunks) {
+    if (c + 1 >= rounds) break;
+    if (c + 2 < rounds) {
       load_a(c + 2, va0);
       load_b(c + 2, b0);
     }
     put_a(sa1, va1);
     __syncthreads();
     multiply(sa1, b1);
-    if (c + 2 >= chunks) break;
-    if (c + 3 < chunks) {
+    if (c + 2 >= rounds) break;
+    if (c + 3 < rounds) {
       load_a(c + 3, va1);
       load_b(c + 3, b1);
     }
     put_a(sa0, va0);
     __syncthreads();
+  }
+  if constexpr (kSplit > 1) {  // the first part adds the others' sums
+    static_assert((kSplit - 1) * kThreads * kMI * kNI * 16 <= kSplit * kRowsBytes, "the sums fit over the rows");
+    i32x4* const sums = reinterpret_cast<i32x4*>(rows0);
+    __syncthreads();
+    if (part > 0) {
+#pragma unroll
+      for (int i = 0; i < kMI; ++i)
+#pragma unroll
+        for (int j = 0; j < kNI; ++j) sums[((part - 1) * kMI * kNI + i * kNI + j) * kThreads + tid] = acc[i][j];
+    }
+    __syncthreads();
+    if (part > 0) return;
+#pragma unroll
+    for (int p = 1; p < kSplit; ++p)
+#pragma unroll
+      for (int i = 0; i < kMI; ++i)
+#pragma unroll
+        for (int j = 0; j < kNI; ++j) acc[i][j] += sums[((p - 1) * kMI * kNI + i * kNI + j) * kThreads + tid];
   }
 
 #pragma unroll
@@ -253,11 +293,11 @@ int64_t stream_blocks(int32_t rows, int32_t groups, int32_t n, int tile_m, int t
   return row_slots(rows, groups, tile_m) * (((static_cast<int64_t>(n) + tile_n - 1) / tile_n + 7) / 8 * 8);
 }
 
-template <Out kOut, int kMI, int kNI, int kWaves, int kKC>
+template <Out kOut, int kMI, int kNI, int kWaves, int kKC, int kSplit = 1>
 hipError_t launch_stream(const GemmDeqArgs& a, hipStream_t stream) {
   const dim3 grid(static_cast<uint32_t>(stream_blocks(a.rows, a.groups, a.n, kMI * 16, 16 * kNI * kWaves)));
-  stream_kernel<kOut, kMI, kNI, kWaves, kKC>
-      <<<grid, dim3(kWave * kWaves), 0, stream>>>(a, row_slots(a.rows, a.groups, kMI * 16));
+  stream_kernel<kOut, kMI, kNI, kWaves, kKC, kSplit>
+      <<<grid, dim3(kWave * kWaves * kSplit), 0, stream>>>(a, row_slots(a.rows, a.groups, kMI * 16));
   return hipGetLastError();
 }
 
@@ -347,8 +387,13 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) 
   const int stages = (a.k + kSK - 1) / kSK;
   // Stages past the last one load it again, into slots that are not read; a
   // piece past k reads the row's first piece (its row fragments count as zero).
+  // An expert's tiles in step, so that they share their rows and weights in L2;
+  // the tile of 256 rows is not bound by its loads.  (A k with a tail begins at 0.)
+  constexpr bool kTurned = kTileM < 256 && !kTail;
+  const int start = kTurned ? first_turn(a.k, 0, rs.group, stages) : 0;
+  const auto turn = [&](int s) { return !kTurned || s + start < stages ? s + start : s + start - stages; };
   auto stage_offset = [&](int s) {
-    const int k0 = min(s, stages - 1) * kSK;
+    const int k0 = turn(min(s, stages - 1)) * kSK;
     if constexpr (kTail) return (k0 + piece * 16 < a.k) ? k0 : -piece * 16;
     return k0;
   };
@@ -510,6 +555,7 @@ hipError_t launch_out(const GemmDeqArgs& a, hipStream_t stream) {
   const select::GemmDeqKind kind = select::gemm_deq_kind(a.rows, a.groups, a.n);
   const bool short_chunks = select::gemm_deq_short_chunks(kind, a.k);
   switch (kind) {
+    case select::GemmDeqKind::kSplit16: return launch_stream<kOut, 1, 1, 1, 256, 4>(a, stream);
     case select::GemmDeqKind::kStream16:
       return short_chunks ? launch_stream<kOut, 1, 1, 4, 256>(a, stream) : launch_stream<kOut, 1, 1, 4, 512>(a, stream);
     case select::GemmDeqKind::kStream32:
@@ -525,6 +571,7 @@ hipError_t launch_out(const GemmDeqArgs& a, hipStream_t stream) {
 
 int64_t grouped_gemm_deq_blocks(int32_t rows, int32_t groups, int32_t n) {
   switch (select::gemm_deq_kind(rows, groups, n)) {
+    case select::GemmDeqKind::kSplit16: return stream_blocks(rows, groups, n, 16, 16);
     case select::GemmDeqKind::kStream16: return stream_blocks(rows, groups, n, 16, 64);
     case select::GemmDeqKind::kStream32: return stream_blocks(rows, groups, n, 32, 64);
     case select::GemmDeqKind::kTile64: return tile_blocks(rows, groups, n, 64, 128);

@@ -24,14 +24,22 @@ namespace select {
 // tile256, 16, 11, 8.6 with stream32; 1000 rows, k 4096, n 1024, 8 experts, 152
 // of tile64: 36 with tile256, 21, 19 with tile64, 30 with stream32; 8000 such
 // rows, 140 of tile256: 44 with tile256, 53 with tile128).
-enum class GemmDeqKind { kStream16, kStream32, kTile64, kTile128, kTile256 };
+//
+// Where all workgroups of 16 columns fit on the chip at once (four a CU), those
+// are the fastest (split16, and the best of the others; us): 2 rows, 8 experts,
+// k 5904, n 213: 6.9, 10.6; 30, 5, 5488, 1546: 12.5, 12.9; 128, 4, 7168, 512:
+// 11.7, 18.8; 1000, 1, 7168, 128: 13.4, 20.0; 24, 12, 7168, 1024 (832 of them):
+// 20.4, 21.8; but 128, 2, 4096, 2048 (1280): 15.0, 13.0.
+enum class GemmDeqKind { kStream16, kStream32, kTile64, kTile128, kTile256, kSplit16 };
 
 // Workgroups to expect: every other expert ends inside a tile.
 constexpr int64_t gemm_deq_workgroups(int32_t rows, int32_t groups, int32_t n, int tile_m, int tile_n) {
   return (rows / tile_m + (int64_t(groups) + 1) / 2) * ((int64_t(n) + tile_n - 1) / tile_n);
 }
 constexpr GemmDeqKind gemm_deq_kind(int32_t rows, int32_t groups, int32_t n) {
-  constexpr int64_t kFewWorkgroups = 128, kFewTile64 = 144;
+  constexpr int64_t kFewWorkgroups = 128, kFewTile64 = 144, kSplitWorkgroups = 1024;
+  const int64_t slots16 = rows / 16 + (rows < groups ? rows : groups);
+  if (slots16 * ((int64_t(n) + 15) / 16) <= kSplitWorkgroups) return GemmDeqKind::kSplit16;
   const int64_t mean = (int64_t(rows) + groups - 1) / groups;
   if (mean <= 4) return GemmDeqKind::kStream16;
   if (mean > 128 && gemm_deq_workgroups(rows, groups, n, 256, 256) >= kFewWorkgroups) return GemmDeqKind::kTile256;
@@ -41,10 +49,10 @@ constexpr GemmDeqKind gemm_deq_kind(int32_t rows, int32_t groups, int32_t n) {
 
 // The streams' chunks of k: 256 bytes end nearer to a short k, 512 have half the
 // barriers (us, 256 and 512; stream16, 48 rows: k 512 8.5 and 9.4, k 768 13.4,
-// 16.4, k 1024 30.9, 30.0; stream32: k 1040 7.5, 8.4, k 2048 48.1, 49.3, k 7168
-// 44.3, 38.3).
+// 16.4, k 1024 30.9, 30.0; stream32: k 1040 7.8, 8.5, k 1536 7.3, 7.3, k 2048
+// 9.9, 8.4, k 4112 16.2, 15.9).
 constexpr bool gemm_deq_short_chunks(GemmDeqKind kind, int32_t k) {
-  return kind == GemmDeqKind::kStream16 ? k < 1024 : k <= 2048;
+  return k < (kind == GemmDeqKind::kStream16 ? 1024 : 1536);
 }
 
 // Results of the tiles: non-temporally where weights, rows and results are more

@@ -19,7 +19,7 @@ int main() {
     std::printf("%d\n", static_cast<int>(moe::select::gemm_deq_kind(rows, groups, n)));
 }
 """
-KINDS = ["stream16", "stream32", "tile64", "tile128", "tile256"]
+KINDS = ["stream16", "stream32", "tile64", "tile128", "tile256", "split16"]
 
 
 def kinds(shapes):
@@ -43,7 +43,7 @@ def test_rule_at_its_borders():
     got = kinds([(1, 1, 1), (4, 1, 65536), (5, 1, 65536), (16 * 16, 16, 7168), (17 * 16, 16, 7168), (48 * 16, 16, 7168),
                  (49 * 16, 16, 7168), (128 * 16, 16, 7168), (129 * 16, 16, 7168), (4096, 2, 64), (big, 65536, 65536),
                  (1, 65536, 65536), (big, 1, 1)])
-    assert got == ["stream16", "stream16", "tile64", "tile64", "tile64", "tile64", "tile128", "tile128", "tile256",
+    assert got == ["split16", "stream16", "tile64", "tile64", "tile64", "tile64", "tile128", "tile128", "tile256",
                    "stream32", "tile256", "stream16", "tile256"]
 
 
@@ -51,9 +51,11 @@ def test_compiled_instances():
     if not kernel_remarks.hipcc_available():
         pytest.skip("hipcc not available")
     names = kernel_remarks.demangle(kernel_remarks.kernel_remarks()).values()
-    stream = {m.group(1, 2, 3) for m in
-              (re.search(r"::stream_kernel<\(moe::Out\)(\d), (\d+), \d+, \d+, (\d+)>", s) for s in names) if m}
+    stream = {m.group(1, 2, 3, 4, 5) for m in
+              (re.search(r"::stream_kernel<\(moe::Out\)(\d), (\d+), 1, (\d+), (\d+), (\d+)>", s) for s in names) if m}
     tile = {m.group(1, 2, 3) for m in
             (re.search(r"::tile_kernel<\(moe::Out\)(\d), (\d+), \d+, \d+, (\w+)>", s) for s in names) if m}
-    assert stream == {(o, *r) for o in "012" for r in (("1", "256"), ("1", "512"), ("2", "256"), ("2", "512"))}
+    assert stream == {(o, *r) for o in "012" for r in (
+        ("1", "1", "256", "4"), ("1", "4", "256", "1"), ("1", "4", "512", "1"), ("2", "4", "256", "1"),
+        ("2", "4", "512", "1"))}
     assert tile == {(o, r, t) for o in "012" for r in ("64", "128", "256") for t in ("true", "false")}

@@ -215,3 +215,11 @@ def test_gemm_deq_large_weights(kind):
     rows, n, counts = TILED["tile64"]
     log(f"gemm_deq large weights {kind}")
     check(np.random.default_rng(9), rows, 4112, n - 1, counts, kind)
+
+
+@pytest.mark.parametrize("tile", TILED)
+def test_gemm_deq_turned_k(tile):
+    """A k of whole 4096s, which the experts and columns walk from places of their own."""
+    rows, n, counts = TILED[tile]
+    log(f"gemm_deq {tile} k 4096")
+    check(np.random.default_rng(10), rows, 4096, n, counts, "bf16")
