@@ -73,6 +73,10 @@ constexpr bool gemm_deq_nt(int64_t rows, int64_t groups, int64_t k, int64_t n, i
 // 24.1 us; 768: 37.8, 35.0; 1024: 48.8, 52.3; 4096: 198, 210).
 constexpr int64_t kCombineBackwardNtBytes = int64_t(96) << 20;
 constexpr bool combine_backward_nt(int64_t row_bytes) { return row_bytes > kCombineBackwardNtBytes; }
+// Short rows: 16 lanes an entry, four a wave (16 lanes and a wave, 4096 tokens, 8
+// entries, bf16, us: h 64 4.6 and 9.5, h 256 8.7, 14.2, h 512 14.4, 17.5, h 1024
+// 26.2, 26.2; 61 tokens, 5, h 1000: 3.9, 2.5).
+constexpr bool combine_backward_short(int32_t hidden) { return hidden <= 512; }
 
 // ---- router and its gradient: (lanes of a token, experts of a lane) -----------
 // 16 lanes a token, four tokens a wave, where a row of 16 holds the experts

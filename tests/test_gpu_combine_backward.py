@@ -64,7 +64,8 @@ def expected(g, y, w, row, kind, rows):
 
 @pytest.mark.parametrize("bs,h,k,epr,ranks", [(1, 8, 1, 1, 1), (3, 64, 4, 2, 3), (17, 1000, 5, 8, 3), (40, 2048, 8, 16, 2),
                                               (5, 7168, 8, 16, 16), (7, 4104, 9, 3, 2), (4, 520, 32, 40, 1),
-                                              (2, 16384, 3, 4, 1), (6, 512, 17, 5, 4)])
+                                              (2, 16384, 3, 4, 1), (6, 512, 17, 5, 4), (301, 72, 9, 6, 2),
+                                              (131, 504, 5, 3, 4), (50, 520, 9, 7, 2)])
 @pytest.mark.parametrize("kind", ["bf16", "fp16"])
 @pytest.mark.parametrize("grad", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("inplace", [False, True], ids=["", "inplace"])
