@@ -153,8 +153,11 @@ def _dev(t: Optional[torch.Tensor], name: str, dtype=None, optional: bool = Fals
         if optional:
             return None
         raise ValueError(f"{name} is required")
-    if isinstance(t, torch.Tensor) and t.is_cuda and (dtype is None or t.dtype is dtype) and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.is_cuda and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # no tensor
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if dtype is not None and t.dtype != dtype:
@@ -166,7 +169,14 @@ def _need(t: Optional[torch.Tensor], name: str, count: int) -> None:
     """Raise unless ``t`` (if given) holds at least ``count`` elements: the
     library takes bare pointers, so an undersized tensor would be written or
     read past its end."""
-    if t is not None and isinstance(t, torch.Tensor) and t.numel() < count:
+    if t is None:
+        return
+    try:
+        if t.numel() >= count:
+            return
+    except AttributeError:  # no tensor: _dev says so
+        return
+    if isinstance(t, torch.Tensor):
         raise ValueError(f"{name} holds {t.numel()} elements, the call needs {count}")
 
 
@@ -189,7 +199,7 @@ def _need_routes(expert_num_per_rank: int, rank_size: int, put_offset: Optional[
 def _need_scales(token_scale: torch.Tensor, rows: int, stride: int) -> None:
     if rows > 0 and stride >= 4:
         need = (rows - 1) * stride + 4
-        have = token_scale.numel() * token_scale.element_size()
+        have = token_scale.nbytes
         if have < need:
             raise ValueError(f"token_scale holds {have} bytes, rows at stride {stride} need {need}")
 
@@ -501,9 +511,10 @@ def _logit_rows(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
     dense (the rows themselves may lie apart)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be [bs, num_experts]")
-    bs, e = t.shape
+    bs, e = shape
     if t.is_contiguous():
         return bs, e, e
     stride, inner = t.stride()
@@ -533,7 +544,8 @@ def moe_route(logits: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.
     topk = shape[1]
     if topk_weights.shape != shape:
         raise ValueError("topk_weights must be [bs, topk]")
-    _need(bias, "bias", e)
+    if bias is not None:
+        _need(bias, "bias", e)
     if token_mask is not None:
         _need(token_mask, "token_mask", bs)
         if token_mask.dtype is not torch.uint8 and token_mask.dtype is not torch.bool:
@@ -587,10 +599,10 @@ def moe_combine_backward(grad_out: torch.Tensor, recv_x: torch.Tensor, recv_type
     _need_routes(expert_num_per_rank, rank_size, put_offset, recv_base)
     _check("moe_combine_backward", _lib.moe_combine_backward(
         _dev(grad_out, "grad_out"), dtype_code(grad_out.dtype), _dev(recv_x, "recv_x"), recv_type,
-        recv_x.numel() * recv_x.element_size(), bs, hidden, topk, _dev(topk_idx, "topk_idx", torch.int32),
+        recv_x.nbytes, bs, hidden, topk, _dev(topk_idx, "topk_idx", torch.int32),
         _dev(topk_weights, "topk_weights", torch.float32), _dev(send_token_idx, "send_token_idx", torch.int32),
         _dev(put_offset, "put_offset", torch.int32), _dev(recv_base, "recv_base", torch.int32), expert_num_per_rank,
-        rank_size, _dev(grad_recv, "grad_recv"), grad_recv.numel() * grad_recv.element_size(),
+        rank_size, _dev(grad_recv, "grad_recv"), grad_recv.nbytes,
         _dev(grad_weights, "grad_weights", torch.float32), _stream(stream)))
 
 
@@ -605,11 +617,11 @@ def moe_combine_backward_src(grad_out: torch.Tensor, recv_x: torch.Tensor, recv_
     _need_routes(expert_num_per_rank, rank_size, put_offset, recv_base, put_offset.shape[1])
     _check("moe_combine_backward_src", _lib.moe_combine_backward_src(
         _dev(grad_out, "grad_out"), dtype_code(grad_out.dtype), _dev(recv_x, "recv_x"), recv_type,
-        recv_x.numel() * recv_x.element_size(), bs, hidden, topk, _dev(topk_idx, "topk_idx", torch.int32),
+        recv_x.nbytes, bs, hidden, topk, _dev(topk_idx, "topk_idx", torch.int32),
         _dev(topk_weights, "topk_weights", torch.float32), _dev(send_token_idx, "send_token_idx", torch.int32),
         _dev(put_offset, "put_offset", torch.int32), _dev(recv_base, "recv_base", torch.int32), expert_num_per_rank,
         rank_size, put_offset.shape[1], src_rank, _dev(grad_recv, "grad_recv"),
-        grad_recv.numel() * grad_recv.element_size(), _dev(grad_weights, "grad_weights", torch.float32),
+        grad_recv.nbytes, _dev(grad_weights, "grad_weights", torch.float32),
         _stream(stream)))
 
 
@@ -640,7 +652,7 @@ def moe_grouped_gemm_deq_i8(a: torch.Tensor, a_row_bytes: int, rows: int, k: int
     _check("moe_grouped_gemm_deq_i8", _lib.moe_grouped_gemm_deq_i8(
         _dev(a, "a"), a_row_bytes, rows, k, _dev(group_count, "group_count", torch.int32), groups, _dev(w, "w"), n,
         _dev(weight_scale, "weight_scale", torch.float32), token_scale.data_ptr(), token_scale_stride,
-        _dev(out, "out"), dtype_code(out.dtype), out.numel() * out.element_size(), _stream(stream)))
+        _dev(out, "out"), dtype_code(out.dtype), out.nbytes, _stream(stream)))
 
 
 def token_scales_of(recv_x: torch.Tensor, hidden: int) -> Tuple[torch.Tensor, int]:
