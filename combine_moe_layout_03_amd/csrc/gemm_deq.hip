@@ -13,13 +13,13 @@
 // Two kernels (select_layer.h has the rule):
 //
 // stream_kernel, for experts with few rows, where the weights' bytes are the
-// work: a workgroup takes kMI x 16 rows and 64 columns.  The rows lie in LDS
-// in chunks of kKC bytes of k, two buffers; a wave owns 16 columns and loads
-// their weights straight into registers, two chunks ahead, each byte once.  (A
-// fragment load touches 16 rows at 64 bytes each; with the rows' fragments
-// loaded that way too, a decode step took 50 us instead of 44.)  24 rows over
-// 16 experts, k 2048, n 7168: 44 us = 5.35 TB/s, which is what a large copy
-// reaches on this card.  Where such workgroups would leave most CUs idle, one
+// work: a workgroup takes kMI x 16 rows and 64 columns, or 32 and two parts of
+// k.  The rows lie in LDS in chunks of kKC bytes of k, two buffers; a wave owns
+// 16 columns and loads their weights straight into registers, two chunks ahead,
+// each byte once.  (A fragment load touches 16 rows at 64 bytes each; with the
+// rows' fragments loaded that way too, a decode step took 50 us instead of 44.)
+// 24 rows over 16 experts, k 2048, n 7168: 43 us = 5.5 TB/s, more than a large
+// copy reaches on this card.  Where such workgroups would leave most CUs idle, one
 // takes 16 columns only and its four waves a quarter of k each (64 rows over 8
 // experts, k 4096, n 1024: 8.9 us instead of 12.4; the same split within 64
 // columns, 12.8: a CU's loads in flight are the limit there, not the chain of
@@ -557,7 +557,8 @@ hipError_t launch_out(const GemmDeqArgs& a, hipStream_t stream) {
   switch (kind) {
     case select::GemmDeqKind::kSplit16: return launch_stream<kOut, 1, 1, 1, 256, 4>(a, stream);
     case select::GemmDeqKind::kStream16:
-      return short_chunks ? launch_stream<kOut, 1, 1, 4, 256>(a, stream) : launch_stream<kOut, 1, 1, 4, 512>(a, stream);
+      return short_chunks ? launch_stream<kOut, 1, 1, 4, 256>(a, stream)
+                          : launch_stream<kOut, 1, 1, 2, 256, 2>(a, stream);
     case select::GemmDeqKind::kStream32:
       return short_chunks ? launch_stream<kOut, 2, 1, 4, 256>(a, stream) : launch_stream<kOut, 2, 1, 4, 512>(a, stream);
     case select::GemmDeqKind::kTile64: return launch_tile<kOut, 64, 128, 2>(a, stream);
@@ -572,7 +573,7 @@ hipError_t launch_out(const GemmDeqArgs& a, hipStream_t stream) {
 int64_t grouped_gemm_deq_blocks(int32_t rows, int32_t groups, int32_t n) {
   switch (select::gemm_deq_kind(rows, groups, n)) {
     case select::GemmDeqKind::kSplit16: return stream_blocks(rows, groups, n, 16, 16);
-    case select::GemmDeqKind::kStream16: return stream_blocks(rows, groups, n, 16, 64);
+    case select::GemmDeqKind::kStream16: return stream_blocks(rows, groups, n, 16, 32);  // (64 for a short k)
     case select::GemmDeqKind::kStream32: return stream_blocks(rows, groups, n, 32, 64);
     case select::GemmDeqKind::kTile64: return tile_blocks(rows, groups, n, 64, 128);
     case select::GemmDeqKind::kTile128: return tile_blocks(rows, groups, n, 128, 128);

@@ -48,9 +48,11 @@ constexpr GemmDeqKind gemm_deq_kind(int32_t rows, int32_t groups, int32_t n) {
 }
 
 // The streams' chunks of k: 256 bytes end nearer to a short k, 512 have half the
-// barriers (us, 256 and 512; stream16, 48 rows: k 512 8.5 and 9.4, k 768 13.4,
-// 16.4, k 1024 30.9, 30.0; stream32: k 1040 7.8, 8.5, k 1536 7.3, 7.3, k 2048
-// 9.9, 8.4, k 4112 16.2, 15.9).
+// barriers; stream16 takes the 512 as two parts of 256, each the work of two of
+// its waves (us, 256, 512 and two parts; stream16, 48 rows: k 512 8.5, 9.4, -, k
+// 768 13.4, 16.4, 16.7, k 1024 30.9, 30.9, 30.1, 64 rows: k 2048 48.1, 46.2, 44.0,
+// 24 rows: k 7168 -, 81.0, 76.9; stream32: k 1040 7.8, 8.5, k 1536 7.3, 7.3, k
+// 2048 9.9, 8.4, k 4112 16.2, 15.9).
 constexpr bool gemm_deq_short_chunks(GemmDeqKind kind, int32_t k) {
   return k < (kind == GemmDeqKind::kStream16 ? 1024 : 1536);
 }

@@ -56,6 +56,6 @@ def test_compiled_instances():
     tile = {m.group(1, 2, 3) for m in
             (re.search(r"::tile_kernel<\(moe::Out\)(\d), (\d+), \d+, \d+, (\w+)>", s) for s in names) if m}
     assert stream == {(o, *r) for o in "012" for r in (
-        ("1", "1", "256", "4"), ("1", "4", "256", "1"), ("1", "4", "512", "1"), ("2", "4", "256", "1"),
+        ("1", "1", "256", "4"), ("1", "4", "256", "1"), ("1", "2", "256", "2"), ("2", "4", "256", "1"),
         ("2", "4", "512", "1"))}
     assert tile == {(o, r, t) for o in "012" for r in ("64", "128", "256") for t in ("true", "false")}
