@@ -54,6 +54,7 @@
 #include "gemm.h"
 #include "layer.h"
 #include "router_util.h"
+#include "row_range.h"
 #include "row_slots.h"
 
 #pragma clang fp contract(off)
@@ -166,7 +167,7 @@ __global__ __launch_bounds__(kWave* kWaves* kSplit) void stream_kernel(GemmDeqAr
 #pragma unroll
   for (int q = 0; q < kCopies; ++q) {
     const int p = q * kThreads + tid, r = p / kRowPieces, c = p % kRowPieces;
-    pa[q] = a.a + min(rs.row0 + r, rs.row_end - 1) * a.a_stride;
+    pa[q] = a.a + tile_row(rs.row0, rs.row_end, r) * a.a_stride;
     ka[q] = c * 16;
     la[q] = r * kKC + (c ^ (r % 16)) * 16;
   }
@@ -178,7 +179,8 @@ __global__ __launch_bounds__(kWave* kWaves* kSplit) void stream_kernel(GemmDeqAr
     for (int q = 0; q < 4; ++q) w[j][q] = ws[min(col0 + j * 16 + lane / 16 * 4 + q, a.n - 1)];
 #pragma unroll
   for (int i = 0; i < kMI; ++i)
-    ts[i] = *reinterpret_cast<const float*>(a.token_scale + min(rs.row0 + i * 16 + lane % 16, rs.row_end - 1) * a.ts_stride);
+    ts[i] = *reinterpret_cast<const float*>(a.token_scale +
+                                            tile_row(rs.row0, rs.row_end, i * 16 + lane % 16) * a.ts_stride);
   const int rounds = (a.k + kSplit * kKC - 1) / (kSplit * kKC);
   const int start = first_turn(a.k, block, rs.group, rounds);
   const auto turn = [&](int r) { return r + start < rounds ? r + start : r + start - rounds; };
@@ -278,12 +280,12 @@ __global__ __launch_bounds__(kWave* kWaves* kSplit) void stream_kernel(GemmDeqAr
     if (col >= a.n) continue;
 #pragma unroll
     for (int i = 0; i < kMI; ++i) {
-      const int row = rs.row0 + i * 16 + lane % 16;
-      if (row < rs.row_end) {
+      const int r = i * 16 + lane % 16;
+      if (tile_has_row(rs.row0, rs.row_end, r)) {
         float v[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[q] = static_cast<float>(acc[i][j][q]) * w[j][q] * ts[i];
-        store_columns<kOut>(a, row, col, v);
+        store_columns<kOut>(a, rs.row0 + r, col, v);
       }
     }
   }
@@ -359,7 +361,7 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) 
 #pragma unroll
   for (int q = 0; q < kLoadsA; ++q) {
     const int r = kRowsPerLoad * (q * kTileWaves + wave) + lane / 8;
-    src_a[q] = a.a + min(row0 + r, row_end - 1) * a.a_stride + piece * 16;
+    src_a[q] = a.a + tile_row(row0, row_end, r) * a.a_stride + piece * 16;
   }
 #pragma unroll
   for (int q = 0; q < kLoadsB; ++q) {
@@ -377,7 +379,7 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) 
 #pragma unroll
     for (int i = 0; i < kMI; ++i)
       ts[i] = *reinterpret_cast<const float*>(a.token_scale +
-                                              min(row0 + wm * kWaveM + i * 16 + l16, row_end - 1) * a.ts_stride);
+                                              tile_row(row0, row_end, wm * kWaveM + i * 16 + l16) * a.ts_stride);
 #pragma unroll
     for (int p = 0; p < kNI / 2; ++p)
 #pragma unroll
@@ -530,8 +532,8 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) 
     for (int t = 0; t < 16 * kRowPieces / kWave; ++t) {
       const int r = (t * kWave + lane) / kRowPieces, c = (t * kWave + lane) % kRowPieces;
       const u32x4 bits = *reinterpret_cast<const u32x4*>(place(r, c));
-      const int row = row0 + wm * kWaveM + i * 16 + r;
-      if (row < row_end) store_piece<kOut>(a, row, col0 + wn * kWaveN + c * kPieceCols, bits);
+      const int tr = wm * kWaveM + i * 16 + r;
+      if (tile_has_row(row0, row_end, tr)) store_piece<kOut>(a, row0 + tr, col0 + wn * kWaveN + c * kPieceCols, bits);
     }
     wave_lds_sync();
   }
