@@ -657,7 +657,7 @@ int moe_grouped_gemm_deq_i8(const void* a, int64_t a_row_bytes, int32_t rows, in
       !aligned(token_scale, 4) || !aligned(out, es))
     return MOE_ERR_BAD_ALIGN;
   if (out_bytes / es / static_cast<size_t>(n) < static_cast<size_t>(rows)) return MOE_ERR_BUFFER_TOO_SMALL;
-  if (moe::grouped_gemm_deq_blocks(rows, groups, n) > moe::kGemmMaxBlocks) return MOE_ERR_UNSUPPORTED;
+  if (!moe::grouped_gemm_deq_fits(rows, groups, n)) return MOE_ERR_UNSUPPORTED;
   moe::GemmDeqArgs g{};
   g.a = static_cast<const int8_t*>(a);
   g.a_stride = a_row_bytes;

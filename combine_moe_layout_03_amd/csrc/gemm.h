@@ -39,7 +39,13 @@ constexpr int kGemmStageK = select::kGemmStageK;  // bytes of k per LDS stage
 constexpr int kGemmSlotsA = 2, kGemmSlotsB = 3;    // LDS slots of a stage's A and B rows
 constexpr int kGemmXcdColGroups = 4;               // column groups of the tile order
 constexpr int kGemmXcdRows = 8;                    // row slots per XCD block
-constexpr int64_t kGemmMaxBlocks = int64_t(1) << 24;
+// A launch has fewer than 2^32 threads.
+constexpr int64_t kMaxLaunchThreads = (int64_t(1) << 32) - 1;
+// Workgroups of one launch at most.  With so few, row0 + 255 of every tile
+// stays below 2^31.
+constexpr int64_t kGemmMaxBlocks = (int64_t(1) << 23) - 1;
+static_assert(kGemmMaxBlocks * 64 * kGemmWavesM * kGemmWavesN <= kMaxLaunchThreads, "threads of a launch");
+static_assert(kGemmMaxBlocks * kGemmTileM < (int64_t(1) << 31), "rows of a launch's tiles");
 // Workgroups of one launch (row slots x column tiles), plain and fused.
 int64_t grouped_gemm_blocks(int64_t rows, int32_t groups, int32_t n);
 int64_t grouped_gemm_swiglu_blocks(int64_t rows, int32_t groups, int32_t sn);

@@ -572,21 +572,24 @@ hipError_t launch_out(const GemmDeqArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-int64_t grouped_gemm_deq_blocks(int32_t rows, int32_t groups, int32_t n) {
+bool grouped_gemm_deq_fits(int32_t rows, int32_t groups, int32_t n) {
+  constexpr int64_t kStreamBlocks = kMaxLaunchThreads / (4 * kWave);  // four waves, in one part of k or more
+  constexpr int64_t kTileBlocks = kMaxLaunchThreads / (kTileWaves * kWave);
   switch (select::gemm_deq_kind(rows, groups, n)) {
-    case select::GemmDeqKind::kSplit16: return stream_blocks(rows, groups, n, 16, 16);
-    case select::GemmDeqKind::kStream16: return stream_blocks(rows, groups, n, 16, 32);  // (64 for a short k)
-    case select::GemmDeqKind::kStream32: return stream_blocks(rows, groups, n, 32, 64);
-    case select::GemmDeqKind::kTile64: return tile_blocks(rows, groups, n, 64, 128);
-    case select::GemmDeqKind::kTile128: return tile_blocks(rows, groups, n, 128, 128);
-    case select::GemmDeqKind::kTile256: return tile_blocks(rows, groups, n, 256, 256);
+    case select::GemmDeqKind::kSplit16: return stream_blocks(rows, groups, n, 16, 16) <= kStreamBlocks;
+    case select::GemmDeqKind::kStream16:  // (64 columns for a short k)
+      return stream_blocks(rows, groups, n, 16, 32) <= kStreamBlocks;
+    case select::GemmDeqKind::kStream32: return stream_blocks(rows, groups, n, 32, 64) <= kStreamBlocks;
+    case select::GemmDeqKind::kTile64: return tile_blocks(rows, groups, n, 64, 128) <= kTileBlocks;
+    case select::GemmDeqKind::kTile128: return tile_blocks(rows, groups, n, 128, 128) <= kTileBlocks;
+    case select::GemmDeqKind::kTile256: return tile_blocks(rows, groups, n, 256, 256) <= kTileBlocks;
   }
-  return 0;
+  return false;
 }
 
 hipError_t launch_grouped_gemm_deq(GemmDeqArgs a, Out out_type, hipStream_t stream) {
   if (a.rows == 0) return hipSuccess;
-  if (grouped_gemm_deq_blocks(a.rows, a.groups, a.n) > kGemmMaxBlocks) return hipErrorInvalidValue;
+  if (!grouped_gemm_deq_fits(a.rows, a.groups, a.n)) return hipErrorInvalidValue;
   a.nt = select::gemm_deq_nt(a.rows, a.groups, a.k, a.n, out_type == Out::kF32 ? 4 : 2);
   switch (out_type) {
     case Out::kBf16: return launch_out<Out::kBf16>(a, stream);

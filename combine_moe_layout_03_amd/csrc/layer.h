@@ -50,8 +50,8 @@ struct GemmDeqArgs {
   void* out;                   // [rows][n]
   bool nt;                     // set by the launcher: the tiles' results are stored non-temporally
 };
-// Workgroups of one launch.
-int64_t grouped_gemm_deq_blocks(int32_t rows, int32_t groups, int32_t n);
+// Whether one launch holds the call's threads.
+bool grouped_gemm_deq_fits(int32_t rows, int32_t groups, int32_t n);
 hipError_t launch_grouped_gemm_deq(GemmDeqArgs a, Out out_type, hipStream_t stream);
 
 }  // namespace moe

@@ -347,7 +347,7 @@ int moe_deq_swiglu_quant(const int32_t* acc, int32_t rows, int32_t n, const floa
  *
  * Requires rows >= 0, k >= 1, n >= 1, groups >= 1, aRowBytes >= k (else
  * MOE_ERR_BAD_SHAPE); k % 16 == 0, k <= MOE_GEMM_MAX_K, n <= MOE_GEMM_MAX_N,
- * groups <= MOE_GEMM_MAX_GROUPS, and at most 2^24 workgroups in the launch
+ * groups <= MOE_GEMM_MAX_GROUPS, and fewer than 2^23 workgroups in the launch
  * (row slots ceil(rows / 256) + groups, rounded up to a multiple of 16 when
  * ceil(n / 256) % 4 == 0, times ceil(n / 256)) (else MOE_ERR_UNSUPPORTED);
  * aRowBytes a multiple of 16 (else MOE_ERR_BAD_ALIGN); outBytes as above
@@ -389,7 +389,7 @@ int moe_gemm_swiglu_quant_workspace_bytes(int32_t rows, int32_t n, size_t* bytes
  * Requires rows >= 0, k >= 1, n >= 1, groups >= 1, aRowBytes >= k,
  * tokenScaleStride a multiple of 4 and >= 4 (else MOE_ERR_BAD_SHAPE);
  * k % 16 == 0, k <= MOE_GEMM_MAX_K, n % 4 == 0, 2n <= MOE_GEMM_MAX_N, groups
- * <= MOE_GEMM_MAX_GROUPS, and at most 2^24 workgroups in the matmul launch
+ * <= MOE_GEMM_MAX_GROUPS, and fewer than 2^23 workgroups in the matmul launch
  * (moe_grouped_gemm_i8's count with ceil(n / 128) column tiles) (else
  * MOE_ERR_UNSUPPORTED); aRowBytes a multiple of 16 (else MOE_ERR_BAD_ALIGN);
  * a small out buffer gives MOE_ERR_BUFFER_TOO_SMALL, a small workspace
@@ -526,9 +526,11 @@ int moe_combine_backward_src(const void* gradOut, moe_dtype gradOutType, const v
  *            aligned to its element, outBytes >= rows * n elements.  A 16-bit
  *            out with n = hidden is the receive buffer that moe_combine reads.
  *            Rows that no expert owns are not written.
- * Requires as moe_grouped_gemm_i8, tokenScaleStride a multiple of 4 and >= 4
- * (else MOE_ERR_BAD_SHAPE); another outType gives MOE_ERR_BAD_DTYPE.  rows ==
- * 0 enqueues nothing.  One launch, no workspace. */
+ * Requires as moe_grouped_gemm_i8, but for its limit of workgroups: the launch
+ * has fewer than 2^32 threads, 256 for each tile of 16 or 32 rows or 512 for
+ * each of 64 rows or more (else MOE_ERR_UNSUPPORTED); tokenScaleStride a
+ * multiple of 4 and >= 4 (else MOE_ERR_BAD_SHAPE); another outType gives
+ * MOE_ERR_BAD_DTYPE.  rows == 0 enqueues nothing.  One launch, no workspace. */
 int moe_grouped_gemm_deq_i8(const void* a, int64_t aRowBytes, int32_t rows, int32_t k,
                             const int32_t* groupCount, int32_t groups, const void* w, int32_t n,
                             const float* weightScale, const void* tokenScale, int64_t tokenScaleStride,
