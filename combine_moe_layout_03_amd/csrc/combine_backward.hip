@@ -155,9 +155,22 @@ hipError_t launch_combine_backward(const RouteArgs& r, const void* grad_out, Out
                                    hipStream_t stream) {
   const uint8_t* recv = static_cast<const uint8_t*>(recv_x);
   uint8_t* grad = static_cast<uint8_t*>(grad_recv);
-  return recv_type == Half::kFp16
-             ? launch_rows<true>(r, grad_out, grad_type, recv, topk_w, grad, grad_weights, stream)
-             : launch_rows<false>(r, grad_out, grad_type, recv, topk_w, grad, grad_weights, stream);
+  const int64_t grad_row = static_cast<int64_t>(r.hidden) * (grad_type == Out::kF32 ? 4 : 2);
+  const int32_t tokens = select::combine_backward_launch_tokens(r.k);
+  for (int64_t first = 0; first < r.bs; first += tokens) {
+    RouteArgs part = r;
+    part.bs = static_cast<int32_t>(r.bs - first < tokens ? r.bs - first : tokens);
+    part.topk_idx += first * r.k;
+    part.send_token_idx += first * r.k;
+    const void* g = static_cast<const uint8_t*>(grad_out) + first * grad_row;
+    const float* w = topk_w + first * r.k;
+    float* gw = grad_weights + first * r.k;
+    const hipError_t e = recv_type == Half::kFp16
+                             ? launch_rows<true>(part, g, grad_type, recv, w, grad, gw, stream)
+                             : launch_rows<false>(part, g, grad_type, recv, w, grad, gw, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace moe

@@ -28,6 +28,18 @@ struct RouterArgs {
   void* grad_logits;          // row t at element t * grad_stride
   int64_t grad_stride;
 };
+// The call's tokens from `first` on, as many as one launch takes.
+inline RouterArgs router_part(RouterArgs a, Out logits_type, int32_t first) {
+  const int64_t es = logits_type == Out::kF32 ? 4 : 2, at = first;
+  a.bs = a.bs - first < select::router_launch_tokens() ? a.bs - first : select::router_launch_tokens();
+  a.logits = static_cast<const uint8_t*>(a.logits) + at * a.stride * es;
+  a.topk_idx += at * a.k;
+  if (a.topk_weights != nullptr) a.topk_weights += at * a.k;
+  if (a.token_mask != nullptr) a.token_mask += at;
+  if (a.grad_weights != nullptr) a.grad_weights += at * a.k;
+  if (a.grad_logits != nullptr) a.grad_logits = static_cast<uint8_t*>(a.grad_logits) + at * a.grad_stride * es;
+  return a;
+}
 hipError_t launch_route(const RouterArgs& a, Out logits_type, bool sigmoid, hipStream_t stream);
 hipError_t launch_route_backward(const RouterArgs& a, Out logits_type, bool sigmoid, hipStream_t stream);
 hipError_t launch_combine_backward(const RouteArgs& r, const void* grad_out, Out grad_type, const void* recv_x,

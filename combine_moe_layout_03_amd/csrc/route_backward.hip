@@ -119,7 +119,13 @@ hipError_t launch_score(const RouterArgs& a, Out type, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_route_backward(const RouterArgs& a, Out logits_type, bool sigmoid, hipStream_t stream) {
-  return sigmoid ? launch_score<true>(a, logits_type, stream) : launch_score<false>(a, logits_type, stream);
+  for (int64_t first = 0; first < a.bs; first += select::router_launch_tokens()) {
+    const RouterArgs part = router_part(a, logits_type, static_cast<int32_t>(first));
+    const hipError_t e =
+        sigmoid ? launch_score<true>(part, logits_type, stream) : launch_score<false>(part, logits_type, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace moe

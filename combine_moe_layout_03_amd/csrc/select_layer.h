@@ -98,5 +98,12 @@ constexpr RouterShape router_shape(int bs, int experts, int topk) {
   return RouterShape{0, 0};
 }
 
+// ---- tokens of one launch ------------------------------------------------------
+// A launch has fewer than 2^32 threads, and the router and the gradients give
+// up to a wave to a token or an entry; a larger batch is launched in parts.
+constexpr int32_t kLaunchWaves = int32_t(1) << 25;
+constexpr int32_t router_launch_tokens() { return kLaunchWaves; }
+constexpr int32_t combine_backward_launch_tokens(int32_t topk) { return kLaunchWaves / topk; }
+
 }  // namespace select
 }  // namespace moe

@@ -441,7 +441,8 @@ int moe_grouped_gemm_swiglu_quant_i8(const void* a, int64_t aRowBytes, int32_t r
  * groupTop 1 or 2 (else MOE_ERR_BAD_SHAPE); numExperts <= MOE_MAX_EXPERTS,
  * topk <= MOE_MAX_TOPK, numGroups <= MOE_ROUTE_MAX_GROUPS, bs * topk < 2^31
  * (else MOE_ERR_UNSUPPORTED); a known score and renormalize 0 or 1 (else
- * MOE_ERR_BAD_DTYPE).  bs == 0 enqueues nothing.  One launch, no workspace. */
+ * MOE_ERR_BAD_DTYPE).  bs == 0 enqueues nothing.  One launch up to 2^25 tokens
+ * (larger batches in parts), no workspace. */
 int moe_route(const void* logits, moe_dtype logitsType, int64_t logitsStride, int32_t bs,
               int32_t numExperts, int32_t topk, moe_score score, const float* bias, int32_t numGroups,
               int32_t topkGroups, int32_t groupTop, int renormalize, float scale,
@@ -464,7 +465,7 @@ int moe_route(const void* logits, moe_dtype logitsType, int64_t logitsStride, in
  *                   t * gradStride (gradStride >= numExperts); every element
  *                   of a row is written, computed in binary32 and rounded
  *                   once.  Must not overlap logits.
- * Limits and errors as moe_route.  One launch, no workspace. */
+ * Limits, errors and launches as moe_route. */
 int moe_route_backward(const float* gradWeights, const void* logits, moe_dtype logitsType,
                        int64_t logitsStride, const int32_t* topkIdx, int32_t bs, int32_t numExperts,
                        int32_t topk, moe_score score, int renormalize, float scale, void* gradLogits,
@@ -489,7 +490,8 @@ int moe_route_backward(const float* gradWeights, const void* logits, moe_dtype l
  *      gradWeights  device float [bs][topk].
  * The sums do not depend on scheduling.  gradRecvBytes below bs * topk rows
  * gives MOE_ERR_BUFFER_TOO_SMALL; an entry whose row falls outside either
- * buffer is skipped.  One launch, no workspace. */
+ * buffer is skipped.  One launch up to 2^25 entries (larger batches in parts),
+ * no workspace. */
 int moe_combine_backward(const void* gradOut, moe_dtype gradOutType, const void* recvX, moe_dtype recvType,
                          size_t recvXBytes, int32_t bs, int32_t hidden, int32_t topk, const int32_t* topkIdx,
                          const float* topkWeights, const int32_t* sendTokenIdx, const int32_t* putOffset,
