@@ -532,7 +532,7 @@ def moe_route(logits: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.
     """The router: logits [bs, num_experts] (bf16, fp16 or fp32, rows dense) ->
     topk_idx int32 and topk_weights float32 [bs, topk].  ``score`` is
     MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID; ``bias`` float32 [num_experts]
-    counts for the choice alone; of num_groups groups the topk_groups with the
+    counts for the choice alone (-inf or NaN: the expert is not chosen); of num_groups groups the topk_groups with the
     largest value (their best expert's, or the sum of their two best scores
     with group_top 2) keep their experts; token_mask (uint8 or bool [bs])
     takes a token out where it is 0.  Entries without an eligible expert get

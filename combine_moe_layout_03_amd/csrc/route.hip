@@ -192,12 +192,13 @@ __device__ __forceinline__ void grid_values(const RouterArgs& a, const float (&x
 #pragma unroll
   for (int i = 0; i < kVpl; ++i) {
     u[i] = __builtin_rint(__builtin_fma(u[i], share, static_cast<double>(bias[i]) * kGrid));
-    clip |= __builtin_fabsf(bias[i]) > 1000.0f;
+    clip |= !(__builtin_fabsf(bias[i]) <= 1000.0f);
   }
-  if (__any(clip)) {
+  if (__any(clip)) {  // large, infinite or NaN
     asm volatile("");  // a branch, not selects
 #pragma unroll
-    for (int i = 0; i < kVpl; ++i) u[i] = __builtin_fmin(__builtin_fmax(u[i], -kClip), kClip);
+    for (int i = 0; i < kVpl; ++i)
+      u[i] = unless(!(bias[i] > -__builtin_inff()), __builtin_fmin(__builtin_fmax(u[i], -kClip), kClip));
   }
 #pragma unroll
   for (int i = 0; i < kVpl; ++i) u[i] = unless(!(x[i] > -__builtin_inff()), u[i]);

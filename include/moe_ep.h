@@ -413,7 +413,8 @@ int moe_grouped_gemm_swiglu_quant_i8(const void* a, int64_t aRowBytes, int32_t r
  *                   or MOE_FP32), row t at element t * logitsStride
  *                   (logitsStride >= numExperts), aligned to its element.
  *      bias         device float [numExperts] or NULL: added to the scores
- *                   for the choice alone, never to the weights.  Finite.
+ *                   for the choice alone, never to the weights.  An expert
+ *                   whose bias is -inf or NaN is not chosen.
  *      tokenMask    device bytes [bs] or NULL: a token whose byte is 0 gets
  *                   no expert; what its logits hold is ignored.
  * An expert with a logit of -inf or NaN is not eligible; +inf counts as the
