@@ -4,19 +4,18 @@
 // 16 entries, batches that fill the chip that way) or of a wave; lane l holds
 // the kVpl experts from l kVpl.
 //
-// The choice is made on keys: binary64 whole numbers N 2^11 + (2047 - e),
-// where N orders the selection values of the experts -- the grid value u 2^30
-// of a biased score (|u| <= 2^10, so |N| <= 2^40, and 2^41 for a sum of two),
-// or the logit's bits mapped to a whole number of the same order -- and the
-// expert's id e below it settles ties for the lower id.  Every key is exact
-// (at most 2^52 + 2^11) and no two are equal, so one maximum (a v_max_f64 takes
-// as long as a v_max_f32 here) names value and expert at once.  A lane sorts
-// its keys; then each of k rounds takes the largest of the lanes' first keys,
-// and the lane that had it moves its list up.  Groups are ranked by the same
-// means.
+// The choice is made on keys: binary64 selection values -- score + bias, or the
+// logit itself -- whose lowest 11 bits are replaced by the expert's id, so that
+// of equal values the lower id has the larger key.  A value keeps 42 significant
+// bits whatever its size (a logit has 24), and no two keys are equal, so one
+// maximum (a v_max_f64 takes as long as a v_max_f32 here) names value and
+// expert at once.  A lane sorts its keys; then each of k rounds takes the
+// largest of the lanes' first keys, and the lane that had it moves its list up.
+// Groups are ranked by the same means.  (Values on a grid of 2^-30 lost the
+// order of scores that are all small, where binary32 scores keep it.)
 //
-// Scores for the choice are computed in binary64 (exp64 below; the error of a
-// score is below 2^-44, far below the grid), weights in binary32.
+// Scores for the choice are computed in binary64 (exp64 below), weights in
+// binary32.
 //
 // Bound by the vector ALU: some 1200 instructions for four tokens of 256
 // experts, 450 of them the sigmoids (binary64 runs at the rate of binary32
@@ -34,36 +33,39 @@ namespace {
 // Waves of a workgroup: its tokens' LDS stays within 52 KB.
 constexpr int route_waves(int lanes, int vpl) { return lanes * vpl > 512 ? 2 : 4; }
 // The value and the key of an expert that cannot be chosen: any number below
-// kNone (see unless()).
-constexpr double kNone = -1e30;
-constexpr int kIdBits = 11;
-constexpr double kIdSpan = 1 << kIdBits;
-static_assert(MOE_MAX_EXPERTS <= (1 << kIdBits) && MOE_ROUTE_MAX_GROUPS <= kWave, "ids fit below the value");
+// kNone (see unless()), which is below every logit.
+constexpr double kNone = -1e200;
+constexpr uint32_t kIdMask = 2047;  // the bits of a key that hold the id
+static_assert(MOE_MAX_EXPERTS <= kIdMask + 1 && MOE_ROUTE_MAX_GROUPS <= kWave, "ids fit below the value");
 
 // v, or if `none` a number below kNone: one select, of the upper word.
 __device__ __forceinline__ double unless(bool none, double v) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint64_t hi = none ? uint64_t(0xc7e00000) : b >> 32;  // about -2^127
+  const uint64_t hi = none ? uint64_t(0xf8300000) : b >> 32;  // about -2^900
   return __builtin_bit_cast(double, (hi << 32) | (b & 0xffffffffu));
 }
 
-__device__ __forceinline__ double make_key(double value, int id) {
-  return __builtin_fma(value, kIdSpan, static_cast<double>((1 << kIdBits) - 1 - id));  // exact
+// The id's bits count down for a positive value and up for a negative one: of
+// two keys of one value the lower id's is the larger.  `not_id` is ~id in the
+// bits of kIdMask.
+__device__ __forceinline__ double make_key(double value, uint32_t not_id) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, value);
+  const uint32_t hi = static_cast<uint32_t>(b >> 32), sign = static_cast<uint32_t>(static_cast<int32_t>(hi) >> 31);
+  uint32_t lo;  // (the compiler takes five instructions for these three)
+  asm("v_bfi_b32 %0, %1, %2, %3" : "=v"(lo) : "s"(kIdMask), "v"(not_id ^ sign), "v"(static_cast<uint32_t>(b)));
+  return __builtin_bit_cast(double, (uint64_t(hi) << 32) | lo);
 }
-// The whole number above a key's id, and the id below it (every step exact,
-// also for the sum of two values at their bound).
-__device__ __forceinline__ double key_value(double key) { return __builtin_floor(key * (1.0 / kIdSpan)); }
+// A key's value, and any value as a key holds it; a key's id.
+__device__ __forceinline__ double key_value(double key) {
+  return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, key) & ~uint64_t(kIdMask));
+}
 __device__ __forceinline__ int key_id(double key) {
-  return (1 << kIdBits) - 1 - static_cast<int>(__builtin_fma(key_value(key), -kIdSpan, key));
+  const uint64_t b = __builtin_bit_cast(uint64_t, key);
+  const uint32_t sign = static_cast<uint32_t>(static_cast<int32_t>(b >> 32) >> 31);
+  return static_cast<int>((~static_cast<uint32_t>(b) ^ sign) & kIdMask);
 }
 
-// Whole number of the same order as the (finite) logit.
-__device__ __forceinline__ double logit_value(float x) {
-  const int b = __float_as_int(x);
-  return static_cast<double>(b ^ ((b >> 31) & 0x7fffffff));
-}
-
-// e^x for |x| <= 64: x = n ln 2 + r, |r| <= ln(2) / 2, the Taylor polynomial
+// e^x for |x| <= 700: x = n ln 2 + r, |r| <= ln(2) / 2, the Taylor polynomial
 // of degree 10 (its remainder is below r^11 / 11! e^r < 2^-41 of the result),
 // times 2^n.  The coefficients are kept out of the compiler's sight: for ones
 // that it knows, each v_fmac_f64 gets two moves.
@@ -164,37 +166,35 @@ constexpr bool lane_groups(int group_size, int vpl) {
   return group_size % vpl == 0 && lanes <= 16 && (lanes & (lanes - 1)) == 0;
 }
 
-// The selection values of a lane's experts as whole numbers: `u` the grid
-// values of the scores with their bias.
+// The selection values of a lane's experts: their scores with the bias.
 template <bool kSigmoid, int kL, int kVpl>
-__device__ __forceinline__ void grid_values(const RouterArgs& a, const float (&x)[kVpl], const float (&bias)[kVpl],
-                                            float top, double (&u)[kVpl]) {
-  constexpr double kGrid = 1073741824.0, kClip = 1024.0 * kGrid;
+__device__ __forceinline__ void score_values(const float (&x)[kVpl], const float (&bias)[kVpl], float top,
+                                             double (&u)[kVpl]) {
+  constexpr double kClip = 1024.0;
   const Exp64 exp64;
-  double share = kGrid;
   if constexpr (kSigmoid) {
 #pragma unroll
     for (int i = 0; i < kVpl; ++i) {
-      const float c = __builtin_amdgcn_fmed3f(x[i], -64.0f, 64.0f);  // past that s is 0 or 1 on the grid
-      u[i] = reciprocal(1.0 + exp64(-static_cast<double>(c)));
+      // binary32 has no score below e^-104, and they are equal here
+      const float c = __builtin_amdgcn_fmed3f(x[i], -104.0f, 104.0f);
+      u[i] = reciprocal(1.0 + exp64(-static_cast<double>(c))) + static_cast<double>(bias[i]);
     }
   } else {
     double z = 0.0;
 #pragma unroll
     for (int i = 0; i < kVpl; ++i) {
-      // (below e^-64 a score is 0 on the grid, and the sum does not feel it)
-      u[i] = exp64(__builtin_fmax(static_cast<double>(x[i]) - static_cast<double>(top), -64.0));
+      // (times a share of 2^-11 or more that is still a normal number)
+      u[i] = exp64(__builtin_fmax(static_cast<double>(x[i]) - static_cast<double>(top), -690.0));
       z += x[i] > -__builtin_inff() ? u[i] : 0.0;
     }
-    share = kGrid * reciprocal(__builtin_fmax(token_sum<kL>(z), 1.0));
-  }
-  bool clip = false;
+    const double share = reciprocal(__builtin_fmax(token_sum<kL>(z), 1.0));
 #pragma unroll
-  for (int i = 0; i < kVpl; ++i) {
-    u[i] = __builtin_rint(__builtin_fma(u[i], share, static_cast<double>(bias[i]) * kGrid));
-    clip |= !(__builtin_fabsf(bias[i]) <= 1000.0f);
+    for (int i = 0; i < kVpl; ++i) u[i] = __builtin_fma(u[i], share, static_cast<double>(bias[i]));
   }
-  if (__any(clip)) {  // large, infinite or NaN
+  float size = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kVpl; ++i) size += __builtin_fabsf(bias[i]);
+  if (__any(!(size <= 1000.0f))) {  // some may be large, infinite or NaN
     asm volatile("");  // a branch, not selects
 #pragma unroll
     for (int i = 0; i < kVpl; ++i)
@@ -236,7 +236,7 @@ template <int kL, int kVpl>
 __device__ __forceinline__ bool keep_lane(const RouterArgs& a, TwoLargest best, int lane) {
   const int lanes_log2 = __builtin_ctz(a.group_size / kVpl);
   best.merge_lanes(lanes_log2);
-  double key = make_key(best.value(a.group_top), lane >> lanes_log2);
+  double key = make_key(best.value(a.group_top), ~static_cast<uint32_t>(lane >> lanes_log2));
   bool keep = false;
   for (int j = 0; j < a.keep; ++j)
     if (key == token_max<kL>(key)) keep = true, key = 2 * kNone;  // all of the group's lanes
@@ -269,7 +269,7 @@ __device__ __forceinline__ uint64_t keep_bits(const RouterArgs& a, int lane, con
       for (int m = lane & ((1 << share) - 1); m < a.group_size; m += 1 << share)
         best.add(values[value_place<kVpl>(g * a.group_size + m)]);
     if (r == 0) best.merge_lanes(share);  // more rounds are of groups with a lane each
-    key[r] = make_key(best.value(a.group_top), g);
+    key[r] = make_key(best.value(a.group_top), ~static_cast<uint32_t>(g));
   }
   uint64_t kept = 0;
   for (int j = 0; j < a.keep; ++j) {
@@ -374,12 +374,12 @@ __global__ __launch_bounds__(kWave* route_waves(kL, kVpl)) void route_kernel(Rou
     sum = token_sum<kL>(sum);
   }
 
-  double v[kVpl];  // selection values as whole numbers, then keys
+  double v[kVpl];  // selection values, then keys
   if (a.bias != nullptr) {
-    grid_values<kSigmoid, kL, kVpl>(a, x, bias, top, v);
+    score_values<kSigmoid, kL, kVpl>(x, bias, top, v);
   } else {
 #pragma unroll
-    for (int i = 0; i < kVpl; ++i) v[i] = unless(!(x[i] > -__builtin_inff()), logit_value(x[i]));
+    for (int i = 0; i < kVpl; ++i) v[i] = unless(!(x[i] > -__builtin_inff()), static_cast<double>(x[i]));
   }
   // Groups are ranked by these values, or by scores of their own.  A lane of a
   // group of whole lanes sorts its keys first and has its group's candidates
@@ -390,11 +390,13 @@ __global__ __launch_bounds__(kWave* route_waves(kL, kVpl)) void route_kernel(Rou
   if (a.groups > 1 && (own_scores || !whole_lanes)) {
     double u[kVpl];
     if (own_scores) {
-      grid_values<kSigmoid, kL, kVpl>(a, x, bias, top, u);
+      score_values<kSigmoid, kL, kVpl>(x, bias, top, u);
     } else {
 #pragma unroll
       for (int i = 0; i < kVpl; ++i) u[i] = v[i];
     }
+#pragma unroll
+    for (int i = 0; i < kVpl; ++i) u[i] = key_value(u[i]);
     if (whole_lanes) {
 #pragma unroll
       for (int i = 0; i < kVpl; ++i) best.add(u[i]);
@@ -411,9 +413,8 @@ __global__ __launch_bounds__(kWave* route_waves(kL, kVpl)) void route_kernel(Rou
       }
     }
   }
-  const double base = static_cast<double>((1 << kIdBits) - 1 - e0);
 #pragma unroll
-  for (int i = 0; i < kVpl; ++i) v[i] = __builtin_fma(v[i], kIdSpan, base) - static_cast<double>(i);
+  for (int i = 0; i < kVpl; ++i) v[i] = make_key(v[i], ~static_cast<uint32_t>(e0) ^ static_cast<uint32_t>(i));
   sort_lane<kL, kVpl>(v, a.k);
   if (whole_lanes) {
     if (!own_scores) {

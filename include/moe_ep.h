@@ -420,14 +420,18 @@ int moe_grouped_gemm_swiglu_quant_i8(const void* a, int64_t aRowBytes, int32_t r
  * An expert with a logit of -inf or NaN is not eligible; +inf counts as the
  * largest finite binary32.  Over the eligible experts of a token
  *   s_e = softmax or sigmoid of the logit x_e
- *   u_e = s_e + bias_e rounded to a multiple of 2^-30, within [-1024, 1024]
+ *   u_e = s_e + bias_e within [-1024, 1024]
  *   v_e = u_e with a bias, x_e without one (s grows with x)
  * and, with numGroups > 1, the experts in groups of numExperts / numGroups
  * consecutive ids: a group's value is its largest v (groupTop 1) or the sum
  * of its two largest u (groupTop 2; of the only one, if one is eligible), and
  * the topkGroups groups of largest value keep their experts.  Among those
  * the topk experts of largest v are chosen.  Equal values go to the lower id,
- * for groups and experts.
+ * for groups and experts.  In u the sigmoid is taken of max(x_e, -104), the
+ * softmax's e^(x_e - max x) of an exponent of -690 at least, and a u, and a sum
+ * of two, is held to 42 significant bits (the rest is cut off): values that agree
+ * in that are equal.  So bias = NULL and a bias of zeros choose alike except
+ * where scores are closer than that (sigmoids of logits past 28, say).
  * Out: topkIdx      device int32 [bs][topk]: the chosen experts, v descending;
  *                   -1 (a bad id: no row is sent) where fewer are eligible.
  *      topkWeights  device float [bs][topk]: scale * s_e, with renormalize
@@ -435,7 +439,7 @@ int moe_grouped_gemm_swiglu_quant_i8(const void* a, int64_t aRowBytes, int32_t r
  *                   is taken of scores scaled by the largest chosen one, so
  *                   it holds where the scores themselves underflow.
  * The choice is exact for these definitions up to the error of the binary64
- * scores (below 2^-44); weights are computed in binary32.
+ * scores; weights are computed in binary32.
  *
  * Requires bs >= 0, numExperts >= 1, 1 <= topkGroups <= numGroups, numGroups
  * a divisor of numExperts, 1 <= topk <= topkGroups * numExperts / numGroups,
