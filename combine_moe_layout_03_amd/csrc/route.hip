@@ -14,8 +14,9 @@
 // Groups are ranked by the same means.  (Values on a grid of 2^-30 lost the
 // order of scores that are all small, where binary32 scores keep it.)
 //
-// Scores for the choice are computed in binary64 (exp64 below), weights in
-// binary32.
+// Scores for the choice are computed in binary64, off by less than 2^-40 of
+// themselves (exp64.h: an exponential, for the softmax over a sum of such, and a
+// reciprocal); weights in binary32.
 //
 // Bound by the vector ALU: some 1200 instructions for four tokens of 256
 // experts, 450 of them the sigmoids (binary64 runs at the rate of binary32
@@ -24,6 +25,7 @@
 // in which values lie too close, was not faster (18 us: one token in 250 is
 // such, and a launch waits for its slowest wave).
 #include "device_util.h"
+#include "exp64.h"
 #include "layer.h"
 #include "router_util.h"
 
@@ -65,27 +67,20 @@ __device__ __forceinline__ int key_id(double key) {
   return static_cast<int>((~static_cast<uint32_t>(b) ^ sign) & kIdMask);
 }
 
-// e^x for |x| <= 700: x = n ln 2 + r, |r| <= ln(2) / 2, the Taylor polynomial
-// of degree 10 (its remainder is below r^11 / 11! e^r < 2^-41 of the result),
-// times 2^n.  The coefficients are kept out of the compiler's sight: for ones
+// e^x (exp64.h).  The coefficients are kept out of the compiler's sight: for ones
 // that it knows, each v_fmac_f64 gets two moves.
 struct Exp64 {
   double c[8];
-  __device__ __forceinline__ Exp64() : c{1.0 / 3628800.0, 1.0 / 362880.0, 1.0 / 40320.0, 1.0 / 5040.0,
-                                         1.0 / 720.0, 1.0 / 120.0, 1.0 / 24.0, 1.0 / 6.0} {
+  __device__ __forceinline__ Exp64() {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) asm("" : "+v"(c[i]));
+    for (int i = 0; i < 8; ++i) {
+      c[i] = kExpTerms[i];
+      asm("" : "+v"(c[i]));
+    }
   }
   __device__ __forceinline__ double operator()(double x) const {
-    const double n = __builtin_rint(x * 1.4426950408889634);
-    const double r = __builtin_fma(n, -0.6931471805599453, x);
-    double p = __builtin_fma(c[0], r, c[1]);
-#pragma unroll
-    for (int i = 2; i < 8; ++i) p = __builtin_fma(p, r, c[i]);
-    p = __builtin_fma(p, r, 0.5);
-    p = __builtin_fma(p, r, 1.0);
-    p = __builtin_fma(p, r, 1.0);
-    return __builtin_amdgcn_ldexp(p, static_cast<int>(n));
+    const double n = __builtin_rint(x * kLog2E);
+    return __builtin_amdgcn_ldexp(exp_reduced(c, x, n), static_cast<int>(n));
   }
 };
 // 1 / d for 1 <= d: the hardware's estimate (2^-24) and a Newton step.

@@ -439,7 +439,7 @@ int moe_grouped_gemm_swiglu_quant_i8(const void* a, int64_t aRowBytes, int32_t r
  *                   is taken of scores scaled by the largest chosen one, so
  *                   it holds where the scores themselves underflow.
  * The choice is exact for these definitions up to the error of the binary64
- * scores; weights are computed in binary32.
+ * scores (below 2^-40 of a score); weights are computed in binary32.
  *
  * Requires bs >= 0, numExperts >= 1, 1 <= topkGroups <= numGroups, numGroups
  * a divisor of numExperts, 1 <= topk <= topkGroups * numExperts / numGroups,
