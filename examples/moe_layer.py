@@ -28,7 +28,8 @@ import combine_moe_layout_03_amd as M  # noqa: E402
 
 class ServingLayer:
     """w1 int8 [E, 2n, h] (gate rows, then up rows) with scales [E, 2n], w2 int8 [E, h, n] with scales [E, h], gate
-    [E, h] and bias [E] of the router; up to ``tokens`` tokens a step."""
+    [E, h] and bias [E] of the router; up to ``tokens`` tokens a step, whose results stand in the first rows of
+    ``idx``, ``weights`` and ``out``."""
 
     def __init__(self, tokens, topk, w1, w1_scale, w2, w2_scale, gate, bias, groups, topk_groups, scale):
         self.w1, self.w1_scale, self.w2, self.w2_scale = w1, w1_scale, w2, w2_scale
@@ -47,20 +48,21 @@ class ServingLayer:
         self.out = torch.zeros((tokens, hidden), dtype=torch.bfloat16, device=dev)
 
     def step(self, x, token_mask=None):
-        ep = self.ep
+        ep, bs = self.ep, x.shape[0]
+        idx, weights, out = self.idx[:bs], self.weights[:bs], self.out[:bs]
         logits = x.float() @ self.gate.t()
-        M.moe_route(logits, self.idx, self.weights, M.MOE_SCORE_SIGMOID, bias=self.bias, num_groups=self.groups,
+        M.moe_route(logits, idx, weights, M.MOE_SCORE_SIGMOID, bias=self.bias, num_groups=self.groups,
                     topk_groups=self.topk_groups, group_top=2, scale=self.scale, token_mask=token_mask)
-        ep.layout_notify_dispatch(x, self.idx)
+        ep.layout_notify_dispatch(x, idx)
         scale, stride = M.token_scales_of(ep.recv_x, self.hidden)
         M.moe_grouped_gemm_swiglu_quant_i8(ep.recv_x, ep.row_bytes, self.rows, self.hidden, ep.recv_token_per_expert,
                                            self.w1, self.w1_scale, scale, self.act, self.workspace, stride)
         scale, stride = M.token_scales_of(self.act, self.n)
         M.moe_grouped_gemm_deq_i8(self.act, self.act_bytes, self.rows, self.n, ep.recv_token_per_expert, self.w2,
                                   self.w2_scale, scale, self.out_rows, stride)
-        M.moe_combine(self.out_rows, M.MOE_BF16, self.hidden, self.idx, self.weights, ep.send_token_idx, ep.put_offset,
-                      ep.recv_base, ep.epr, ep.ranks, self.out)
-        return self.out
+        M.moe_combine(self.out_rows, M.MOE_BF16, self.hidden, idx, weights, ep.send_token_idx, ep.put_offset,
+                      ep.recv_base, ep.epr, ep.ranks, out)
+        return out
 
 
 class TrainingLayer:
