@@ -68,7 +68,7 @@ __global__ __launch_bounds__(kWaves* kWave) void route_backward_kernel(RouterArg
     ds = id >= 0 ? g * (expf(xm - top) / sum) : 0.0f;
     const float dot = token_sum<kL>(ds);
 #pragma unroll
-    for (int i = 0; i < kVpl; ++i) p[i] = -(p[i] / sum) * dot;
+    for (int i = 0; i < kVpl; ++i) p[i] = p[i] > 0.0f ? -(p[i] / sum) * dot : 0.0f;  // 0 also where dot is not finite
     wave_lds_sync();
     Row::put(place, lane, p);
   } else if (a.renorm) {
