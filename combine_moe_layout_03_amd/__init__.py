@@ -649,6 +649,8 @@ def moe_grouped_gemm_deq_i8(a: torch.Tensor, a_row_bytes: int, rows: int, k: int
         raise ValueError("a must be a byte buffer")
     if rows > 0 and a.numel() < (rows - 1) * a_row_bytes + k:
         raise ValueError("a is smaller than (rows - 1) * a_row_bytes + k bytes")
+    if token_scale.dtype not in (torch.float32, torch.uint8, torch.int8) or not token_scale.is_contiguous():
+        raise ValueError("token_scale must be contiguous float32 or bytes")
     if not token_scale.is_cuda:
         raise ValueError("token_scale must be a device tensor")
     _need_scales(token_scale, rows, token_scale_stride)
