@@ -26,17 +26,6 @@ namespace {
 constexpr int kMaxWaves = 8;  // of a workgroup
 constexpr int kUnroll = 2;    // chunks in flight per lane, with a sum each
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-
-template <bool kFp16>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (kFp16) return f32_to_f16(round_f32(a)) | (f32_to_f16(round_f32(b)) << 16);
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
-}
-
 template <bool kFp16>
 __device__ __forceinline__ void widen(const u32x4& w, float (&f)[8]) {
 #pragma unroll

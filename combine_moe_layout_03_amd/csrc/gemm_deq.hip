@@ -63,24 +63,10 @@ namespace moe {
 namespace {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 #define MOE_LDS __attribute__((address_space(3)))
 
-template <Out kOut>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (kOut == Out::kFp16) return f32_to_f16(round_f32(a)) | (f32_to_f16(round_f32(b)) << 16);
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
-}
-
-// Stores at any element's address: a row of an odd n starts anywhere, and one
-// unaligned store of 16 bytes costs far less than eight stores.
-typedef f32x4 f32x4_u __attribute__((aligned(4)));
-typedef u32x2 u32x2_u __attribute__((aligned(2)));
-typedef u32x4 u32x4_u __attribute__((aligned(2)));
+// Stores below are at any element's address: one unaligned store of 16 bytes
+// costs far less than eight stores.
 
 // Where along k a workgroup begins (the sums are exact in any order).  Rows that
 // lie a multiple of 4096 bytes apart fall into few memory channels, and
@@ -100,7 +86,7 @@ __device__ __forceinline__ void store_columns(const GemmDeqArgs& a, int64_t row,
       *reinterpret_cast<f32x4_u*>(static_cast<float*>(a.out) + at) = f32x4{v[0], v[1], v[2], v[3]};
     else
       *reinterpret_cast<u32x2_u*>(static_cast<uint16_t*>(a.out) + at) =
-          u32x2{pack2<kOut>(v[0], v[1]), pack2<kOut>(v[2], v[3])};
+          u32x2{pack2<kOut == Out::kFp16>(v[0], v[1]), pack2<kOut == Out::kFp16>(v[2], v[3])};
   } else {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -524,7 +510,7 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) 
         *reinterpret_cast<f32x4*>(place(l16, c + 1)) = f32x4{v[4], v[5], v[6], v[7]};
       } else {
         *reinterpret_cast<u32x4*>(place(l16, c)) =
-            u32x4{pack2<kOut>(v[0], v[1]), pack2<kOut>(v[2], v[3]), pack2<kOut>(v[4], v[5]), pack2<kOut>(v[6], v[7])};
+            u32x4{pack2<kOut == Out::kFp16>(v[0], v[1]), pack2<kOut == Out::kFp16>(v[2], v[3]), pack2<kOut == Out::kFp16>(v[4], v[5]), pack2<kOut == Out::kFp16>(v[6], v[7])};
       }
     }
     wave_lds_sync();

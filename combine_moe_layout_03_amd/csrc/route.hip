@@ -445,30 +445,17 @@ template <bool kSigmoid, int kL, int kVpl>
 hipError_t launch_shape(const RouterArgs& a, Out type, hipStream_t stream) {
   constexpr int kWaves = route_waves(kL, kVpl), kTokens = kWave / kL * kWaves;
   const dim3 grid(static_cast<unsigned>((a.bs + kTokens - 1) / kTokens)), block(kWaves * kWave);
-  const size_t lds = a.groups > 1 && !lane_groups(a.group_size, kVpl) ? sizeof(double) * kTokens * (a.num_experts + a.num_experts / kVpl) : 0;
+  const bool through_lds = a.groups > 1 && !lane_groups(a.group_size, kVpl);
+  const size_t lds = through_lds ? sizeof(double) * kTokens * (a.num_experts + a.num_experts / kVpl) : 0;
   hipLaunchKernelGGL((route_kernel<kSigmoid, kL, kVpl>), grid, block, lds, stream, a, type);
   return hipGetLastError();
 }
 
-// One case per entry of select::kRouterShapes.
 template <bool kSigmoid>
 hipError_t launch_score(const RouterArgs& a, Out type, hipStream_t stream) {
-  const select::RouterShape s = select::router_shape(a.bs, a.num_experts, a.k);
-#define MOE_ROUTE_CASE(L, V) \
-  if (s.lanes == (L) && s.vpl == (V)) return launch_shape<kSigmoid, L, V>(a, type, stream);
-  MOE_ROUTE_CASE(16, 1)
-  MOE_ROUTE_CASE(16, 2)
-  MOE_ROUTE_CASE(16, 4)
-  MOE_ROUTE_CASE(16, 8)
-  MOE_ROUTE_CASE(16, 16)
-  MOE_ROUTE_CASE(64, 1)
-  MOE_ROUTE_CASE(64, 2)
-  MOE_ROUTE_CASE(64, 4)
-  MOE_ROUTE_CASE(64, 8)
-  MOE_ROUTE_CASE(64, 16)
-  MOE_ROUTE_CASE(64, 32)
-#undef MOE_ROUTE_CASE
-  return hipErrorInvalidValue;
+  return with_router_shape(select::router_shape(a.bs, a.num_experts, a.k), [&](auto lanes, auto vpl) {
+    return launch_shape<kSigmoid, decltype(lanes)::value, decltype(vpl)::value>(a, type, stream);
+  });
 }
 
 }  // namespace

@@ -1,13 +1,36 @@
-// Device helpers of the router and its gradient: wave reductions, logits of
-// three types, and the selection keys.
+// Helpers of the router, of the gradients and of the second expert matmul:
+// vector types and 16-bit pairs, logits of three types, reductions over a
+// token's lanes, a token's row through LDS, and the launch by the router's shape.
 #pragma once
 
 #include <float.h>
 
+#include <type_traits>
+#include <utility>
+
 #include "device_util.h"
 #include "launch.h"
+#include "select_layer.h"
 
 namespace moe {
+
+// f(lanes, vpl) with the shape as compile-time constants; one instance of f for
+// each of select::kRouterShapes.
+template <typename F, size_t... I>
+hipError_t with_router_shape(select::RouterShape s, F f, std::index_sequence<I...>) {
+  hipError_t e = hipErrorInvalidValue;
+  const auto is = [&](select::RouterShape t) { return s.lanes == t.lanes && s.vpl == t.vpl; };
+  ((is(select::kRouterShapes[I]) ? void(e = f(std::integral_constant<int, select::kRouterShapes[I].lanes>{},
+                                              std::integral_constant<int, select::kRouterShapes[I].vpl>{}))
+                                 : void()),
+   ...);
+  return e;
+}
+template <typename F>
+hipError_t with_router_shape(select::RouterShape s, F f) {
+  constexpr size_t kCount = sizeof(select::kRouterShapes) / sizeof(select::kRouterShapes[0]);
+  return with_router_shape(s, f, std::make_index_sequence<kCount>{});
+}
 
 template <Out kType>
 __device__ __forceinline__ float load_float(const void* base, int64_t i) {
@@ -106,13 +129,22 @@ __device__ __forceinline__ void wave_lds_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Rows start at any element: the vector accesses below are unaligned ones.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+// Accesses at any element's address (a row of an odd length starts anywhere).
 typedef f32x4 f32x4_u __attribute__((aligned(4)));
 typedef u32x2 u32x2_u __attribute__((aligned(2)));
 typedef u32x4 u32x4_u __attribute__((aligned(2)));
+
+// Two values rounded to 16 bits, the first in the lower half.
+template <bool kFp16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (kFp16) return f32_to_f16(round_f32(a)) | (f32_to_f16(round_f32(b)) << 16);
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
+}
 
 __device__ __forceinline__ float load_logit(const void* base, Out type, int64_t i) {
   if (type == Out::kF32) return load_float<Out::kF32>(base, i);
