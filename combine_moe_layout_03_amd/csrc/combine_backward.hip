@@ -9,11 +9,13 @@
 // gradient in y's place, so a row may be replaced in place.  A sum is a
 // lane's even and odd chunks in order, both, then the lanes: a fixed order.
 //
-// Bound by the rows' bytes: 4096 tokens x 8 entries, h 7168, bf16, 194 us for
-// 0.999 GB = 5.2 TB/s, the rate of a large copy.  (A workgroup per token that
-// takes its rows together: 211 us; row by row with g in registers: 193-204.)
-// The rows are loaded non-temporally, and stored so where they are more than
-// the Infinity Cache keeps (select_layer.h).
+// Bound by the rows' bytes: 4096 tokens x 8 entries, h 7168, bf16, 195 us for
+// 0.999 GB = 5.1 TB/s (a large copy_ of torch 5.1-5.3, its elementwise kernel
+// with one read and one write stream 6.2).  (A workgroup per token that takes its
+// rows together: 211 us; row by row with g in registers: 193-204.)  The rows are
+// loaded non-temporally, and stored so where they are more than the Infinity
+// Cache keeps (select_layer.h); that instance has a wave an entry whatever the
+// rows' length.
 #include "device_util.h"
 #include "layer.h"
 #include "router_util.h"

@@ -18,8 +18,8 @@
 // 16 columns and loads their weights straight into registers, two chunks ahead,
 // each byte once.  (A fragment load touches 16 rows at 64 bytes each; with the
 // rows' fragments loaded that way too, a decode step took 50 us instead of 44.)
-// 24 rows over 16 experts, k 2048, n 7168: 43 us = 5.5 TB/s, more than a large
-// copy reaches on this card.  Where such workgroups would leave most CUs idle, one
+// 24 rows over 16 experts, k 2048, n 7168: 43 us = 5.5 TB/s, nearly all of it
+// reads.  Where such workgroups would leave most CUs idle, one
 // takes 16 columns only and its four waves a quarter of k each (64 rows over 8
 // experts, k 4096, n 1024: 8.9 us instead of 12.4; the same split within 64
 // columns, 12.8: a CU's loads in flight are the limit there, not the chain of
@@ -38,9 +38,8 @@
 // launch's bound: an eighth each, in an order in which an XCD's L2 holds the
 // weights of 1024 columns while the rows pass.  (Dealt by the bound, XCDs with
 // empty slots idled: 16384 rows over 64 experts, k and n 2048, took 132 us
-// instead of 112.)  1000 rows over 16 experts, k 2048, n 7168: 54 us = 4.7 TB/s.
-// 32768 rows: 463 us = 2.08 POP/s, which is what a large library product
-// reaches.  A tile there takes 33 us: 3 to find its rows and load its first
+// instead of 112.)  1000 rows over 16 experts, k 2048, n 7168: 53 us = 4.7 TB/s.
+// 32768 rows: 460 us = 2.09 POP/s (a large library product: 2.12).  A tile there takes 33 us: 3 to find its rows and load its first
 // stages, 24 for 16 stages, 5 for its results.  A stage keeps the matrix cores
 // busy for 2048 cycles and LDS too (192 KB of fragments, 64 KB of loads at 128
 // bytes a cycle), 17 us of the 24 at the clock that the chip holds under this

@@ -20,10 +20,11 @@
 //
 // Bound by the vector ALU: some 1200 instructions for four tokens of 256
 // experts, 450 of them the sigmoids (binary64 runs at the rate of binary32
-// here), issued in 75 % of the cycles.  16384 tokens x 256 experts, 8 groups,
-// fp32: 13 us, where the bytes alone take 3.4.  A choice in 32 bits, with this one behind it for the waves
-// in which values lie too close, was not faster (18 us: one token in 250 is
-// such, and a launch waits for its slowest wave).
+// here), issued in 73 % of the cycles.  16384 tokens x 256 experts, 8 groups,
+// fp32: 13 us, where the bytes alone take 2.9; 160 experts in 8 groups, which
+// are not whole lanes: 17 us and 1.9.  A choice in 32 bits, with this one behind
+// it for the waves in which values lie too close, was not faster (18 us: one
+// token in 250 is such, and a launch waits for its slowest wave).
 #include "device_util.h"
 #include "exp64.h"
 #include "layer.h"
@@ -240,8 +241,8 @@ __device__ __forceinline__ bool keep_lane(const RouterArgs& a, TwoLargest best, 
 
 // Place of an expert's value: a lane's experts apart from the next lane's by
 // one, so that lanes that store together meet in few banks (16384 tokens, 160
-// experts, 8 groups: 15.1 us instead of 16.8; with fewer experts a lane the
-// places cost what the banks did).
+// experts, 8 groups: 15.1 us instead of 16.8 when this was measured, 16.5 with
+// the keys of now; with fewer experts a lane the places cost what the banks did).
 template <int kVpl>
 __device__ __forceinline__ int value_place(int e) {
   return kVpl >= 16 ? e + e / kVpl : e;

@@ -9,8 +9,9 @@
 // A token is the work of 16 lanes or of a wave, as in route.hip: lane j < k
 // works on entry j and puts its value at the expert's place in a row of LDS,
 // which the lanes cleared or, for the last formula, filled.  Bound by the bytes:
-// 16384 tokens x 256 experts, fp32, sigmoid: 5.7 us for 17 MB of gradients and
-// the lines of the chosen logits; the last formula reads all of them.
+// 16384 tokens x 256 experts, fp32, sigmoid: 5.2 us for 17 MB of gradients and
+// the lines of the chosen logits (12 MB); the last formula reads all of them (8.7
+// us, where its bytes take 5.6).
 #include "device_util.h"
 #include "layer.h"
 #include "router_util.h"

@@ -11,7 +11,8 @@ namespace select {
 
 // ---- second expert matmul: kernel and tile ----------------------------------
 // The kernel and tile of a call.  The rows an expert has on average (when all
-// have some) decide how many rows a tile takes, measured at 16 experts whose
+// have some, and the counts add up to the call's rows: the host does not know
+// less) decide how many rows a tile takes, measured at 16 experts whose
 // counts fall as rank^-1/2 (us; stream16, stream32, tile64, tile128, tile256):
 //   k 2048, n 7168, 24 rows: 44, 44, 46       k 7168, n 2048, 16 rows: 41, 42, 48
 //   64: 46, 47, 47                            128: 55, 56, 51
@@ -23,7 +24,8 @@ namespace select {
 // 1001, 7 experts, 128 workgroups of tile64 by the estimate below: 22 us with
 // tile256, 16, 11, 8.6 with stream32; 1000 rows, k 4096, n 1024, 8 experts, 152
 // of tile64: 36 with tile256, 21, 19 with tile64, 30 with stream32; 8000 such
-// rows, 140 of tile256: 44 with tile256, 53 with tile128).
+// rows, 140 of tile256: 44 with tile256, 53 with tile128).  kFewTile64 lies
+// between the first two of these, which differ in k as well.
 //
 // Where all workgroups of 16 columns fit on the chip at once (four a CU), those
 // are the fastest (split16, and the best of the others; us): 2 rows, 8 experts,
@@ -77,7 +79,8 @@ constexpr int64_t kCombineBackwardNtBytes = int64_t(96) << 20;
 constexpr bool combine_backward_nt(int64_t row_bytes) { return row_bytes > kCombineBackwardNtBytes; }
 // Short rows: 16 lanes an entry, four a wave (16 lanes and a wave, 4096 tokens, 8
 // entries, bf16, us: h 64 4.6 and 9.5, h 256 8.7, 14.2, h 512 14.4, 17.5, h 1024
-// 26.2, 26.2; 61 tokens, 5, h 1000: 3.9, 2.5).
+// 26.2, 26.2; 61 tokens, 5, h 1000: 3.9, 2.5).  Rows past kCombineBackwardNtBytes
+// take a wave all the same (8 entries, h 256, 16384 and 32768 tokens: 26, 90).
 constexpr bool combine_backward_short(int32_t hidden) { return hidden <= 512; }
 
 // ---- router and its gradient: (lanes of a token, experts of a lane) -----------
