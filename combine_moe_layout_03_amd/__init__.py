@@ -126,6 +126,7 @@ def moe_last_hip_error() -> int:
     return _lib.moe_last_hip_error()
 
 
+_SCALE_TYPES = (torch.float32, torch.uint8, torch.int8)  # token scales, or the byte buffer that they lie in
 _DTYPE = {torch.bfloat16: MOE_BF16, torch.float16: MOE_FP16, torch.float32: MOE_FP32}
 
 
@@ -649,7 +650,7 @@ def moe_grouped_gemm_deq_i8(a: torch.Tensor, a_row_bytes: int, rows: int, k: int
         raise ValueError("a must be a byte buffer")
     if rows > 0 and a.numel() < (rows - 1) * a_row_bytes + k:
         raise ValueError("a is smaller than (rows - 1) * a_row_bytes + k bytes")
-    if token_scale.dtype not in (torch.float32, torch.uint8, torch.int8) or not token_scale.is_contiguous():
+    if token_scale.dtype not in _SCALE_TYPES or not token_scale.is_contiguous():
         raise ValueError("token_scale must be contiguous float32 or bytes")
     if not token_scale.is_cuda:
         raise ValueError("token_scale must be a device tensor")

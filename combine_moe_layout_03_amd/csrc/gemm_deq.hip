@@ -508,8 +508,9 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) 
         *reinterpret_cast<f32x4*>(place(l16, c)) = f32x4{v[0], v[1], v[2], v[3]};
         *reinterpret_cast<f32x4*>(place(l16, c + 1)) = f32x4{v[4], v[5], v[6], v[7]};
       } else {
-        *reinterpret_cast<u32x4*>(place(l16, c)) =
-            u32x4{pack2<kOut == Out::kFp16>(v[0], v[1]), pack2<kOut == Out::kFp16>(v[2], v[3]), pack2<kOut == Out::kFp16>(v[4], v[5]), pack2<kOut == Out::kFp16>(v[6], v[7])};
+        constexpr bool kFp16 = kOut == Out::kFp16;
+        *reinterpret_cast<u32x4*>(place(l16, c)) = u32x4{pack2<kFp16>(v[0], v[1]), pack2<kFp16>(v[2], v[3]),
+                                                         pack2<kFp16>(v[4], v[5]), pack2<kFp16>(v[6], v[7])};
       }
     }
     wave_lds_sync();
