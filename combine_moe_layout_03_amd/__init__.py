@@ -33,9 +33,12 @@ __all__ = [
     "moe_gemm_swiglu_quant_workspace_bytes", "moe_grouped_gemm_swiglu_quant_i8",
     "MOE_NO_ALLOC_SCRATCH_BYTES", "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID", "MOE_ROUTE_MAX_GROUPS", "moe_route",
     "moe_route_backward", "moe_combine_backward", "moe_combine_backward_src", "moe_grouped_gemm_deq_i8",
+    "MOE_E4M3_BLOCKSCALE", "moe_rms_norm", "moe_rms_norm_backward_workspace_bytes", "moe_rms_norm_backward",
+    "moe_grouped_gemm_f8", "moe_gemm_swiglu_quant_f8_workspace_bytes", "moe_grouped_gemm_swiglu_quant_f8",
+    "block_scales_of",
 ]
 
-MOE_BF16, MOE_FP16, MOE_FP32, MOE_INT8_ROWSCALE = 0, 1, 2, 3
+MOE_BF16, MOE_FP16, MOE_FP32, MOE_INT8_ROWSCALE, MOE_E4M3_BLOCKSCALE = 0, 1, 2, 3, 4
 MOE_MAX_EXPERTS, MOE_MAX_HIDDEN, MOE_MAX_TOPK, MOE_MAX_SOURCES = 2048, 16384, 32, 384
 MOE_EPILOGUE_MAX_N = 4096
 MOE_GEMM_MAX_K = MOE_GEMM_MAX_N = MOE_GEMM_MAX_GROUPS = 65536
@@ -84,6 +87,14 @@ _SIGS = {
                                   _I32, _P, _SZ, _P, _P], _INT),
     "moe_grouped_gemm_deq_i8": ([_P, ctypes.c_int64, _I32, _I32, _P, _I32, _P, _I32, _P, _P, ctypes.c_int64, _P, _INT,
                                  _SZ, _P], _INT),
+    "moe_rms_norm": ([_P, _P, _INT, _P, ctypes.c_float, _I32, _I32, _P, _P, _INT, _P, _SZ, _P, _P], _INT),
+    "moe_rms_norm_backward_workspace_bytes": ([_I32, _I32, ctypes.POINTER(_SZ)], _INT),
+    "moe_rms_norm_backward": ([_P, _INT, _P, _P, _INT, _P, _P, _P, _I32, _I32, _P, _P, _P, _SZ, _P], _INT),
+    "moe_grouped_gemm_f8": ([_P, ctypes.c_int64, _I32, _I32, _P, _I32, _P, _I32, _P, _P, ctypes.c_int64, _P, _INT,
+                             _SZ, _P], _INT),
+    "moe_gemm_swiglu_quant_f8_workspace_bytes": ([_I32, _I32, ctypes.POINTER(_SZ)], _INT),
+    "moe_grouped_gemm_swiglu_quant_f8": ([_P, ctypes.c_int64, _I32, _I32, _P, _I32, _P, _I32, _P, _P, ctypes.c_int64,
+                                          _P, _SZ, _P, _SZ, _P], _INT),
     "moe_status_str": ([_INT], ctypes.c_char_p),
     "moe_last_hip_error": ([], _INT),
 }
@@ -208,6 +219,20 @@ def _need_scales(token_scale: torch.Tensor, rows: int, stride: int) -> None:
             raise ValueError(f"token_scale holds {have} bytes, rows at stride {stride} need {need}")
 
 
+def _recv_code(dtype: torch.dtype) -> int:
+    return MOE_E4M3_BLOCKSCALE if dtype is torch.float8_e4m3fn else dtype_code(dtype)
+
+
+def _row_type(x: torch.Tensor) -> Tuple[int, int, int]:
+    """(bs, hidden, type) of the rows that dispatch takes; e4m3 rows (bytes) are moved as 16-bit ones."""
+    bs, hidden = x.shape
+    if x.dtype is not torch.uint8:
+        return bs, hidden, dtype_code(x.dtype)
+    if hidden % 128:
+        raise ValueError("e4m3 rows are whole lines of 128 bytes")
+    return bs, hidden // 2, MOE_BF16
+
+
 def moe_recv_row_bytes(hidden: int, recv_type: int) -> int:
     out = _SZ(0)
     _check("moe_recv_row_bytes", _lib.moe_recv_row_bytes(hidden, recv_type, ctypes.byref(out)))
@@ -287,14 +312,16 @@ def moe_notify(token_per_expert: torch.Tensor, expert_num_per_rank: int, rank_si
 def moe_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, send_token_idx: torch.Tensor,
                  put_offset: torch.Tensor, recv_base: torch.Tensor, expert_num_per_rank: int,
                  rank_size: int, quant_int8: bool, recv_x: torch.Tensor, stream=None) -> None:
+    """x [bs, hidden] of bf16 or fp16; or e4m3 rows, uint8 [bs, row bytes] (``moe_rms_norm``'s rows; quant_int8
+    False), which are copied whole."""
     if x.dim() != 2 or topk_idx.dim() != 2:
         raise ValueError("x must be [bs, hidden] and topk_idx [bs, topk]")
-    bs, hidden = x.shape
+    bs, hidden, x_type = _row_type(x)
     topk = topk_idx.shape[1]
     _need(send_token_idx, "send_token_idx", bs * topk)
     _need_routes(expert_num_per_rank, rank_size, put_offset, recv_base)
     _check("moe_dispatch", _lib.moe_dispatch(
-        _dev(x, "x"), dtype_code(x.dtype), bs, hidden, topk,
+        _dev(x, "x"), x_type, bs, hidden, topk,
         _dev(topk_idx, "topk_idx", torch.int32), _dev(send_token_idx, "send_token_idx", torch.int32),
         _dev(put_offset, "put_offset", torch.int32), _dev(recv_base, "recv_base", torch.int32),
         expert_num_per_rank, rank_size, 1 if quant_int8 else 0, _dev(recv_x, "recv_x"),
@@ -349,12 +376,12 @@ def moe_dispatch_src(x: torch.Tensor, topk_idx: torch.Tensor, send_token_idx: to
     """Dispatch of source ``src_rank``; put_offset is [E, num_src]."""
     if x.dim() != 2 or topk_idx.dim() != 2 or put_offset.dim() != 2:
         raise ValueError("x must be [bs, hidden], topk_idx [bs, topk], put_offset [E, num_src]")
-    bs, hidden = x.shape
+    bs, hidden, x_type = _row_type(x)
     topk = topk_idx.shape[1]
     _need(send_token_idx, "send_token_idx", bs * topk)
     _need_routes(expert_num_per_rank, rank_size, put_offset, recv_base, put_offset.shape[1])
     _check("moe_dispatch_src", _lib.moe_dispatch_src(
-        _dev(x, "x"), dtype_code(x.dtype), bs, hidden, topk,
+        _dev(x, "x"), x_type, bs, hidden, topk,
         _dev(topk_idx, "topk_idx", torch.int32), _dev(send_token_idx, "send_token_idx", torch.int32),
         _dev(put_offset, "put_offset", torch.int32), _dev(recv_base, "recv_base", torch.int32),
         expert_num_per_rank, rank_size, put_offset.shape[1], src_rank, 1 if quant_int8 else 0,
@@ -386,7 +413,7 @@ def moe_fused_supported(bs: int, hidden: int, topk: int, expert_num_per_rank: in
                         x_dtype: torch.dtype, quant_int8: bool) -> bool:
     out = _INT(0)
     _check("moe_fused_supported", _lib.moe_fused_supported(
-        bs, hidden, topk, expert_num_per_rank, rank_size, dtype_code(x_dtype), 1 if quant_int8 else 0,
+        bs, hidden, topk, expert_num_per_rank, rank_size, _recv_code(x_dtype), 1 if quant_int8 else 0,
         ctypes.byref(out)))
     return bool(out.value)
 
@@ -400,7 +427,7 @@ def moe_layout_notify_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, expert_n
                                workspace: torch.Tensor, stream=None) -> None:
     if x.dim() != 2 or topk_idx.dim() != 2:
         raise ValueError("x must be [bs, hidden] and topk_idx [bs, topk]")
-    bs, hidden = x.shape
+    bs, hidden, x_type = _row_type(x)
     topk = topk_idx.shape[1]
     _need_layout(bs, topk, expert_num_per_rank, rank_size, token_per_expert, token_per_rank, send_token_idx,
                  bad_id_count)
@@ -411,7 +438,7 @@ def moe_layout_notify_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, expert_n
     _need_routes(expert_num_per_rank, rank_size, put_offset, recv_base)
     i32 = torch.int32
     _check("moe_layout_notify_dispatch", _lib.moe_layout_notify_dispatch(
-        _dev(x, "x"), dtype_code(x.dtype), bs, hidden, topk, _dev(topk_idx, "topk_idx", i32),
+        _dev(x, "x"), x_type, bs, hidden, topk, _dev(topk_idx, "topk_idx", i32),
         expert_num_per_rank, rank_size, 1 if quant_int8 else 0,
         _dev(token_per_expert, "token_per_expert", i32), _dev(token_per_rank, "token_per_rank", i32),
         _dev(send_token_idx, "send_token_idx", i32), _dev(bad_id_count, "bad_id_count", i32, optional=True),
@@ -661,6 +688,158 @@ def moe_grouped_gemm_deq_i8(a: torch.Tensor, a_row_bytes: int, rows: int, k: int
         _dev(out, "out"), dtype_code(out.dtype), out.nbytes, _stream(stream)))
 
 
+def _row_matrix(t: torch.Tensor, name: str, shape, dtype=None):
+    """The device pointer of an optional matrix of ``shape``."""
+    if t is None:
+        return None
+    p = _dev(t, name, dtype)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be [bs, hidden]")
+    return p
+
+
+def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+                 sum: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                 rows: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Root-mean-square norm: s = x + residual (x [bs, hidden] of bf16, fp16 or
+    fp32, residual and sum of the same type; s is written to ``sum``, which may
+    be x or residual), then (s / sqrt(mean(s^2) + eps)) * weight (float32
+    [hidden]), to ``out`` [bs, hidden] of any of the three types and to
+    ``rows``, a uint8 buffer of bs e4m3 rows (moe_recv_row_bytes(hidden,
+    MOE_E4M3_BLOCKSCALE) bytes each, a scale for each 128 columns).  rstd
+    float32 [bs] gets 1 / sqrt(...), for ``moe_rms_norm_backward``."""
+    px = _dev(x, "x")
+    shape, dtype = x.shape, x.dtype
+    if len(shape) != 2:
+        raise ValueError("x must be [bs, hidden]")
+    bs, hidden = shape
+    if weight.numel() != hidden:
+        raise ValueError("weight must hold hidden floats")
+    _need(rstd, "rstd", bs)
+    _check("moe_rms_norm", _lib.moe_rms_norm(
+        px, _row_matrix(residual, "residual", shape, dtype), dtype_code(dtype), _dev(weight, "weight", torch.float32),
+        eps, bs, hidden, _row_matrix(sum, "sum", shape, dtype), _row_matrix(out, "out", shape),
+        0 if out is None else dtype_code(out.dtype), _dev(rows, "rows", torch.uint8, optional=True),
+        0 if rows is None else rows.nbytes, _dev(rstd, "rstd", torch.float32, optional=True), _stream(stream)))
+
+
+def moe_rms_norm_backward_workspace_bytes(bs: int, hidden: int) -> int:
+    out = _SZ(0)
+    _check("moe_rms_norm_backward_workspace_bytes",
+           _lib.moe_rms_norm_backward_workspace_bytes(bs, hidden, ctypes.byref(out)))
+    return out.value
+
+
+def moe_rms_norm_backward(grad_out: torch.Tensor, sum: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                          grad_x: torch.Tensor, grad_sum: Optional[torch.Tensor] = None,
+                          grad_weight: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                          token_mask: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The norm's gradient: grad_out [bs, hidden] (bf16, fp16 or fp32) and sum,
+    weight and rstd as ``moe_rms_norm`` gave and had them -> grad_x of sum's
+    type (of x and of the residual alike; grad_sum, the gradient that reaches
+    the sum past the norm, is added) and grad_weight float32 [hidden], which
+    needs a workspace of moe_rms_norm_backward_workspace_bytes(bs, hidden)
+    bytes.  token_mask (uint8 or bool [bs]) takes a token out where it is 0."""
+    pg = _dev(grad_out, "grad_out")
+    shape, dtype = sum.shape, sum.dtype
+    if len(shape) != 2 or grad_out.shape != shape:
+        raise ValueError("grad_out and sum must be [bs, hidden]")
+    bs, hidden = shape
+    if weight.numel() != hidden:
+        raise ValueError("weight must hold hidden floats")
+    _need(rstd, "rstd", bs)
+    if grad_weight is not None and grad_weight.numel() != hidden:
+        raise ValueError("grad_weight must hold hidden floats")
+    if token_mask is not None:
+        _need(token_mask, "token_mask", bs)
+        if token_mask.dtype is not torch.uint8 and token_mask.dtype is not torch.bool:
+            raise ValueError("token_mask must be uint8 or bool")
+    if grad_x is None:
+        raise ValueError("grad_x is required")
+    _check("moe_rms_norm_backward", _lib.moe_rms_norm_backward(
+        pg, dtype_code(grad_out.dtype), _row_matrix(grad_sum, "grad_sum", shape, dtype), _dev(sum, "sum"),
+        dtype_code(dtype), _dev(weight, "weight", torch.float32), _dev(rstd, "rstd", torch.float32),
+        _dev(token_mask, "token_mask", optional=True), bs, hidden, _row_matrix(grad_x, "grad_x", shape, dtype),
+        _dev(grad_weight, "grad_weight", torch.float32, optional=True), _dev(workspace, "workspace", optional=True),
+        0 if workspace is None else workspace.nbytes, _stream(stream)))
+
+
+_CODE_TYPES = (torch.float8_e4m3fn, torch.uint8, torch.int8)  # e4m3 codes, or the bytes that hold them
+
+
+def _gemm_f8_sizes(a, a_row_bytes, rows, k, group_count, w, weight_scale, token_scale, token_scale_stride, halves):
+    shape = w.shape
+    if len(shape) != 3 or shape[2] != k or w.dtype not in _CODE_TYPES or shape[1] % halves:
+        raise ValueError("w must be e4m3 [groups, n, k]" if halves == 1 else "w must be e4m3 [groups, 2n, k]")
+    groups, n = shape[0], shape[1] // halves
+    if group_count.numel() != groups:
+        raise ValueError("group_count must hold one count per group")
+    blocks = (k + 127) // 128
+    if weight_scale.numel() != groups * halves * ((n + 127) // 128) * blocks:
+        raise ValueError("weight_scale must hold a float for each 128 x 128 of each expert's weights")
+    if a.dtype not in _CODE_TYPES:
+        raise ValueError("a must be a byte buffer")
+    if rows > 0 and a.numel() < (rows - 1) * a_row_bytes + k:
+        raise ValueError("a is smaller than (rows - 1) * a_row_bytes + k bytes")
+    if token_scale.dtype not in _SCALE_TYPES or not token_scale.is_contiguous():
+        raise ValueError("token_scale must be contiguous float32 or bytes")
+    if not token_scale.is_cuda:
+        raise ValueError("token_scale must be a device tensor")
+    if rows > 0 and token_scale.nbytes < (rows - 1) * token_scale_stride + 4 * blocks:
+        raise ValueError(f"token_scale holds {token_scale.nbytes} bytes, rows at stride {token_scale_stride} need "
+                         f"{(rows - 1) * token_scale_stride + 4 * blocks}")
+    return groups, n
+
+
+def moe_grouped_gemm_f8(a: torch.Tensor, a_row_bytes: int, rows: int, k: int, group_count: torch.Tensor,
+                        w: torch.Tensor, weight_scale: torch.Tensor, token_scale: torch.Tensor, out: torch.Tensor,
+                        token_scale_stride: Optional[int] = None, stream=None) -> None:
+    """Expert product in 8-bit floats: ``a`` is a device byte buffer whose row m
+    starts at byte m * a_row_bytes and holds k e4m3 codes; group_count int32
+    [groups] (device) gives each expert's rows in order; w e4m3 [groups, n, k];
+    weight_scale float32 [groups, ceil(n / 128), ceil(k / 128)]; the scales of
+    row m, a float for each 128 of k, are read from byte m * token_scale_stride
+    of ``token_scale`` on (float32 [rows, ceil(k / 128)], the default stride, or
+    e4m3 rows at their scales' byte, see ``block_scales_of``); out [rows, n] of
+    bf16, fp16 or fp32 (rows of no expert are not written)."""
+    if token_scale_stride is None:
+        token_scale_stride = (k + 127) // 128 * 4
+    groups, n = _gemm_f8_sizes(a, a_row_bytes, rows, k, group_count, w, weight_scale, token_scale, token_scale_stride,
+                               1)
+    _check("moe_grouped_gemm_f8", _lib.moe_grouped_gemm_f8(
+        _dev(a, "a"), a_row_bytes, rows, k, _dev(group_count, "group_count", torch.int32), groups, _dev(w, "w"), n,
+        _dev(weight_scale, "weight_scale", torch.float32), token_scale.data_ptr(), token_scale_stride,
+        _dev(out, "out"), dtype_code(out.dtype), out.nbytes, _stream(stream)))
+
+
+def moe_gemm_swiglu_quant_f8_workspace_bytes(rows: int, n: int) -> int:
+    out = _SZ(0)
+    _check("moe_gemm_swiglu_quant_f8_workspace_bytes",
+           _lib.moe_gemm_swiglu_quant_f8_workspace_bytes(rows, n, ctypes.byref(out)))
+    return out.value
+
+
+def moe_grouped_gemm_swiglu_quant_f8(a: torch.Tensor, a_row_bytes: int, rows: int, k: int, group_count: torch.Tensor,
+                                     w: torch.Tensor, weight_scale: torch.Tensor, token_scale: torch.Tensor,
+                                     out: torch.Tensor, workspace: Optional[torch.Tensor] = None,
+                                     token_scale_stride: Optional[int] = None, stream=None) -> None:
+    """The first expert product in 8-bit floats with its gate: arguments as
+    ``moe_grouped_gemm_f8``, but w e4m3 [groups, 2n, k] (gate rows, then up
+    rows), weight_scale float32 [groups, 2 * ceil(n / 128), ceil(k / 128)], out
+    a uint8 buffer of e4m3 rows (moe_recv_row_bytes(n, MOE_E4M3_BLOCKSCALE)
+    bytes each; rows of no expert are not written), and workspace a device
+    buffer of moe_gemm_swiglu_quant_f8_workspace_bytes(rows, n) bytes."""
+    if token_scale_stride is None:
+        token_scale_stride = (k + 127) // 128 * 4
+    groups, n = _gemm_f8_sizes(a, a_row_bytes, rows, k, group_count, w, weight_scale, token_scale, token_scale_stride,
+                               2)
+    _check("moe_grouped_gemm_swiglu_quant_f8", _lib.moe_grouped_gemm_swiglu_quant_f8(
+        _dev(a, "a"), a_row_bytes, rows, k, _dev(group_count, "group_count", torch.int32), groups, _dev(w, "w"), n,
+        _dev(weight_scale, "weight_scale", torch.float32), token_scale.data_ptr(), token_scale_stride,
+        _dev(out, "out"), out.nbytes, _dev(workspace, "workspace", optional=True),
+        0 if workspace is None else workspace.nbytes, _stream(stream)))
+
+
 def token_scales_of(recv_x: torch.Tensor, hidden: int) -> Tuple[torch.Tensor, int]:
     """(base tensor view, byte stride) that addresses the inverse scales of an
     int8 receive buffer in place, for ``moe_deq_swiglu_quant``."""
@@ -669,11 +848,23 @@ def token_scales_of(recv_x: torch.Tensor, hidden: int) -> Tuple[torch.Tensor, in
     return recv_x[off:], rb
 
 
+def block_scales_of(rows: torch.Tensor, width: int) -> Tuple[torch.Tensor, int]:
+    """(base tensor view, byte stride) that addresses the scales of a buffer of
+    e4m3 rows in place, for the 8-bit float products."""
+    return rows.view(-1)[(width + 31) // 32 * 32:], moe_recv_row_bytes(width, MOE_E4M3_BLOCKSCALE)
+
+
+def _out_dtype(x_dtype: torch.dtype) -> torch.dtype:
+    return torch.bfloat16 if x_dtype is torch.float8_e4m3fn else x_dtype
+
+
 class EpBuffers:
     """Device buffers of one pipeline shape, allocated once through torch.
 
     ``run`` enqueues layout -> notify -> dispatch -> combine on the current
-    stream and allocates nothing."""
+    stream and allocates nothing.  With x_dtype float8_e4m3fn (quant_int8
+    False) the receive buffer holds e4m3 rows, for the expert products;
+    combine reads what they make, not this buffer."""
 
     def __init__(self, bs: int, hidden: int, topk: int, expert_num_per_rank: int, rank_size: int,
                  x_dtype: torch.dtype = torch.bfloat16, quant_int8: bool = True,
@@ -683,7 +874,7 @@ class EpBuffers:
         self.epr, self.ranks, self.num_experts = expert_num_per_rank, rank_size, e
         self.quant_int8 = quant_int8
         self.x_dtype = x_dtype
-        self.recv_type = MOE_INT8_ROWSCALE if quant_int8 else dtype_code(x_dtype)
+        self.recv_type = MOE_INT8_ROWSCALE if quant_int8 else _recv_code(x_dtype)
         self.row_bytes = moe_recv_row_bytes(hidden, self.recv_type)
         i32 = dict(dtype=torch.int32, device=device)
         self.token_per_expert = torch.zeros(e, **i32)
@@ -697,7 +888,7 @@ class EpBuffers:
         self.recv_base = torch.zeros(rank_size, **i32)
         self.recv_token_per_expert = torch.zeros(e, **i32)
         self.recv_x = torch.zeros(bs * topk * self.row_bytes, dtype=torch.uint8, device=device)
-        self.out = torch.zeros((bs, hidden), dtype=out_dtype or x_dtype, device=device)
+        self.out = torch.zeros((bs, hidden), dtype=out_dtype or _out_dtype(x_dtype), device=device)
 
     def layout(self, topk_idx, stream=None):
         moe_layout(topk_idx, self.epr, self.ranks, self.token_per_expert, self.token_per_rank,
@@ -753,7 +944,7 @@ class EpMultiBuffers:
         self.num_src = len(sizes)
         self.epr, self.ranks, self.num_experts = expert_num_per_rank, rank_size, e
         self.quant_int8 = quant_int8
-        self.recv_type = MOE_INT8_ROWSCALE if quant_int8 else dtype_code(x_dtype)
+        self.recv_type = MOE_INT8_ROWSCALE if quant_int8 else _recv_code(x_dtype)
         self.row_bytes = moe_recv_row_bytes(hidden, self.recv_type)
         i32 = dict(dtype=torch.int32, device=device)
         self.token_per_expert = torch.zeros((self.num_src, e), **i32)
@@ -770,7 +961,7 @@ class EpMultiBuffers:
         self.recv_token_per_expert = torch.zeros(e, **i32)
         self.total_rows = sum(sizes) * topk
         self.recv_x = torch.zeros(self.total_rows * self.row_bytes, dtype=torch.uint8, device=device)
-        self.out = [torch.zeros((b, hidden), dtype=out_dtype or x_dtype, device=device) for b in sizes]
+        self.out = [torch.zeros((b, hidden), dtype=out_dtype or _out_dtype(x_dtype), device=device) for b in sizes]
 
     def layout(self, src: int, topk_idx, stream=None):
         moe_layout(topk_idx, self.epr, self.ranks, self.token_per_expert[src], self.token_per_rank[src],

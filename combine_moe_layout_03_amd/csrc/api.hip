@@ -7,9 +7,12 @@
 #include <atomic>
 #include <limits>
 
+#include "block_rows.h"
 #include "launch.h"
 #include "gemm.h"
+#include "gemm_f8.h"
 #include "layer.h"
+#include "norm.h"
 #include "moe_ep.h"
 
 namespace {
@@ -56,6 +59,12 @@ size_t align32(int64_t v) { return static_cast<size_t>((v + 31) / 32 * 32); }
 constexpr size_t kRecvLine = 128;
 size_t int8_row_bytes(int64_t hidden) { return (align32(hidden) + 32u + kRecvLine - 1) / kRecvLine * kRecvLine; }
 
+// An e4m3 row: h codes, the blocks' scales from byte align32(h) on, whole lines.
+size_t e4m3_row_bytes(int32_t hidden) {
+  const size_t scales = 4u * static_cast<size_t>((static_cast<int64_t>(hidden) + moe::kF8Block - 1) / moe::kF8Block);
+  return (align32(hidden) + scales + kRecvLine - 1) / kRecvLine * kRecvLine;
+}
+
 // Shared checks on the routing scalars.
 int check_experts(int32_t epr, int32_t ranks) {
   if (epr < 1 || ranks < 1) return MOE_ERR_BAD_SHAPE;
@@ -86,9 +95,23 @@ int row_bytes(int32_t hidden, moe_dtype recv, size_t* bytes) {
     case MOE_INT8_ROWSCALE:
       *bytes = int8_row_bytes(hidden);
       return MOE_OK;
+    case MOE_E4M3_BLOCKSCALE:
+      *bytes = e4m3_row_bytes(hidden);
+      return MOE_OK;
     default:
       return MOE_ERR_BAD_DTYPE;
   }
+}
+
+// e4m3 rows are moved as they are, as 16-bit rows of half their bytes.
+int as_16_bit_rows(int quant_int8, moe_dtype* type, int32_t* hidden) {
+  if (*type != MOE_E4M3_BLOCKSCALE) return MOE_OK;
+  if (quant_int8) return MOE_ERR_BAD_DTYPE;
+  if (*hidden < 1) return MOE_ERR_BAD_SHAPE;
+  if (*hidden % 16 != 0 || *hidden > MOE_MAX_HIDDEN) return MOE_ERR_UNSUPPORTED;
+  *type = MOE_BF16;
+  *hidden = static_cast<int32_t>(e4m3_row_bytes(*hidden) / 2);
+  return MOE_OK;
 }
 
 // Source count and index of a multi-source call.
@@ -242,12 +265,14 @@ int moe_dispatch_src(const void* x, moe_dtype x_type, int32_t bs, int32_t hidden
                      const int32_t* topk_idx, const int32_t* send_token_idx, const int32_t* put_offset,
                      const int32_t* recv_base, int32_t epr, int32_t ranks, int32_t num_src,
                      int32_t src_rank, int quant_int8, void* recv_x, size_t recv_x_bytes, void* stream) {
+  int st = as_16_bit_rows(quant_int8, &x_type, &hidden);
+  if (st) return st;
   if (x_type != MOE_BF16 && x_type != MOE_FP16) return MOE_ERR_BAD_DTYPE;
   if (quant_int8 != 0 && quant_int8 != 1) return MOE_ERR_BAD_DTYPE;
   const moe_dtype recv_type = quant_int8 ? MOE_INT8_ROWSCALE : x_type;
   moe::RouteArgs r{};
-  int st = make_route(bs, hidden, topk, topk_idx, send_token_idx, put_offset, recv_base, epr, ranks,
-                      num_src, src_rank, recv_type, recv_x_bytes, &r);
+  st = make_route(bs, hidden, topk, topk_idx, send_token_idx, put_offset, recv_base, epr, ranks,
+                  num_src, src_rank, recv_type, recv_x_bytes, &r);
   if (st) return st;
   if (bs == 0) return MOE_OK;
   if (!x || !recv_x) return MOE_ERR_NULL_PTR;
@@ -320,8 +345,9 @@ int fused_grid(int32_t bs, int32_t topk, int32_t num_experts, int cus, int32_t* 
 int moe_fused_supported(int32_t bs, int32_t hidden, int32_t topk, int32_t expert_num_per_rank, int32_t ranks,
                         moe_dtype x_type, int quant_int8, int* supported) {
   if (!supported) return MOE_ERR_NULL_PTR;
-  int st = check_tokens(bs, topk);
+  int st = as_16_bit_rows(quant_int8, &x_type, &hidden);
   if (st) return st;
+  if ((st = check_tokens(bs, topk))) return st;
   if ((st = check_experts(expert_num_per_rank, ranks))) return st;
   if ((st = check_hidden(hidden))) return st;
   if (x_type != MOE_BF16 && x_type != MOE_FP16) return MOE_ERR_BAD_DTYPE;
@@ -336,11 +362,12 @@ int moe_layout_notify_dispatch(const void* x, moe_dtype x_type, int32_t bs, int3
                                int32_t* bad_id_count, int32_t* put_offset, int32_t* recv_count,
                                int32_t* recv_base, int32_t* recv_token_per_expert, void* recv_x,
                                size_t recv_x_bytes, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = as_16_bit_rows(quant_int8, &x_type, &hidden);
+  if (st) return st;
   if (x_type != MOE_BF16 && x_type != MOE_FP16) return MOE_ERR_BAD_DTYPE;
   if (quant_int8 != 0 && quant_int8 != 1) return MOE_ERR_BAD_DTYPE;
   const moe_dtype recv_type = quant_int8 ? MOE_INT8_ROWSCALE : x_type;
-  int st = check_tokens(bs, topk);
-  if (st) return st;
+  if ((st = check_tokens(bs, topk))) return st;
   if ((st = check_experts(epr, ranks))) return st;
   if ((st = check_hidden(hidden))) return st;
   if (!token_per_expert || !token_per_rank || !put_offset || !recv_count || !recv_base ||
@@ -538,6 +565,7 @@ moe::Out float_type(moe_dtype t) {
   return t == MOE_FP32 ? moe::Out::kF32 : t == MOE_FP16 ? moe::Out::kFp16 : moe::Out::kBf16;
 }
 size_t float_bytes(moe_dtype t) { return t == MOE_FP32 ? 4 : 2; }
+bool is_float(moe_dtype t) { return t == MOE_BF16 || t == MOE_FP16 || t == MOE_FP32; }
 
 }  // namespace
 
@@ -672,6 +700,166 @@ int moe_grouped_gemm_deq_i8(const void* a, int64_t a_row_bytes, int32_t rows, in
   g.ts_stride = token_scale_stride;
   g.out = out;
   return hip_status(moe::launch_grouped_gemm_deq(g, float_type(out_type), static_cast<hipStream_t>(stream)));
+}
+
+int moe_rms_norm(const void* x, const void* residual, moe_dtype type, const float* weight, float eps, int32_t bs,
+                 int32_t hidden, void* sum, void* out, moe_dtype out_type, void* rows, size_t rows_bytes, float* rstd,
+                 void* stream) {
+  if (bs < 0) return MOE_ERR_BAD_SHAPE;
+  int st = check_hidden(hidden);
+  if (st) return st;
+  if (rows && hidden % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  if (!is_float(type) || (out && !is_float(out_type))) return MOE_ERR_BAD_DTYPE;
+  if (!(eps >= 0.0f)) return MOE_ERR_BAD_SHAPE;
+  if (bs == 0) return MOE_OK;
+  if (!x || !weight || (!out && !rows)) return MOE_ERR_NULL_PTR;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 4) || !aligned(sum, 16) || !aligned(out, 16) ||
+      !aligned(rows, 16) || !aligned(rstd, 4))
+    return MOE_ERR_BAD_ALIGN;
+  const size_t rb = e4m3_row_bytes(hidden);
+  if (rows && rows_bytes / rb < static_cast<size_t>(bs)) return MOE_ERR_BUFFER_TOO_SMALL;
+  moe::NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.weight = weight;
+  a.eps = eps;
+  a.bs = bs;
+  a.hidden = hidden;
+  a.sum = sum;
+  a.out = out;
+  a.out_type = float_type(out_type);
+  a.rows = static_cast<uint8_t*>(rows);
+  a.row_bytes = static_cast<int64_t>(rb);
+  a.scale_off = static_cast<int32_t>(align32(hidden));
+  a.rstd = rstd;
+  return hip_status(moe::launch_rms_norm(a, float_type(type), static_cast<hipStream_t>(stream)));
+}
+
+int moe_rms_norm_backward_workspace_bytes(int32_t bs, int32_t hidden, size_t* bytes) {
+  if (!bytes) return MOE_ERR_NULL_PTR;
+  if (bs < 0) return MOE_ERR_BAD_SHAPE;
+  int st = check_hidden(hidden);
+  if (st) return st;
+  *bytes = static_cast<size_t>(moe::select::norm_backward_parts(bs)) * static_cast<size_t>(hidden) * 4u;
+  return MOE_OK;
+}
+
+int moe_rms_norm_backward(const void* grad_out, moe_dtype grad_out_type, const void* grad_sum, const void* sum,
+                          moe_dtype type, const float* weight, const float* rstd, const uint8_t* token_mask,
+                          int32_t bs, int32_t hidden, void* grad_x, float* grad_weight, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  int st = moe_rms_norm_backward_workspace_bytes(bs, hidden, &need);
+  if (st) return st;
+  if (!is_float(type) || !is_float(grad_out_type)) return MOE_ERR_BAD_DTYPE;
+  if (!grad_weight && bs == 0) return MOE_OK;
+  if (bs > 0 && (!grad_out || !sum || !weight || !rstd || !grad_x)) return MOE_ERR_NULL_PTR;
+  if (grad_weight && need > 0 && !workspace) return MOE_ERR_NULL_PTR;
+  if (!aligned(grad_out, 16) || !aligned(grad_sum, 16) || !aligned(sum, 16) || !aligned(weight, 4) ||
+      !aligned(rstd, 4) || !aligned(grad_x, 16) || !aligned(grad_weight, 4) || !aligned(workspace, 16))
+    return MOE_ERR_BAD_ALIGN;
+  if (grad_weight && workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  moe::NormBackwardArgs a{};
+  a.grad_out = grad_out;
+  a.grad_sum = grad_sum;
+  a.sum = sum;
+  a.weight = weight;
+  a.rstd = rstd;
+  a.token_mask = token_mask;
+  a.bs = bs;
+  a.hidden = hidden;
+  a.grad_x = grad_x;
+  a.grad_weight = grad_weight;
+  a.partial = static_cast<float*>(workspace);
+  return hip_status(moe::launch_rms_norm_backward(a, float_type(type), float_type(grad_out_type),
+                                                  static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
+// Checks and arguments that the two 8-bit float products share.
+int make_gemm_f8(const void* a, int64_t a_row_bytes, int32_t rows, int32_t k, const int32_t* group_count,
+                 int32_t groups, const void* w, int32_t n, const float* weight_scale, const void* token_scale,
+                 int64_t token_scale_stride, const void* out, moe::GemmF8Args* g) {
+  if (!a || !group_count || !w || !weight_scale || !token_scale || !out) return MOE_ERR_NULL_PTR;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(group_count, 4) || !aligned(weight_scale, 4) ||
+      !aligned(token_scale, 4))
+    return MOE_ERR_BAD_ALIGN;
+  g->a = static_cast<const uint8_t*>(a);
+  g->a_stride = a_row_bytes;
+  g->rows = rows;
+  g->k = k;
+  g->group_count = group_count;
+  g->groups = groups;
+  g->w = static_cast<const uint8_t*>(w);
+  g->n = n;
+  g->weight_scale = weight_scale;
+  g->token_scale = static_cast<const uint8_t*>(token_scale);
+  g->ts_stride = token_scale_stride;
+  return MOE_OK;
+}
+int check_gemm_f8(int64_t a_row_bytes, int32_t rows, int32_t k, int32_t groups, int32_t n, int32_t max_n,
+                  int64_t token_scale_stride) {
+  if (rows < 0 || k < 1 || n < 1 || groups < 1 || a_row_bytes < k || token_scale_stride % 4 != 0) return MOE_ERR_BAD_SHAPE;
+  if (k % 16 != 0 || k > MOE_GEMM_MAX_K || n > max_n || groups > MOE_GEMM_MAX_GROUPS) return MOE_ERR_UNSUPPORTED;
+  if (token_scale_stride / 4 < moe::f8_blocks(k)) return MOE_ERR_BAD_SHAPE;
+  if (a_row_bytes % 16 != 0) return MOE_ERR_BAD_ALIGN;
+  return MOE_OK;
+}
+
+}  // namespace
+
+int moe_grouped_gemm_f8(const void* a, int64_t a_row_bytes, int32_t rows, int32_t k, const int32_t* group_count,
+                        int32_t groups, const void* w, int32_t n, const float* weight_scale, const void* token_scale,
+                        int64_t token_scale_stride, void* out, moe_dtype out_type, size_t out_bytes, void* stream) {
+  int st = check_gemm_f8(a_row_bytes, rows, k, groups, n, MOE_GEMM_MAX_N, token_scale_stride);
+  if (st) return st;
+  if (!is_float(out_type)) return MOE_ERR_BAD_DTYPE;
+  if (rows == 0) return MOE_OK;
+  moe::GemmF8Args g{};
+  if ((st = make_gemm_f8(a, a_row_bytes, rows, k, group_count, groups, w, n, weight_scale, token_scale,
+                         token_scale_stride, out, &g)))
+    return st;
+  const size_t es = float_bytes(out_type);
+  if (!aligned(out, es)) return MOE_ERR_BAD_ALIGN;
+  if (out_bytes / es / static_cast<size_t>(n) < static_cast<size_t>(rows)) return MOE_ERR_BUFFER_TOO_SMALL;
+  if (!moe::grouped_gemm_f8_fits(rows, groups, n, false)) return MOE_ERR_UNSUPPORTED;
+  g.out = out;
+  return hip_status(moe::launch_grouped_gemm_f8(g, float_type(out_type), static_cast<hipStream_t>(stream)));
+}
+
+int moe_gemm_swiglu_quant_f8_workspace_bytes(int32_t rows, int32_t n, size_t* bytes) {
+  if (!bytes) return MOE_ERR_NULL_PTR;
+  if (rows < 0 || n < 1) return MOE_ERR_BAD_SHAPE;
+  *bytes = 0;
+  return MOE_OK;
+}
+
+int moe_grouped_gemm_swiglu_quant_f8(const void* a, int64_t a_row_bytes, int32_t rows, int32_t k,
+                                     const int32_t* group_count, int32_t groups, const void* w, int32_t n,
+                                     const float* weight_scale, const void* token_scale, int64_t token_scale_stride,
+                                     void* out, size_t out_bytes, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  int st = check_gemm_f8(a_row_bytes, rows, k, groups, n, MOE_GEMM_MAX_N / 2, token_scale_stride);
+  if (st) return st;
+  if (n % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  moe::GemmF8Args g{};
+  if ((st = make_gemm_f8(a, a_row_bytes, rows, k, group_count, groups, w, n, weight_scale, token_scale,
+                         token_scale_stride, out, &g)))
+    return st;
+  if (!aligned(out, 16) || !aligned(workspace, 16)) return MOE_ERR_BAD_ALIGN;
+  const size_t rb = e4m3_row_bytes(n);
+  if (out_bytes / rb < static_cast<size_t>(rows)) return MOE_ERR_BUFFER_TOO_SMALL;
+  size_t need = 0;
+  if ((st = moe_gemm_swiglu_quant_f8_workspace_bytes(rows, n, &need))) return st;
+  if (need > 0 && !workspace) return MOE_ERR_NULL_PTR;
+  if (workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!moe::grouped_gemm_f8_fits(rows, groups, n, true)) return MOE_ERR_UNSUPPORTED;
+  g.out = out;
+  g.out_row_bytes = static_cast<int64_t>(rb);
+  g.out_scale_off = static_cast<int32_t>(align32(n));
+  return hip_status(moe::launch_grouped_gemm_swiglu_quant_f8(g, static_cast<hipStream_t>(stream)));
 }
 
 const char* moe_status_str(int status) {

@@ -53,7 +53,8 @@ typedef enum {
   MOE_BF16 = 0,          /* bfloat16 */
   MOE_FP16 = 1,          /* IEEE binary16 */
   MOE_FP32 = 2,          /* IEEE binary32 (combine output only) */
-  MOE_INT8_ROWSCALE = 3  /* int8 codes + float inverse scale per row (receive buffer) */
+  MOE_INT8_ROWSCALE = 3, /* int8 codes + float inverse scale per row (receive buffer) */
+  MOE_E4M3_BLOCKSCALE = 4 /* e4m3 codes + float scale per 128 columns of a row */
 } moe_dtype;
 
 /* How the router turns an expert's logit into its score. */
@@ -99,7 +100,15 @@ enum {
  *                         with unspecified contents.  The page places the
  *                         scale but leaves the row stride open; rows here
  *                         start on 128-byte cache-line boundaries (7296 bytes
- *                         at hidden = 7168).
+ *                         at hidden = 7168);
+ *   MOE_E4M3_BLOCKSCALE:  e4m3 codes (8-bit floats with 4 exponent and 3
+ *                         fraction bits, largest 448, one NaN) at bytes [0,
+ *                         hidden), ceil(hidden / 128) floats from byte
+ *                         align32(hidden) on, the scales of the row's blocks
+ *                         of 128 columns, rounded up to a multiple of 128
+ *                         (7424 bytes at hidden = 7168).  No counterpart on
+ *                         the pages.  Column i stands for code[i] *
+ *                         scale[i / 128].
  * Host only; writes *bytes.  Errors: NULL_PTR, BAD_SHAPE (hidden < 1),
  * BAD_DTYPE. */
 int moe_recv_row_bytes(int32_t hidden, moe_dtype recv, size_t* bytes);
@@ -171,7 +180,9 @@ int moe_notify(const int32_t* tokenPerExpert, int32_t expertNumPerRank, int32_t 
  * s >= 0 writes token t's row to receive row
  *     recvBase[e / EPR] + putOffset[e] + s.
  * In:  x         device [bs, hidden] of xType (MOE_BF16 or MOE_FP16), 16-byte
- *                aligned.
+ *                aligned; or bs e4m3 rows (MOE_E4M3_BLOCKSCALE, made by
+ *                moe_rms_norm, hidden % 16 == 0, quantInt8 0), which are
+ *                copied whole.
  *      topkIdx, sendTokenIdx  device int32 [bs, topk] (from moe_layout).
  *      putOffset device int32 [E], recvBase device int32 [R] (from moe_notify).
  *      quantInt8 0: rows are copied as is (receive type = xType);
@@ -542,6 +553,134 @@ int moe_grouped_gemm_deq_i8(const void* a, int64_t aRowBytes, int32_t rows, int3
                             const int32_t* groupCount, int32_t groups, const void* w, int32_t n,
                             const float* weightScale, const void* tokenScale, int64_t tokenScaleStride,
                             void* out, moe_dtype outType, size_t outBytes, void* stream);
+
+/* ---- 8-bit float rows: the norm that makes them, the products that read them */
+
+/* Root-mean-square norm with the residual's addition, in front of the router
+ * and the dispatch (no counterpart on the pages).  For every token t and
+ * column i, in binary32
+ *   s    = x[t][i] + residual[t][i], rounded half-even to `type` (x[t][i]
+ *          without a residual)
+ *   rstd = 1 / sqrt(mean over i of s^2 + eps)
+ *   y    = (s * rstd) * weight[i]
+ * and y is rounded once: half-even to outType, and to e4m3 rows
+ * (moe_recv_row_bytes(hidden, MOE_E4M3_BLOCKSCALE) bytes each), where a block
+ * of 128 columns gets, with d = max(max |y|, 2^-100),
+ *   scale = d / 448,  code = e4m3(y * (448 / d)), half-even.
+ * A NaN in s makes its row NaN; an infinity makes it 0, and NaN where it stands.
+ * In:  x        device [bs][hidden] of type (MOE_BF16, MOE_FP16 or MOE_FP32).
+ *      residual device [bs][hidden] of type, or NULL.
+ *      weight   device float [hidden].  eps >= 0 (else MOE_ERR_BAD_SHAPE).
+ * Out: sum      device [bs][hidden] of type or NULL: s.  May be x or residual.
+ *      out      device [bs][hidden] of outType (the three types above) or NULL.
+ *      rows     device buffer of rowsBytes bytes or NULL: bs e4m3 rows, which
+ *               moe_dispatch carries to the experts as they are.  Padding is
+ *               never written.
+ *      rstd     device float [bs] or NULL, for moe_rms_norm_backward.
+ * At least one of out and rows is given (else MOE_ERR_NULL_PTR).  Matrices
+ * and rows are 16-byte aligned, weight and rstd 4-byte.  Outputs must not
+ * overlap inputs, apart from sum as said, nor each other.
+ * Requires bs >= 0, hidden % 8 == 0, hidden <= MOE_MAX_HIDDEN, with rows hidden
+ * % 16 == 0 (else MOE_ERR_UNSUPPORTED).  bs == 0 enqueues nothing.  One launch
+ * up to 2^21 tokens (larger batches in parts), no workspace. */
+int moe_rms_norm(const void* x, const void* residual, moe_dtype type, const float* weight, float eps,
+                 int32_t bs, int32_t hidden, void* sum, void* out, moe_dtype outType, void* rows,
+                 size_t rowsBytes, float* rstd, void* stream);
+
+/* Bytes of workspace that moe_rms_norm_backward needs to give the weight's
+ * gradient (the query-size, caller-allocates convention of page section 6.7):
+ * 4 * hidden for each of up to 512 parts of the batch.  Host only. */
+int moe_rms_norm_backward_workspace_bytes(int32_t bs, int32_t hidden, size_t* bytes);
+
+/* The norm's gradient (no counterpart on the pages): with g = gradOut, xh = s *
+ * rstd and gw = g * weight, in binary32
+ *   gradX[t][i]   = rstd * (gw - xh * mean over i of (gw * xh)) + gradSum[t][i]
+ *   gradWeight[i] = sum over t of g * xh
+ * gradX is the gradient of x and, the same, of the residual.
+ * In:  gradOut  device [bs][hidden] of gradOutType (MOE_BF16, MOE_FP16 or
+ *               MOE_FP32): the gradient of y.
+ *      gradSum  device [bs][hidden] of type, or NULL: the gradient that
+ *               reaches s past the norm.
+ *      sum, type, weight, rstd: as moe_rms_norm gave and had them.
+ *      tokenMask device bytes [bs] or NULL: a token whose byte is 0 gets
+ *               zeros in gradX and adds nothing to gradWeight, whatever its
+ *               rows hold.
+ * Out: gradX    device [bs][hidden] of type, rounded once.  May be gradSum, or
+ *               gradOut where that has the same type; must not overlap the
+ *               inputs otherwise.
+ *      gradWeight device float [hidden], or NULL (then no workspace is used).
+ * workspace: device, 16-byte aligned, at least
+ * moe_rms_norm_backward_workspace_bytes(bs, hidden) bytes; contents on return
+ * unspecified.  The sums do not depend on scheduling.  bs == 0 writes zeros to
+ * gradWeight.  Limits and errors as moe_rms_norm.  Two launches, one without
+ * gradWeight. */
+int moe_rms_norm_backward(const void* gradOut, moe_dtype gradOutType, const void* gradSum, const void* sum,
+                          moe_dtype type, const float* weight, const float* rstd, const uint8_t* tokenMask,
+                          int32_t bs, int32_t hidden, void* gradX, float* gradWeight, void* workspace,
+                          size_t workspaceBytes, void* stream);
+
+/* Expert product in 8-bit floats (no counterpart on the pages, whose products
+ * are int8): e4m3 rows times each expert's e4m3 weights, scaled for each 128
+ * of a row and for each 128 x 128 of the weights.  For every row m owned by
+ * expert g (as moe_grouped_gemm_i8 defines ownership) and column j < n, with
+ * the blocks b of 128 of k,
+ *   out[m][j] = sum over b of (ts[m][b] * ws[g][j / 128][b]) * p_b,
+ *   p_b       = sum over i in block b of a[m][i] * w[g][j][i]
+ * in binary32, rounded half-even to outType.  The result does not depend on
+ * scheduling.
+ *
+ * a, aRowBytes, rows, k, groupCount, groups: as moe_grouped_gemm_i8, with e4m3
+ *            codes (moe_dispatch's and moe_grouped_gemm_swiglu_quant_f8's rows
+ *            in place with aRowBytes = moe_recv_row_bytes(k,
+ *            MOE_E4M3_BLOCKSCALE)).
+ * w          [groups][n][k] e4m3, device, 16-byte aligned.
+ * weightScale [groups][ceil(n / 128)][ceil(k / 128)] float, device, 4-byte
+ *            aligned.
+ * tokenScale device, 4-byte aligned: the ceil(k / 128) floats of row m stand
+ *            from byte m * tokenScaleStride on (a multiple of 4, at least the
+ *            row's scales).  e4m3 rows' own scales are used in place with
+ *            tokenScale = rows + align32(k) and tokenScaleStride = aRowBytes.
+ * out        [rows][n] of outType (MOE_BF16, MOE_FP16 or MOE_FP32), device,
+ *            aligned to its element, outBytes >= rows * n elements.  A 16-bit
+ *            out with n = hidden is the receive buffer that moe_combine reads.
+ *            Rows that no expert owns are not written.
+ * Requires rows >= 0, k >= 1, n >= 1, groups >= 1, aRowBytes >= k,
+ * tokenScaleStride as above (else MOE_ERR_BAD_SHAPE); k % 16 == 0, k <=
+ * MOE_GEMM_MAX_K, n <= MOE_GEMM_MAX_N, groups <= MOE_GEMM_MAX_GROUPS, and a
+ * launch of fewer than 2^32 threads (else MOE_ERR_UNSUPPORTED); aRowBytes a
+ * multiple of 16 (else MOE_ERR_BAD_ALIGN).  rows == 0 enqueues nothing.  One
+ * launch, no workspace. */
+int moe_grouped_gemm_f8(const void* a, int64_t aRowBytes, int32_t rows, int32_t k, const int32_t* groupCount,
+                        int32_t groups, const void* w, int32_t n, const float* weightScale,
+                        const void* tokenScale, int64_t tokenScaleStride, void* out, moe_dtype outType,
+                        size_t outBytes, void* stream);
+
+/* Bytes of workspace that moe_grouped_gemm_swiglu_quant_f8 needs for `rows`
+ * rows and n activation columns (page section 6.7's convention); at most 4 * n
+ * for each of up to 4096 rows, and 0 for some sizes.  Host only. */
+int moe_gemm_swiglu_quant_f8_workspace_bytes(int32_t rows, int32_t n, size_t* bytes);
+
+/* The first expert product in 8-bit floats with its gate (the pages' int8 form
+ * is section 4.8.1's): with y as moe_grouped_gemm_f8 defines out before its
+ * rounding, for the n gate columns and the n up columns,
+ *   act[m][j] = (y[m][j] / (1 + e^-y[m][j])) * y[m][n + j]
+ * quantised like moe_rms_norm's rows, in blocks of 128 columns.
+ * Arguments as moe_grouped_gemm_f8, but for
+ * w          [groups][2n][k] e4m3: expert g's n gate rows, then its n up rows.
+ * weightScale [groups][2 * ceil(n / 128)][ceil(k / 128)] float: the gate
+ *            rows' blocks, then the up rows' (which begin anew).
+ * out        device, 16-byte aligned, outBytes >= rows * moe_recv_row_bytes(n,
+ *            MOE_E4M3_BLOCKSCALE): e4m3 rows.  Rows that no expert owns are
+ *            not written.  Activations must be finite in binary32.
+ * workspace  device, 16-byte aligned, of
+ *            moe_gemm_swiglu_quant_f8_workspace_bytes(rows, n) bytes (may be
+ *            NULL where that is 0); contents on return unspecified.
+ * Requires as moe_grouped_gemm_f8, n % 16 == 0 and 2n <= MOE_GEMM_MAX_N. */
+int moe_grouped_gemm_swiglu_quant_f8(const void* a, int64_t aRowBytes, int32_t rows, int32_t k,
+                                     const int32_t* groupCount, int32_t groups, const void* w, int32_t n,
+                                     const float* weightScale, const void* tokenScale,
+                                     int64_t tokenScaleStride, void* out, size_t outBytes, void* workspace,
+                                     size_t workspaceBytes, void* stream);
 
 /* Diagnostics.  No counterpart on the pages (their operator calls report
  * failure through the framework's own status; section 6.7 does not show it):
