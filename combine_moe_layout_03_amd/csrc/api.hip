@@ -801,7 +801,9 @@ int make_gemm_f8(const void* a, int64_t a_row_bytes, int32_t rows, int32_t k, co
 int check_gemm_f8(int64_t a_row_bytes, int32_t rows, int32_t k, int32_t groups, int32_t n, int32_t max_n,
                   int64_t token_scale_stride) {
   if (rows < 0 || k < 1 || n < 1 || groups < 1 || a_row_bytes < k || token_scale_stride % 4 != 0) return MOE_ERR_BAD_SHAPE;
-  if (k % 16 != 0 || k > MOE_GEMM_MAX_K || n > max_n || groups > MOE_GEMM_MAX_GROUPS) return MOE_ERR_UNSUPPORTED;
+  if (k % 16 != 0 || k > MOE_GEMM_MAX_K || n > max_n || groups > MOE_GEMM_MAX_GROUPS ||
+      a_row_bytes > moe::kF8MaxRowBytes)
+    return MOE_ERR_UNSUPPORTED;
   if (token_scale_stride / 4 < moe::f8_blocks(k)) return MOE_ERR_BAD_SHAPE;
   if (a_row_bytes % 16 != 0) return MOE_ERR_BAD_ALIGN;
   return MOE_OK;
@@ -823,9 +825,9 @@ int moe_grouped_gemm_f8(const void* a, int64_t a_row_bytes, int32_t rows, int32_
   const size_t es = float_bytes(out_type);
   if (!aligned(out, es)) return MOE_ERR_BAD_ALIGN;
   if (out_bytes / es / static_cast<size_t>(n) < static_cast<size_t>(rows)) return MOE_ERR_BUFFER_TOO_SMALL;
-  if (!moe::grouped_gemm_f8_fits(rows, groups, n, false)) return MOE_ERR_UNSUPPORTED;
+  if (!moe::grouped_gemm_f8_fits(rows, groups, n, static_cast<moe::Form>(float_type(out_type)))) return MOE_ERR_UNSUPPORTED;
   g.out = out;
-  return hip_status(moe::launch_grouped_gemm_f8(g, float_type(out_type), static_cast<hipStream_t>(stream)));
+  return hip_status(moe::launch_grouped_gemm_f8(g, static_cast<moe::Form>(float_type(out_type)), static_cast<hipStream_t>(stream)));
 }
 
 int moe_gemm_swiglu_quant_f8_workspace_bytes(int32_t rows, int32_t n, size_t* bytes) {
@@ -855,11 +857,11 @@ int moe_grouped_gemm_swiglu_quant_f8(const void* a, int64_t a_row_bytes, int32_t
   if ((st = moe_gemm_swiglu_quant_f8_workspace_bytes(rows, n, &need))) return st;
   if (need > 0 && !workspace) return MOE_ERR_NULL_PTR;
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
-  if (!moe::grouped_gemm_f8_fits(rows, groups, n, true)) return MOE_ERR_UNSUPPORTED;
+  if (!moe::grouped_gemm_f8_fits(rows, groups, n, moe::Form::kGated)) return MOE_ERR_UNSUPPORTED;
   g.out = out;
   g.out_row_bytes = static_cast<int64_t>(rb);
   g.out_scale_off = static_cast<int32_t>(align32(n));
-  return hip_status(moe::launch_grouped_gemm_swiglu_quant_f8(g, static_cast<hipStream_t>(stream)));
+  return hip_status(moe::launch_grouped_gemm_f8(g, moe::Form::kGated, static_cast<hipStream_t>(stream)));
 }
 
 const char* moe_status_str(int status) {

@@ -61,6 +61,15 @@ __device__ __forceinline__ WideCodes widen(i32x4 a, i32x4 b) {
   return WideCodes{{widen(i32x2{a[0], a[1]}), widen(i32x2{a[2], a[3]}), widen(i32x2{b[0], b[1]}),
                     widen(i32x2{b[2], b[3]})}};
 }
+// The 8-bit instruction, as it stands.
+__device__ __forceinline__ mfma_f32x4 block_sum(const i32x8& a, const i32x8& b) {
+  constexpr int kE4m3 = 0;
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, mfma_f32x4{0.0f, 0.0f, 0.0f, 0.0f}, kE4m3, kE4m3, 0, 0,
+                                                          0, 0);
+}
+__device__ __forceinline__ i32x8 join(i32x4 a, i32x4 b) {
+  return i32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
 __device__ __forceinline__ mfma_f32x4 block_sum(const WideCodes& a, const WideCodes& b) {
   mfma_f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll

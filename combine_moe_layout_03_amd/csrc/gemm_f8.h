@@ -11,6 +11,9 @@ namespace moe {
 // What becomes of the sums: rounded to a type, or gated and quantised.
 enum class Form { kBf16 = 0, kFp16 = 1, kF32 = 2, kGated = 3 };
 
+// Bytes between rows at most: a tile's rows lie within 32-bit offsets.
+constexpr int64_t kF8MaxRowBytes = int64_t(1) << 23;
+
 struct GemmF8Args {
   const uint8_t* a;            // row m at a + m * a_stride, k e4m3 codes
   int64_t a_stride;            // bytes between rows (a multiple of 16)
@@ -26,10 +29,10 @@ struct GemmF8Args {
   void* out;                   // [rows][n]; with SwiGLU e4m3 rows of out_row_bytes
   int64_t out_row_bytes;
   int32_t out_scale_off;
+  bool nt;                     // set by the launcher: the tiles' results are stored non-temporally
 };
 // Whether one launch holds the call's threads.
-bool grouped_gemm_f8_fits(int32_t rows, int32_t groups, int32_t n, bool swiglu);
-hipError_t launch_grouped_gemm_f8(const GemmF8Args& a, Out out_type, hipStream_t stream);
-hipError_t launch_grouped_gemm_swiglu_quant_f8(const GemmF8Args& a, hipStream_t stream);
+bool grouped_gemm_f8_fits(int32_t rows, int32_t groups, int32_t n, Form form);
+hipError_t launch_grouped_gemm_f8(GemmF8Args a, Form form, hipStream_t stream);
 
 }  // namespace moe

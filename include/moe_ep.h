@@ -646,8 +646,9 @@ int moe_rms_norm_backward(const void* gradOut, moe_dtype gradOutType, const void
  *            Rows that no expert owns are not written.
  * Requires rows >= 0, k >= 1, n >= 1, groups >= 1, aRowBytes >= k,
  * tokenScaleStride as above (else MOE_ERR_BAD_SHAPE); k % 16 == 0, k <=
- * MOE_GEMM_MAX_K, n <= MOE_GEMM_MAX_N, groups <= MOE_GEMM_MAX_GROUPS, and a
- * launch of fewer than 2^32 threads (else MOE_ERR_UNSUPPORTED); aRowBytes a
+ * MOE_GEMM_MAX_K, n <= MOE_GEMM_MAX_N, groups <= MOE_GEMM_MAX_GROUPS,
+ * aRowBytes <= 2^23, and a launch of fewer than 2^32 threads (else
+ * MOE_ERR_UNSUPPORTED); aRowBytes a
  * multiple of 16 (else MOE_ERR_BAD_ALIGN).  rows == 0 enqueues nothing.  One
  * launch, no workspace. */
 int moe_grouped_gemm_f8(const void* a, int64_t aRowBytes, int32_t rows, int32_t k, const int32_t* groupCount,

@@ -4,7 +4,14 @@
 # rows, and n that ends inside a block of 128 columns
 PLAIN = {
     "stream32": (200, 900, [40, 0, 33, 1, 60, 2, 3, 31, 0, 0, 9, 8, 1, 0]),
+    "tile64": (900, 648, [64, 0, 65, 1, 190, 2, 63, 31] + [22] * 22),
+    "tile128": (1800, 700, [128, 0, 129, 1, 400, 2, 127, 31] + [80] * 12),
+    "tile256": (5200, 1603, [256, 2600, 0, 2300]),
 }
 GATED = {
     "stream32": (200, 912, [40, 0, 33, 1, 60, 2, 3, 31, 0, 0, 9, 8, 1, 0]),
+    "tile64": (900, 656, [64, 0, 65, 1, 190, 2, 63, 31] + [22] * 22),
+    "tile128": (1800, 912, [128, 0, 129, 1, 400, 2, 127, 31] + [80] * 12),
 }
+# kernels whose 16-bit results come from the 8-bit matrix instruction
+CUT = ("tile256",)

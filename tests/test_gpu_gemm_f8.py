@@ -8,7 +8,7 @@ import torch
 import block_rows_ref as B
 import combine_moe_layout_03_amd as M
 from gpu_util import log
-from instance_cases_f8 import GATED, PLAIN
+from instance_cases_f8 import CUT, GATED, PLAIN
 
 pytestmark = pytest.mark.gpu
 
@@ -60,12 +60,14 @@ def run_plain(a, ts, w, ws, counts, kind, packed=True, out=None):
     return out.float().cpu().double().numpy()
 
 
-def check_plain(rng, rows, k, n, counts, kind, packed=True, exact=False):
+def check_plain(rng, rows, k, n, counts, kind, packed=True, exact=False, cut=False):
     log(f"gemm_f8 {rows} {k} {n} {counts[:8]} {kind} exact {exact}")
     a, ts, w, ws = inputs(rng, rows, k, n, len(counts), 1, exact)
     got = run_plain(a, ts, w, ws, counts, kind, packed)
     own = B.owners(counts, rows)
     want, err = B.product(a, ts, w, ws, own, n)
+    if cut and kind != "fp32":
+        err = err + B.cut(a, ts, w, ws, own, n)
     at = own >= 0
     if exact:  # sums of whole numbers below 2^24
         assert np.array_equal(got[at], torch.from_numpy(want[at]).to(B.TYPES[kind]).double().numpy())
@@ -147,8 +149,9 @@ def test_gemm_f8_exact_sums(case):
 def test_gemm_f8_every_kernel(name, k):
     rows, n, counts = PLAIN[name]
     kind = ("bf16", "fp16", "fp32")[k // 16 % 3]
-    check_plain(np.random.default_rng(k), rows, k, n, counts, kind)
+    check_plain(np.random.default_rng(k), rows, k, n, counts, kind, cut=name in CUT)
     check_plain(np.random.default_rng(k), rows, k, n - 1, counts, "fp32", exact=True)
+    check_plain(np.random.default_rng(k), rows, k, n - 5, counts, "bf16", exact=True)
 
 
 @pytest.mark.parametrize("name", PLAIN)
@@ -156,7 +159,7 @@ def test_gemm_f8_every_kernel(name, k):
 def test_gemm_f8_every_kernel_and_type(name, kind):
     rows, n, counts = PLAIN[name]
     for k in (144, 256, 2208):
-        check_plain(np.random.default_rng(k), rows, k, n, counts, kind)
+        check_plain(np.random.default_rng(k), rows, k, n, counts, kind, cut=name in CUT)
 
 
 @pytest.mark.parametrize("name", GATED)
