@@ -13,6 +13,7 @@
 #include "gemm_f8.h"
 #include "layer.h"
 #include "norm.h"
+#include "select_f8.h"
 #include "moe_ep.h"
 
 namespace {
@@ -833,7 +834,7 @@ int moe_grouped_gemm_f8(const void* a, int64_t a_row_bytes, int32_t rows, int32_
 int moe_gemm_swiglu_quant_f8_workspace_bytes(int32_t rows, int32_t n, size_t* bytes) {
   if (!bytes) return MOE_ERR_NULL_PTR;
   if (rows < 0 || n < 1) return MOE_ERR_BAD_SHAPE;
-  *bytes = 0;
+  *bytes = rows <= moe::select::kF8ActRows ? static_cast<size_t>(rows) * static_cast<size_t>(n) * 4u : 0u;
   return MOE_OK;
 }
 
@@ -861,6 +862,7 @@ int moe_grouped_gemm_swiglu_quant_f8(const void* a, int64_t a_row_bytes, int32_t
   g.out = out;
   g.out_row_bytes = static_cast<int64_t>(rb);
   g.out_scale_off = static_cast<int32_t>(align32(n));
+  g.workspace = workspace;
   return hip_status(moe::launch_grouped_gemm_f8(g, moe::Form::kGated, static_cast<hipStream_t>(stream)));
 }
 

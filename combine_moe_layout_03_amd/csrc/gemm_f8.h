@@ -9,7 +9,8 @@
 namespace moe {
 
 // What becomes of the sums: rounded to a type, or gated and quantised.
-enum class Form { kBf16 = 0, kFp16 = 1, kF32 = 2, kGated = 3 };
+// (kAct: gated, as binary32, for the workspace of a gated call)
+enum class Form { kBf16 = 0, kFp16 = 1, kF32 = 2, kGated = 3, kAct = 4 };
 
 // Bytes between rows at most: a tile's rows lie within 32-bit offsets.
 constexpr int64_t kF8MaxRowBytes = int64_t(1) << 23;
@@ -29,6 +30,7 @@ struct GemmF8Args {
   void* out;                   // [rows][n]; with SwiGLU e4m3 rows of out_row_bytes
   int64_t out_row_bytes;
   int32_t out_scale_off;
+  void* workspace;             // of a gated call of few rows: the activations, float [rows][n]
   bool nt;                     // set by the launcher: the tiles' results are stored non-temporally
 };
 // Whether one launch holds the call's threads.

@@ -42,7 +42,7 @@ __device__ __forceinline__ float gated(float g, float u) { return g / (1.0f + ex
 // Four consecutive columns of one row, as far as the row goes.
 template <Form kForm>
 __device__ __forceinline__ void store_columns(const GemmF8Args& a, int64_t row, int col, const f32x4& v) {
-  constexpr Out kOut = static_cast<Out>(kForm);
+  constexpr Out kOut = kForm == Form::kAct ? Out::kF32 : static_cast<Out>(kForm);
   const int64_t at = row * a.n + col;
   if (col + 4 <= a.n) {
     if constexpr (kOut == Out::kF32)
@@ -59,20 +59,29 @@ __device__ __forceinline__ void store_columns(const GemmF8Args& a, int64_t row, 
 
 // ---- few rows for each expert -----------------------------------------------------
 
-template <Form kForm, int kMI, int kWaves, int kKC>
-__global__ __launch_bounds__(kWave* kWaves) void stream_f8_kernel(GemmF8Args a, int64_t slots) {
-  constexpr bool kGated = kForm == Form::kGated;
-  constexpr int kNI = kGated ? 2 : 1;  // fragments of 16 columns of a wave: gate and up
-  constexpr int kThreads = kWave * kWaves, kCols = 16 * kWaves, kRows = 16 * kMI;
-  constexpr int kRowPieces = kKC / 16, kSteps = kKC / kF8Block;
-  constexpr int kCopies = kRows * kRowPieces / kThreads;  // pieces of a chunk's rows that a thread brings
-  constexpr int kScales = kRows * kSteps;                 // of a chunk, for each of kNI
-  static_assert(kRowPieces % 16 == 0 && kCopies * kThreads == kRows * kRowPieces, "whole chunks");
+// kMI x 16 rows; a wave has kNW x 16 columns (and as many again with a gate);
+// kSplit parts of kWaves waves share out the chunks of k, and the first adds
+// the others' sums.
+template <Form kForm, int kMI, int kNW, int kWaves, int kKC, int kSplit>
+__global__ __launch_bounds__(kWave* kWaves* kSplit) void stream_f8_kernel(GemmF8Args a, int64_t slots) {
+  constexpr bool kGated = kForm == Form::kAct;
+  constexpr int kHalves = kGated ? 2 : 1, kNI = kHalves * kNW;  // fragments of a wave: gate, then up
+  constexpr int kThreads = kWave * kWaves, kCols = 16 * kNW * kWaves, kRows = 16 * kMI;
+  constexpr int kRowPieces = kKC / 16, kSteps = kKC / kF8Block, kPieces = kRows * kRowPieces;
+  constexpr int kCopies = (kPieces + kThreads - 1) / kThreads;  // pieces of a chunk's rows that a thread brings
+  constexpr int kScales = kRows * kSteps;                       // of a chunk, for each half
+  static_assert(kRowPieces % 8 == 0 && (kPieces % kThreads == 0 || kCopies == 1), "whole chunks");
   static_assert(kScales <= kThreads && kF8Block % kCols == 0, "a scale a thread, one block of columns a workgroup");
-  __shared__ __attribute__((aligned(1024))) uint8_t rows[2][kRows * kKC];
-  __shared__ float scales[2][kNI][kScales];
-  __shared__ float row_max[kGated ? kWaves : 1][kRows];
-  const int tid = threadIdx.x, lane = tid % kWave, wave = uniform(tid / kWave);
+  constexpr int kRowsBytes = kRows * kKC;
+  // two buffers of every part's rows; later the sums of all parts but the first
+  constexpr int kSumsBytes = (kSplit - 1) * kThreads * kMI * kNI * 16;
+  __shared__ __attribute__((aligned(1024)))
+  uint8_t rows[2 * kSplit * kRowsBytes > kSumsBytes ? 2 * kSplit * kRowsBytes : kSumsBytes];
+  __shared__ float scales[2][kSplit][kHalves][kScales];
+  const int tid = threadIdx.x % kThreads, lane = tid % kWave, wave = uniform(tid / kWave);
+  const int part = kSplit == 1 ? 0 : uniform(threadIdx.x / kThreads);
+  uint8_t* const sa0 = rows + part * kRowsBytes;
+  uint8_t* const sa1 = sa0 + kSplit * kRowsBytes;
   // workgroups of one block of columns lie on one XCD, an expert's slots next to each other
   const int64_t x = blockIdx.x % 8, y = blockIdx.x / 8;
   const int64_t slot = y % slots, block = y / slots * 8 + x;
@@ -80,40 +89,43 @@ __global__ __launch_bounds__(kWave* kWaves) void stream_f8_kernel(GemmF8Args a, 
   RowSlot rs;
   if (!find_row_slot<kRows>(a.group_count, a.groups, a.rows, slot, lane, &rs)) return;
 
-  const int col0 = static_cast<int>(block) * kCols + wave * 16;
+  const int col0 = static_cast<int>(block) * kCols + wave * 16 * kNW;
   const int piece = lane / 16 * 16, l16 = lane % 16;
   const int kb = f8_blocks(a.k), nb = f8_blocks(a.n);
   const uint8_t* pb[kNI];
-  const float* ws[kNI];
+  const float* ws[kHalves];
 #pragma unroll
-  for (int j = 0; j < kNI; ++j) {
-    const int64_t half = static_cast<int64_t>(rs.group) * kNI + j;
-    pb[j] = a.w + (half * a.n + min(col0 + l16, a.n - 1)) * a.k;
-    ws[j] = a.weight_scale + (half * nb + static_cast<int>(block) * kCols / kF8Block) * kb;
+  for (int h = 0; h < kHalves; ++h) {
+    const int64_t half = static_cast<int64_t>(rs.group) * kHalves + h;
+#pragma unroll
+    for (int j = 0; j < kNW; ++j) pb[h * kNW + j] = a.w + (half * a.n + min(col0 + j * 16 + l16, a.n - 1)) * a.k;
+    ws[h] = a.weight_scale + (half * nb + static_cast<int>(block) * kCols / kF8Block) * kb;
   }
   const uint8_t* pa[kCopies];
   int ka[kCopies], la[kCopies];
 #pragma unroll
   for (int q = 0; q < kCopies; ++q) {
     const int p = q * kThreads + tid, r = p / kRowPieces, c = p % kRowPieces;
-    pa[q] = a.a + tile_row(rs.row0, rs.row_end, r) * a.a_stride;
+    pa[q] = a.a + tile_row(rs.row0, rs.row_end, min(r, kRows - 1)) * a.a_stride;
     ka[q] = c * 16;
-    la[q] = r * kKC + (c ^ (r % 16)) * 16;
+    la[q] = r * kKC + (c ^ (r % (kRowPieces < 16 ? kRowPieces : 16))) * 16;
   }
   // scale tid of a chunk: step tid / kRows, row tid % kRows
   const int sr = tid % kRows, sb = tid / kRows;
   const float* pts = reinterpret_cast<const float*>(
       a.token_scale + static_cast<int64_t>(tile_row(rs.row0, rs.row_end, sr)) * a.ts_stride);
-  const int rounds = (a.k + kKC - 1) / kKC;
-  // Past k the rows' codes count as zero, and so do their scales; the weights there are some of the same column's.
+  const int rounds = (a.k + kSplit * kKC - 1) / (kSplit * kKC);
+  // Past k the rows' codes count as zero, and so do their scales; the weights
+  // there are some of the same column's.
   struct Codes {
     i32x4 a, b;
   };
   struct Rows {
     i32x4 v[kCopies];
-    float s[kNI];
+    float s[kHalves];
   };
-  auto load_a = [&](int chunk, Rows& to) {
+  auto load_a = [&](int round, Rows& to) {
+    const int chunk = round * kSplit + part;
 #pragma unroll
     for (int q = 0; q < kCopies; ++q) {
       const int at = chunk * kKC + ka[q];
@@ -124,16 +136,18 @@ __global__ __launch_bounds__(kWave* kWaves) void stream_f8_kernel(GemmF8Args a, 
     const bool have = tid < kScales && b < kb;
     const float ts = have ? pts[b] : 0.0f;
 #pragma unroll
-    for (int j = 0; j < kNI; ++j) to.s[j] = have ? ts * ws[j][b] : 0.0f;
+    for (int h = 0; h < kHalves; ++h) to.s[h] = have ? ts * ws[h][b] : 0.0f;
   };
   auto put_a = [&](int buf, const Rows& from) {
 #pragma unroll
-    for (int q = 0; q < kCopies; ++q) *reinterpret_cast<i32x4*>(rows[buf] + la[q]) = from.v[q];
+    for (int q = 0; q < kCopies; ++q)
+      if (kPieces % kThreads == 0 || tid < kPieces) *reinterpret_cast<i32x4*>((buf ? sa1 : sa0) + la[q]) = from.v[q];
 #pragma unroll
-    for (int j = 0; j < kNI; ++j)
-      if (tid < kScales) scales[buf][j][tid] = from.s[j];
+    for (int h = 0; h < kHalves; ++h)
+      if (tid < kScales) scales[buf][part][h][tid] = from.s[h];
   };
-  auto load_b = [&](int chunk, Codes (&v)[kSteps][kNI]) {
+  auto load_b = [&](int round, Codes (&v)[kSteps][kNI]) {
+    const int chunk = round * kSplit + part;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const int at = chunk * kKC + s * kF8Block + piece;
@@ -156,13 +170,14 @@ __global__ __launch_bounds__(kWave* kWaves) void stream_f8_kernel(GemmF8Args a, 
       for (int j = 0; j < kNI; ++j) w[j] = widen(b[s][j].a, b[s][j].b);
 #pragma unroll
       for (int i = 0; i < kMI; ++i) {
-        const uint8_t* row = rows[buf] + (i * 16 + l16) * kKC;
-        const WideCodes f = widen(*reinterpret_cast<const i32x4*>(row + ((s * 8 + lane / 16) ^ l16) * 16),
-                                  *reinterpret_cast<const i32x4*>(row + ((s * 8 + 4 + lane / 16) ^ l16) * 16));
+        const int r = i * 16 + l16, turn = r % (kRowPieces < 16 ? kRowPieces : 16);
+        const uint8_t* row = (buf ? sa1 : sa0) + r * kKC;
+        const WideCodes f = widen(*reinterpret_cast<const i32x4*>(row + ((s * 8 + lane / 16) ^ turn) * 16),
+                                  *reinterpret_cast<const i32x4*>(row + ((s * 8 + 4 + lane / 16) ^ turn) * 16));
 #pragma unroll
         for (int j = 0; j < kNI; ++j) {
           const f32x4 p = block_sum(w[j], f);
-          const float scale = scales[buf][j][s * kRows + i * 16 + l16];
+          const float scale = scales[buf][part][j / kNW][s * kRows + r];
 #pragma unroll
           for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(p[q], scale, acc[i][j][q]);
         }
@@ -199,45 +214,40 @@ __global__ __launch_bounds__(kWave* kWaves) void stream_f8_kernel(GemmF8Args a, 
     put_a(0, a0);
     __syncthreads();
   }
-
-  const int col = col0 + lane / 16 * 4;
-  if constexpr (!kGated) {
-    if (col >= a.n) return;
+  if constexpr (kSplit > 1) {  // the first part adds the others' sums
+    f32x4* const sums = reinterpret_cast<f32x4*>(rows);
+    __syncthreads();
+    if (part > 0) {
 #pragma unroll
-    for (int i = 0; i < kMI; ++i) {
-      const int r = i * 16 + l16;
-      if (tile_has_row(rs.row0, rs.row_end, r)) store_columns<kForm>(a, rs.row0 + r, col, acc[i][0]);
-    }
-  } else {
-    // n is a multiple of 16: a wave's columns all exist, or none does
-    float act[kMI][4];
+      for (int i = 0; i < kMI; ++i)
 #pragma unroll
-    for (int i = 0; i < kMI; ++i) {
-      float m = 0.0f;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        act[i][q] = gated(acc[i][0][q], acc[i][1][q]);
-        m = __builtin_fmaxf(m, __builtin_fabsf(act[i][q]));
-      }
-      m = __builtin_fmaxf(m, __shfl_xor(m, 16));
-      m = __builtin_fmaxf(m, __shfl_xor(m, 32));
-      if (lane < 16) row_max[wave][i * 16 + lane] = col0 < a.n ? m : 0.0f;
+        for (int j = 0; j < kNI; ++j) sums[((part - 1) * kMI * kNI + i * kNI + j) * kThreads + tid] = acc[i][j];
     }
     __syncthreads();
-    if (col0 >= a.n) return;
+    if (part == 0) {
+#pragma unroll
+      for (int p = 1; p < kSplit; ++p)
+#pragma unroll
+        for (int i = 0; i < kMI; ++i)
+#pragma unroll
+          for (int j = 0; j < kNI; ++j) acc[i][j] += sums[((p - 1) * kMI * kNI + i * kNI + j) * kThreads + tid];
+    } else {
+      return;
+    }
+  }
+
+  const int col = col0 + lane / 16 * 4;
+#pragma unroll
+  for (int j = 0; j < kNW; ++j) {
+    if (col + j * 16 >= a.n) continue;
 #pragma unroll
     for (int i = 0; i < kMI; ++i) {
       const int r = i * 16 + l16;
-      float m = 0.0f;
+      if constexpr (kGated) {
 #pragma unroll
-      for (int v = 0; v < kWaves; ++v) m = __builtin_fmaxf(m, row_max[v][r]);
-      float scale, factor;
-      f8_scale(m, scale, factor);
-      if (!tile_has_row(rs.row0, rs.row_end, r)) continue;
-      uint8_t* dst = static_cast<uint8_t*>(a.out) + static_cast<int64_t>(rs.row0 + r) * a.out_row_bytes;
-      *reinterpret_cast<uint32_t*>(dst + col) =
-          f8_pack4(act[i][0] * factor, act[i][1] * factor, act[i][2] * factor, act[i][3] * factor);
-      if (wave == 0 && lane < 16) *reinterpret_cast<float*>(dst + a.out_scale_off + block * 4) = scale;
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = gated(acc[i][j][q], acc[i][kNW + j][q]);
+      }
+      if (tile_has_row(rs.row0, rs.row_end, r)) store_columns<kForm>(a, rs.row0 + r, col + j * 16, acc[i][j]);
     }
   }
 }
@@ -246,17 +256,16 @@ int64_t stream_blocks(int32_t rows, int32_t groups, int32_t n, int tile_m, int t
   return row_slots(rows, groups, tile_m) * (((static_cast<int64_t>(n) + tile_n - 1) / tile_n + 7) / 8 * 8);
 }
 
-template <Form kForm, int kMI, int kWaves, int kKC>
+template <Form kForm, int kMI, int kNW, int kWaves, int kKC, int kSplit>
 hipError_t launch_stream(const GemmF8Args& a, hipStream_t stream) {
-  const dim3 grid(static_cast<uint32_t>(stream_blocks(a.rows, a.groups, a.n, kMI * 16, 16 * kWaves)));
-  stream_f8_kernel<kForm, kMI, kWaves, kKC>
-      <<<grid, dim3(kWave * kWaves), 0, stream>>>(a, row_slots(a.rows, a.groups, kMI * 16));
+  const dim3 grid(static_cast<uint32_t>(stream_blocks(a.rows, a.groups, a.n, kMI * 16, 16 * kNW * kWaves)));
+  stream_f8_kernel<kForm, kMI, kNW, kWaves, kKC, kSplit>
+      <<<grid, dim3(kWave * kWaves * kSplit), 0, stream>>>(a, row_slots(a.rows, a.groups, kMI * 16));
   return hipGetLastError();
 }
 
 // ---- many rows for each expert -----------------------------------------------------
 
-constexpr int kTileWaves = 8;
 constexpr int kSK = kF8Block;     // bytes of k per stage: one block
 constexpr int kRound = 6;         // stages of a round: the slots' places come round again
 constexpr int kGroupCols = 1024;  // rows of weights of a group of column tiles
@@ -291,7 +300,7 @@ __device__ __forceinline__ void spread_rows(float v, float (&to)[kMI]) {
 // 16 bytes of consecutive columns of one row, as far as the row goes.
 template <Form kForm>
 __device__ __forceinline__ void store_piece(const GemmF8Args& a, int64_t row, int col, const u32x4& bits) {
-  constexpr int kSize = kForm == Form::kF32 ? 4 : 2, kCols = 16 / kSize;
+  constexpr int kSize = kForm == Form::kF32 || kForm == Form::kAct ? 4 : 2, kCols = 16 / kSize;
   const int64_t at = row * a.n + col;
   if (col + kCols <= a.n) {
     u32x4_u* const dst = reinterpret_cast<u32x4_u*>(static_cast<uint8_t*>(a.out) + at * kSize);
@@ -306,287 +315,176 @@ __device__ __forceinline__ void store_piece(const GemmF8Args& a, int64_t row, in
 #pragma unroll
     for (int q = 0; q < kCols; ++q) {
       if (col + q >= a.n) continue;
-      if constexpr (kForm == Form::kF32) static_cast<uint32_t*>(a.out)[at + q] = bits[q];
+      if constexpr (kSize == 4) static_cast<uint32_t*>(a.out)[at + q] = bits[q];
       else static_cast<uint16_t*>(a.out)[at + q] = static_cast<uint16_t>(bits[q / 2] >> (q % 2 * 16));
     }
   }
 }
 
-template <bool kWide>
-struct Fragment;
-template <>
-struct Fragment<true> {
-  WideCodes c;
-  __device__ __forceinline__ void set(i32x4 a, i32x4 b) { c = widen(a, b); }
-};
-template <>
-struct Fragment<false> {
-  i32x8 c;
-  __device__ __forceinline__ void set(i32x4 a, i32x4 b) { c = join(a, b); }
-};
-// The block's sums of one fragment of weights with kMI of rows, the chains of
-// instructions side by side.
-template <int kMI>
-__device__ __forceinline__ void block_sums(const Fragment<true>& w, const Fragment<true> (&a)[kMI], f32x4 (&p)[kMI]) {
-#pragma unroll
-  for (int i = 0; i < kMI; ++i) p[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-#pragma unroll
-    for (int i = 0; i < kMI; ++i) p[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.c.v[q], a[i].c.v[q], p[i], 0, 0, 0);
-}
-template <int kMI>
-__device__ __forceinline__ void block_sums(const Fragment<false>& w, const Fragment<false> (&a)[kMI], f32x4 (&p)[kMI]) {
-#pragma unroll
-  for (int i = 0; i < kMI; ++i) p[i] = block_sum(w.c, a[i].c);
-}
+// What every wave of a tile knows: the tile's rows and columns, its share of
+// the loads, and where its scales stand.
+//
+// Tiles in order: groups of column tiles, the row slots of a group, its
+// columns; XCD x (workgroups x, x + 8, ...) takes the x-th eighth of the tiles
+// that the counts give.
+template <Form kForm, int kTileM, int kTileN, int kWavesM, int kWavesN_>
+struct TileWave {
+  static constexpr bool kGated = kForm == Form::kGated || kForm == Form::kAct;
+  static constexpr int kHalves = kGated ? 2 : 1;  // gate and up
+  static constexpr int kWavesN = kWavesN_, kTileWaves = kWavesM * kWavesN;
+  static constexpr int kWaveM = kTileM / kWavesM, kWaveN = kTileN / kWavesN;
+  static constexpr int kMI = kWaveM / 16, kNI = kWaveN / 16;
+  static constexpr int kCols = kTileN / kHalves;  // columns of the result
+  static constexpr int kRowsPerLoad = kWave / (kSK / 16);
+  static constexpr int kLoadsA = kTileM / kRowsPerLoad / kTileWaves, kLoadsB = kTileN / kRowsPerLoad / kTileWaves;
+  static_assert(kTileWaves % 2 == 0 && kWaveM % 32 == 0, "what the swizzles go by");
+  static_assert(kF8Block % (kWaveN / kHalves) == 0 && (kForm != Form::kGated || kCols == kF8Block) &&
+                    kWaveN / kHalves % 32 == 0,
+                "a wave's columns share a scale, and fall into pairs of fragments");
 
-template <Form kForm, bool kWide, int kTileM, int kTileN, int kWavesM, bool kTail>
-__global__ __launch_bounds__(kWave* kTileWaves) void tile_f8_kernel(GemmF8Args a) {
-  constexpr bool kGated = kForm == Form::kGated;
-  constexpr int kHalves = kGated ? 2 : 1;  // gate and up
-  constexpr int kWavesN = kTileWaves / kWavesM;
-  constexpr int kWaveM = kTileM / kWavesM, kWaveN = kTileN / kWavesN;
-  constexpr int kMI = kWaveM / 16, kNI = kWaveN / 16, kStepNI = kNI / 2;
-  constexpr int kCols = kTileN / kHalves;  // columns of the result
-  constexpr int kRowsPerLoad = kWave / (kSK / 16);
-  constexpr int kLoadsA = kTileM / kRowsPerLoad / kTileWaves, kLoadsB = kTileN / kRowsPerLoad / kTileWaves;
-  static_assert(kF8Block % (kWaveN / kHalves) == 0 && (!kGated || kCols == kF8Block), "a wave's columns share a scale");
-  __shared__ __attribute__((aligned(1024))) uint8_t sa0[kTileM * kSK];
-  __shared__ __attribute__((aligned(1024))) uint8_t sa1[kTileM * kSK];
-  __shared__ __attribute__((aligned(1024))) uint8_t sb0[kTileN * kSK];
-  __shared__ __attribute__((aligned(1024))) uint8_t sb1[kTileN * kSK];
-  __shared__ __attribute__((aligned(1024))) uint8_t sb2[kTileN * kSK];
-  const int tid = threadIdx.x, lane = tid % kWave, wave = uniform(tid / kWave);
-
-  // Tiles in order: groups of column tiles, the row slots of a group, its
-  // columns; XCD x (workgroups x, x + 8, ...) takes the x-th eighth of the
-  // tiles that the counts give.
-  constexpr int kGroup = kGroupCols / kTileN;
-  const int64_t n_tiles = (a.n + kCols - 1) / kCols;
-  int64_t col_tile = 0;
-  const auto pick = [&](int64_t slots) -> int64_t {
-    const int64_t tiles = n_tiles * slots, per_xcd = (tiles + 7) / 8;
-    const int64_t l = blockIdx.x / 8, t = blockIdx.x % 8 * per_xcd + l;
-    if (l >= per_xcd || t >= tiles) return -1;
-    const int64_t group = t / (slots * kGroup), within = t - group * slots * kGroup;
-    const int64_t width = min(n_tiles - group * kGroup, static_cast<int64_t>(kGroup));
-    col_tile = group * kGroup + within % width;
-    return within / width;
-  };
-  RowSlot rs;
-  if (!place_row_slot<kTileM>(a.group_count, a.groups, a.rows, lane, pick, &rs)) return;  // the whole workgroup
-  const int row0 = rs.row0, row_end = rs.row_end;
-  const int col0 = static_cast<int>(col_tile) * kCols;
-  const int wm = wave / kWavesN, wn = wave % kWavesN;
-  const int l16 = lane % 16;
-
-  // Load q of this wave fills the stage rows from 8 (q 8 + wave); lane l
-  // fetches the piece that belongs at position l % 8 of row l / 8, the same
-  // piece for every q.  A wave's stage rows of weights are its gate rows, then
-  // its up rows.
-  const int piece = (lane % 8) ^ swizzle(kRowsPerLoad * wave + lane / 8);
-  // Offsets from the tile's first row fit in 32 bits: 256 rows of at most
+  int lane, wave, wm, wn, l16, row0, row_end, col0, stages;
+  // Load q of a wave fills the stage rows from 8 (q kTileWaves + wave); lane l
+  // fetches the piece that belongs at position l % 8 of row l / 8.  A wave's stage rows of weights are its gate rows, then its up
+  // rows.  Offsets from the tile's first row fit in 32 bits: 256 rows of at most
   // kF8MaxRowBytes, and weights of at most 2^16 columns by 2^16 with 256 more.
-  const uint8_t* const base_a = a.a + row0 * a.a_stride;
-  const uint8_t* const base_b = a.w + (static_cast<int64_t>(rs.group) * kHalves * a.n + col0) * a.k;
+  int piece, k;  // (the piece of load 0)
+  // kTileWaves is even: q turns the bit of swizzle() that rows 16 apart differ in.
+  __device__ __forceinline__ int piece_of(int q) const { return piece ^ ((q * (kTileWaves / 2) & 1) << 1); }
+  const uint8_t *base_a, *base_b;
   uint32_t src_a[kLoadsA], src_b[kLoadsB];
-#pragma unroll
-  for (int q = 0; q < kLoadsA; ++q) {
-    const int r = kRowsPerLoad * (q * kTileWaves + wave) + lane / 8;
-    src_a[q] = static_cast<uint32_t>(tile_row(row0, row_end, r) - row0) * static_cast<uint32_t>(a.a_stride) + piece * 16;
-  }
-#pragma unroll
-  for (int q = 0; q < kLoadsB; ++q) {
-    const int r = kRowsPerLoad * (q * kTileWaves + wave) + lane / 8;
-    constexpr int kPart = kWaveN / kHalves;
-    const int half = r % kWaveN / kPart, c = r / kWaveN * kPart + r % kPart;
-    src_b[q] = static_cast<uint32_t>(half * a.n + min(c, a.n - 1 - col0)) * static_cast<uint32_t>(a.k) + piece * 16;
-  }
-  // The scales: lane l has those of the wave's row l, two stages ahead; the
-  // weights' are the same in every lane, and come a round's at a time.
-  const int stages = f8_blocks(a.k), nb = f8_blocks(a.n);
-  const float* const ts_row = reinterpret_cast<const float*>(
-      a.token_scale + static_cast<int64_t>(tile_row(row0, row_end, wm * kWaveM + lane % kWaveM)) * a.ts_stride);
-  const int col_block = uniform(min((col0 + wn * (kWaveN / kHalves)) / kF8Block, nb - 1));
-  const float* ws[kHalves];
-#pragma unroll
-  for (int h = 0; h < kHalves; ++h)
-    ws[h] = a.weight_scale + ((static_cast<int64_t>(rs.group) * kHalves + h) * nb + col_block) * stages;
-  float row_scale[2];  // of this stage and the next
-  struct ColScales {
-    float v[kHalves][kRound];
-  };
-  const auto load_col_scales = [&](int first, ColScales& s) {
-#pragma unroll
-    for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-      for (int q = 0; q < kRound; ++q) s.v[h][q] = ws[h][min(first + q, stages - 1)];
-  };
-  // Stages past the last one load it again, into slots that are not read; a
-  // piece past k reads the row's first piece (its row fragments count as zero).
-  auto stage_offset = [&](int s) {
-    return min(s, stages - 1) * kSK;
-  };
-  auto tail_offset = [&](int k0) { return static_cast<uint32_t>((k0 + piece * 16 < a.k) ? k0 : -piece * 16); };
-  auto issue_a = [&](int s, uint8_t* buf) {
-    const int k0 = stage_offset(s);
+  const float* ts_row;        // the scales of the wave's row lane % kWaveM
+  const float* ws[kHalves];   // of its columns
+  // Fragments: pair p, tile t of the weights is row 32 p + 8 (l16 / 4) + 4 t +
+  // l16 % 4, so that a lane ends with 8 consecutive columns in the two tiles.
+  int frag_a, frag_b, swz_a, swz_b;
+
+  __device__ __forceinline__ bool set(const GemmF8Args& a) {
+    lane = threadIdx.x % kWave, wave = uniform(threadIdx.x / kWave);
+    constexpr int kGroup = kGroupCols / kTileN;
+    const int64_t n_tiles = (a.n + kCols - 1) / kCols;
+    int64_t col_tile = 0;
+    const auto pick = [&](int64_t slots) -> int64_t {
+      const int64_t tiles = n_tiles * slots, per_xcd = (tiles + 7) / 8;
+      const int64_t l = blockIdx.x / 8, t = blockIdx.x % 8 * per_xcd + l;
+      if (l >= per_xcd || t >= tiles) return -1;
+      const int64_t group = t / (slots * kGroup), within = t - group * slots * kGroup;
+      const int64_t width = min(n_tiles - group * kGroup, static_cast<int64_t>(kGroup));
+      col_tile = group * kGroup + within % width;
+      return within / width;
+    };
+    RowSlot rs;
+    if (!place_row_slot<kTileM>(a.group_count, a.groups, a.rows, lane, pick, &rs)) return false;
+    row0 = rs.row0, row_end = rs.row_end;
+    col0 = static_cast<int>(col_tile) * kCols;
+    wm = wave / kWavesN, wn = wave % kWavesN, l16 = lane % 16;
+    stages = f8_blocks(a.k), k = a.k;
+    piece = (lane % 8) ^ swizzle(kRowsPerLoad * wave + lane / 8);
+    base_a = a.a + row0 * a.a_stride;
+    base_b = a.w + (static_cast<int64_t>(rs.group) * kHalves * a.n + col0) * a.k;
 #pragma unroll
     for (int q = 0; q < kLoadsA; ++q) {
-      const uint8_t* src;
-      if constexpr (kTail) src = base_a + (src_a[q] + tail_offset(k0));
-      else src = base_a + k0 + src_a[q];
-      __builtin_amdgcn_global_load_lds(src, (MOE_LDS void*)(buf + (q * kTileWaves + wave) * kRowsPerLoad * kSK), 16, 0,
-                                       0);
+      const int r = kRowsPerLoad * (q * kTileWaves + wave) + lane / 8;
+      src_a[q] = static_cast<uint32_t>(tile_row(row0, row_end, r) - row0) * static_cast<uint32_t>(a.a_stride) + piece_of(q) * 16;
     }
-  };
-  auto issue_b = [&](int s, uint8_t* buf) {
-    const int k0 = stage_offset(s);
 #pragma unroll
     for (int q = 0; q < kLoadsB; ++q) {
-      const uint8_t* src;
-      if constexpr (kTail) src = base_b + (src_b[q] + tail_offset(k0));
-      else src = base_b + k0 + src_b[q];
-      __builtin_amdgcn_global_load_lds(src, (MOE_LDS void*)(buf + (q * kTileWaves + wave) * kRowsPerLoad * kSK), 16, 0,
-                                       0);
+      const int r = kRowsPerLoad * (q * kTileWaves + wave) + lane / 8;
+      constexpr int kPart = kWaveN / kHalves;
+      const int half = r % kWaveN / kPart, c = r / kWaveN * kPart + r % kPart;
+      src_b[q] = static_cast<uint32_t>(half * a.n + min(c, a.n - 1 - col0)) * static_cast<uint32_t>(a.k) + piece_of(q) * 16;
     }
-  };
-
-  const int frag_a = (wm * kWaveM + l16) * kSK;
-  // pair p, tile t of the weights: row 32 p + 8 (l16 / 4) + 4 t + l16 % 4, so
-  // that a lane ends with 8 consecutive columns in the two tiles
-  const int row_b = 8 * (l16 / 4) + l16 % 4;
-  const int frag_b = (wn * kWaveN + row_b) * kSK;
-  const int swz_a = swizzle(l16), swz_b = swizzle(row_b);
-  f32x4 acc[kMI][kNI];
+    ts_row = reinterpret_cast<const float*>(
+        a.token_scale + static_cast<int64_t>(tile_row(row0, row_end, wm * kWaveM + lane % kWaveM)) * a.ts_stride);
+    const int nb = f8_blocks(a.n);
+    const int col_block = uniform(min((col0 + wn * (kWaveN / kHalves)) / kF8Block, nb - 1));
 #pragma unroll
-  for (int i = 0; i < kMI; ++i)
-#pragma unroll
-    for (int j = 0; j < kNI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-  auto barrier = [&]() {
-    __builtin_amdgcn_sched_barrier(0);
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_s_barrier();
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  Fragment<kWide> af[kMI];
-  // Half of a stage's columns: with a gate, its gate or its up columns.
-  auto step = [&](int S, int h, float ts, float w, const uint8_t* ca, const uint8_t* cb, uint8_t* fill_a,
-                  uint8_t* fill_b) {
-    if (h == 0) issue_a(S + 1, fill_a);  // into the slot A(S - 1) used
-    else issue_b(S + 2, fill_b);         // into the slot B(S - 1) used
-    const int p = lane / 16;
-    i32x4 ra[kMI][2], rb[kStepNI][2];
-    if (h == 0) {
-#pragma unroll
-      for (int i = 0; i < kMI; ++i)
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          ra[i][q] = *reinterpret_cast<const i32x4*>(ca + frag_a + i * 16 * kSK +
-                                                     ((4 * q + p) ^ swz_a ^ ((i & 1) << 1)) * 16);
-    }
-#pragma unroll
-    for (int n = 0; n < kStepNI; ++n) {
-      const int j = h * kStepNI + n;
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        rb[n][q] = *reinterpret_cast<const i32x4*>(cb + frag_b + ((j >> 1) * 32 + (j & 1) * 4) * kSK +
-                                                   ((4 * q + p) ^ swz_b ^ ((j & 1) << 1)) * 16);
-    }
-    float s[kMI];
-    spread_rows<kMI>(ts, s);
-#pragma unroll
-    for (int i = 0; i < kMI; ++i) s[i] *= w;
-    // this wave's loads of A(S + 1) and B(S + 1); those of B(S + 2) may still run
-    if (h == 1) __builtin_amdgcn_s_waitcnt(vmcnt_wait(kLoadsB));
-    __builtin_amdgcn_s_waitcnt(kLgkmWait0);
-    if (h == 0) {
-#pragma unroll
-      for (int i = 0; i < kMI; ++i) {
-        if constexpr (kTail) {
-#pragma unroll
-          for (int q = 0; q < 2; ++q) ra[i][q] &= S * kSK + (4 * q + p) * 16 < a.k ? -1 : 0;
-        }
-        af[i].set(ra[i][0], ra[i][1]);
-      }
-    }
-    Fragment<kWide> bf[kStepNI];
-#pragma unroll
-    for (int n = 0; n < kStepNI; ++n) bf[n].set(rb[n][0], rb[n][1]);
-    barrier();
-#pragma unroll
-    for (int n = 0; n < kStepNI; ++n) {
-      f32x4 part[kMI];
-      block_sums<kMI>(bf[n], af, part);
-#pragma unroll
-      for (int i = 0; i < kMI; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          acc[i][h * kStepNI + n][q] = __builtin_fmaf(part[i][q], s[i], acc[i][h * kStepNI + n][q]);
-    }
-    barrier();
-  };
-  auto stage = [&](int S, int u, const ColScales& s, const uint8_t* ca, const uint8_t* cb, uint8_t* fill_a,
-                   uint8_t* fill_b) {
-    step(S, 0, row_scale[u % 2], s.v[0][u], ca, cb, fill_a, fill_b);
-    step(S, 1, row_scale[u % 2], s.v[kHalves - 1][u], ca, cb, fill_a, fill_b);
-    row_scale[u % 2] = ts_row[min(S + 2, stages - 1)];
-  };
-  ColScales now, next;
-  load_col_scales(0, next);
-#pragma unroll
-  for (int u = 0; u < 2; ++u) row_scale[u] = ts_row[min(u, stages - 1)];
-  issue_b(0, sb0);
-  issue_a(0, sa0);
-  issue_b(1, sb1);
-  __builtin_amdgcn_s_waitcnt(vmcnt_wait(kLoadsB));
-  barrier();
-  const int grp = wave / 4;
-  if (grp == 1) barrier();  // the second group runs half a step behind
-  const int rounds = stages / kRound;
-  for (int r = 0; r < rounds; ++r) {
-    now = next;
-    load_col_scales(kRound * (r + 1), next);
-    stage(kRound * r, 0, now, sa0, sb0, sa1, sb2);
-    stage(kRound * r + 1, 1, now, sa1, sb1, sa0, sb0);
-    stage(kRound * r + 2, 2, now, sa0, sb2, sa1, sb1);
-    stage(kRound * r + 3, 3, now, sa1, sb0, sa0, sb2);
-    stage(kRound * r + 4, 4, now, sa0, sb1, sa1, sb0);
-    stage(kRound * r + 5, 5, now, sa1, sb2, sa0, sb1);
+    for (int h = 0; h < kHalves; ++h)
+      ws[h] = a.weight_scale + ((static_cast<int64_t>(rs.group) * kHalves + h) * nb + col_block) * stages;
+    frag_a = (wm * kWaveM + l16) * kSK;
+    const int row_b = 8 * (l16 / 4) + l16 % 4;
+    frag_b = (wn * kWaveN + row_b) * kSK;
+    swz_a = swizzle(l16), swz_b = swizzle(row_b);
+    return true;
   }
-  {
-    const int rest = stages - rounds * kRound;
-    if (rest > 0) stage(kRound * rounds, 0, next, sa0, sb0, sa1, sb2);
-    if (rest > 1) stage(kRound * rounds + 1, 1, next, sa1, sb1, sa0, sb0);
-    if (rest > 2) stage(kRound * rounds + 2, 2, next, sa0, sb2, sa1, sb1);
-    if (rest > 3) stage(kRound * rounds + 3, 3, next, sa1, sb0, sa0, sb2);
-    if (rest > 4) stage(kRound * rounds + 4, 4, next, sa0, sb1, sa1, sb0);
+
+  // Stages past the last one load it again, into slots that are not read; a
+  // piece past k reads the row's first piece (its row fragments count as zero).
+  template <bool kTail, int kLoads>
+  __device__ __forceinline__ void issue(int s, const uint8_t* base, const uint32_t (&src)[kLoads], uint8_t* buf) const {
+    const int k0 = min(s, stages - 1) * kSK;
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+      const uint8_t* p;
+      if constexpr (kTail) p = base + (src[q] + static_cast<uint32_t>((k0 + piece_of(q) * 16 < k) ? k0 : -piece_of(q) * 16));
+      else p = base + k0 + src[q];
+      __builtin_amdgcn_global_load_lds(p, (MOE_LDS void*)(buf + (q * kTileWaves + wave) * kRowsPerLoad * kSK), 16, 0, 0);
+    }
   }
-  if (grp == 0) barrier();  // every wave passes the same number of barriers
-  // no load may still be writing this workgroup's LDS
-  __builtin_amdgcn_s_waitcnt(vmcnt_wait(0));
-  // The results pass through LDS, so that a store's lanes lie along rows (whole
-  // cache lines).  The slots are free once every wave's loads have landed and
-  // its reads are done.
-  barrier();
-  if constexpr (!kGated) {
-    constexpr int kPieceCols = kForm == Form::kF32 ? 4 : 8;  // columns of a 16-byte piece
-    constexpr int kRowPieces = kWaveN / kPieceCols, kWaveBytes = 16 * kRowPieces * 16;
+  // The two pieces of fragment i of a stage's rows, and j of its weights.
+  __device__ __forceinline__ void read_a(const uint8_t* buf, int i, i32x4 (&to)[2]) const {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      to[q] = *reinterpret_cast<const i32x4*>(buf + frag_a + i * 16 * kSK +
+                                              ((4 * q + lane / 16) ^ swz_a ^ ((i & 1) << 1)) * 16);
+  }
+  __device__ __forceinline__ void read_b(const uint8_t* buf, int j, i32x4 (&to)[2]) const {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      to[q] = *reinterpret_cast<const i32x4*>(buf + frag_b + ((j >> 1) * 32 + (j & 1) * 4) * kSK +
+                                              ((4 * q + lane / 16) ^ swz_b ^ ((j & 1) << 1)) * 16);
+  }
+  // Zeros for a row fragment's pieces past k, in stage s.
+  __device__ __forceinline__ void cut_tail(int s, i32x4 (&a)[2]) const {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) a[q] &= s * kSK + (4 * q + lane / 16) * 16 < k ? -1 : 0;
+  }
+};
+
+__device__ __forceinline__ void tile_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_s_barrier();
+  __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// A tile's results.  They pass through LDS, so that a store's lanes lie along
+// rows (whole cache lines): `lds0` and `lds1` of kTileN stage rows each, and
+// `small` for the row maxima.
+template <Form kForm, int kTileM, int kTileN, int kWavesM, int kWavesN, int kMI, int kNI>
+__device__ __forceinline__ void store_tile(const GemmF8Args& a,
+                                           const TileWave<kForm, kTileM, kTileN, kWavesM, kWavesN>& t,
+                                           const f32x4 (&acc)[kMI][kNI], uint8_t* lds0, uint8_t* lds1,
+                                           uint8_t* small) {
+  using T = TileWave<kForm, kTileM, kTileN, kWavesM, kWavesN>;
+  constexpr int kWaveM = T::kWaveM, kWaveN = T::kWaveN, kTileWaves = T::kTileWaves;
+  const int lane = t.lane, wave = t.wave, l16 = t.l16, wm = t.wm, wn = t.wn, col0 = t.col0;
+  const int row0 = t.row0, row_end = t.row_end;
+  if constexpr (kForm != Form::kGated) {
+    constexpr bool kFloats = kForm == Form::kF32 || kForm == Form::kAct;
+    constexpr int kPieceCols = kFloats ? 4 : 8;       // columns of a 16-byte piece
+    constexpr int kWaveCols = kWaveN / T::kHalves;  // of the result
+    constexpr int kRowPieces = kWaveCols / kPieceCols, kWaveBytes = 16 * kRowPieces * 16;
     constexpr int kSlotWaves = kTileN * kSK / kWaveBytes < kTileWaves ? kTileN * kSK / kWaveBytes : kTileWaves;
     static_assert(2 * kSlotWaves >= kTileWaves, "two slots hold every wave's rows");
-    uint8_t* const mine = (wave < kSlotWaves ? sb0 : sb1) + wave % kSlotWaves * kWaveBytes;
+    uint8_t* const mine = (wave < kSlotWaves ? lds0 : lds1) + wave % kSlotWaves * kWaveBytes;
     // piece c of row r lies at c ^ r, so that 16 rows' pieces fall into all banks
     constexpr int kTurn = (kRowPieces < 16 ? kRowPieces : 16) - 1;
     const auto place = [&](int r, int c) { return mine + (r * kRowPieces + (c ^ (r & kTurn))) * 16; };
 #pragma unroll
     for (int i = 0; i < kMI; ++i) {
 #pragma unroll
-      for (int p = 0; p < kNI / 2; ++p) {
-        const f32x4 v = acc[i][2 * p], u = acc[i][2 * p + 1];
+      for (int p = 0; p < kNI / 2 / T::kHalves; ++p) {
+        f32x4 v = acc[i][2 * p], u = acc[i][2 * p + 1];
+        if constexpr (kForm == Form::kAct) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            v[q] = gated(v[q], acc[i][kNI / 2 + 2 * p][q]);
+            u[q] = gated(u[q], acc[i][kNI / 2 + 2 * p + 1][q]);
+          }
+        }
         const int c = (p * 4 + lane / 16) * (8 / kPieceCols);
-        if constexpr (kForm == Form::kF32) {
+        if constexpr (kFloats) {
           *reinterpret_cast<f32x4*>(place(l16, c)) = v;
           *reinterpret_cast<f32x4*>(place(l16, c + 1)) = u;
         } else {
@@ -597,18 +495,19 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_f8_kernel(GemmF8Args a
       }
       wave_lds_sync();
 #pragma unroll
-      for (int t = 0; t < 16 * kRowPieces / kWave; ++t) {
-        const int r = (t * kWave + lane) / kRowPieces, c = (t * kWave + lane) % kRowPieces;
+      for (int x = 0; x < 16 * kRowPieces / kWave; ++x) {
+        const int r = (x * kWave + lane) / kRowPieces, c = (x * kWave + lane) % kRowPieces;
         const u32x4 bits = *reinterpret_cast<const u32x4*>(place(r, c));
         const int tr = wm * kWaveM + i * 16 + r;
-        if (tile_has_row(row0, row_end, tr)) store_piece<kForm>(a, row0 + tr, col0 + wn * kWaveN + c * kPieceCols, bits);
+        if (tile_has_row(row0, row_end, tr))
+          store_piece<kForm>(a, row0 + tr, col0 + wn * kWaveCols + c * kPieceCols, bits);
       }
       wave_lds_sync();
     }
   } else {
-    static_assert(!kGated || kNI == 4, "a pair of gate tiles and a pair of up tiles");
-    float* const row_max = reinterpret_cast<float*>(sa1);  // [kWavesN][kTileM]
-    uint8_t* const codes = sb0;                            // [kTileM][128], piece c of row r at c ^ r
+    static_assert(kForm != Form::kGated || kNI == 4, "a pair of gate tiles and a pair of up tiles");
+    float* const row_max = reinterpret_cast<float*>(small);  // [kWavesN][kTileM]
+    uint8_t* const codes = lds0;                            // [kTileM][128], piece c of row r at c ^ r
     const int wave_col = wn * 32 + lane / 16 * 8;          // this lane's 8 columns of the block
     const bool has = col0 + wave_col < a.n;                // n is a multiple of 16
     float act[kMI][8];
@@ -648,8 +547,8 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_f8_kernel(GemmF8Args a
     const int c = lane % 8;
     if (col0 + c * 16 >= a.n) return;
 #pragma unroll
-    for (int t = 0; t < kTileM / 8 / kTileWaves; ++t) {
-      const int r = (t * kTileWaves + wave) * 8 + lane / 8;
+    for (int x = 0; x < kTileM / 8 / kTileWaves; ++x) {
+      const int r = (x * kTileWaves + wave) * 8 + lane / 8;
       const u32x4 bits = *reinterpret_cast<const u32x4*>(codes + r * kF8Block + ((c ^ (r & 7)) * 16));
       if (tile_has_row(row0, row_end, r))
         *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.out) + static_cast<int64_t>(row0 + r) * a.out_row_bytes + col0 +
@@ -658,59 +557,362 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_f8_kernel(GemmF8Args a
   }
 }
 
+// The 8-bit instruction: eight waves in two groups, one wave of each per SIMD,
+// half a step apart; while one multiplies, the other reads its fragments.
+template <Form kForm, int kTileM, int kTileN, int kWavesM, int kWavesN, bool kTail>
+__global__ __launch_bounds__(kWave* kWavesM* kWavesN) void tile_f8_kernel(GemmF8Args a) {
+  using T = TileWave<kForm, kTileM, kTileN, kWavesM, kWavesN>;
+  static_assert(T::kTileWaves == 8, "two groups of four waves");
+  constexpr int kMI = T::kMI, kNI = T::kNI, kStepNI = kNI / 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t sa0[kTileM * kSK];
+  __shared__ __attribute__((aligned(1024))) uint8_t sa1[kTileM * kSK];
+  __shared__ __attribute__((aligned(1024))) uint8_t sb0[kTileN * kSK];
+  __shared__ __attribute__((aligned(1024))) uint8_t sb1[kTileN * kSK];
+  __shared__ __attribute__((aligned(1024))) uint8_t sb2[kTileN * kSK];
+  T t;
+  if (!t.set(a)) return;  // the whole workgroup
+  const int stages = t.stages;
+  // The scales: lane l has those of the wave's row l, two stages ahead.  The
+  // weights' are the same for all rows; lane l has the one l stages on, a round
+  // ahead.  (As scalar loads they made every wait for LDS wait for memory.)
+  float row_scale[2], col_scales, next_col_scales;
+  const auto load_col_scales = [&](int first) { return t.ws[0][min(first + t.lane, stages - 1)]; };
+  f32x4 acc[kMI][kNI];
+#pragma unroll
+  for (int i = 0; i < kMI; ++i)
+#pragma unroll
+    for (int j = 0; j < kNI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  i32x8 af[kMI];
+  // Half of a stage's columns.
+  auto step = [&](int S, int h, float ts, float w, const uint8_t* ca, const uint8_t* cb, uint8_t* fill_a,
+                  uint8_t* fill_b) {
+    if (h == 0) t.template issue<kTail>(S + 1, t.base_a, t.src_a, fill_a);  // into the slot A(S - 1) used
+    else t.template issue<kTail>(S + 2, t.base_b, t.src_b, fill_b);         // into the slot B(S - 1) used
+    i32x4 ra[kMI][2], rb[kStepNI][2];
+    if (h == 0) {
+#pragma unroll
+      for (int i = 0; i < kMI; ++i) t.read_a(ca, i, ra[i]);
+    }
+#pragma unroll
+    for (int n = 0; n < kStepNI; ++n) t.read_b(cb, h * kStepNI + n, rb[n]);
+    float s[kMI];
+    spread_rows<kMI>(ts, s);
+#pragma unroll
+    for (int i = 0; i < kMI; ++i) s[i] *= w;
+    // this wave's loads of A(S + 1) and B(S + 1); those of B(S + 2) may still run
+    if (h == 1) __builtin_amdgcn_s_waitcnt(vmcnt_wait(T::kLoadsB));
+    __builtin_amdgcn_s_waitcnt(kLgkmWait0);
+    if (h == 0) {
+#pragma unroll
+      for (int i = 0; i < kMI; ++i) {
+        if constexpr (kTail) t.cut_tail(S, ra[i]);
+        af[i] = join(ra[i][0], ra[i][1]);
+      }
+    }
+    tile_barrier();
+#pragma unroll
+    for (int n = 0; n < kStepNI; ++n) {
+      f32x4 part[kMI];
+#pragma unroll
+      for (int i = 0; i < kMI; ++i) part[i] = block_sum(join(rb[n][0], rb[n][1]), af[i]);
+#pragma unroll
+      for (int i = 0; i < kMI; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          acc[i][h * kStepNI + n][q] = __builtin_fmaf(part[i][q], s[i], acc[i][h * kStepNI + n][q]);
+    }
+    tile_barrier();
+  };
+  auto stage = [&](int S, int u, const uint8_t* ca, const uint8_t* cb, uint8_t* fill_a, uint8_t* fill_b) {
+    const float w = lane_float(col_scales, u);
+    step(S, 0, row_scale[u % 2], w, ca, cb, fill_a, fill_b);
+    step(S, 1, row_scale[u % 2], w, ca, cb, fill_a, fill_b);
+    row_scale[u % 2] = t.ts_row[min(S + 2, stages - 1)];
+  };
+  next_col_scales = load_col_scales(0);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) row_scale[u] = t.ts_row[min(u, stages - 1)];
+  t.template issue<kTail>(0, t.base_b, t.src_b, sb0);
+  t.template issue<kTail>(0, t.base_a, t.src_a, sa0);
+  t.template issue<kTail>(1, t.base_b, t.src_b, sb1);
+  __builtin_amdgcn_s_waitcnt(vmcnt_wait(T::kLoadsB));
+  tile_barrier();
+  const int grp = t.wave / 4;
+  if (grp == 1) tile_barrier();  // the second group runs half a step behind
+  const int rounds = stages / kRound;
+  for (int r = 0; r < rounds; ++r) {
+    col_scales = next_col_scales;
+    next_col_scales = load_col_scales(kRound * (r + 1));
+    stage(kRound * r, 0, sa0, sb0, sa1, sb2);
+    stage(kRound * r + 1, 1, sa1, sb1, sa0, sb0);
+    stage(kRound * r + 2, 2, sa0, sb2, sa1, sb1);
+    stage(kRound * r + 3, 3, sa1, sb0, sa0, sb2);
+    stage(kRound * r + 4, 4, sa0, sb1, sa1, sb0);
+    stage(kRound * r + 5, 5, sa1, sb2, sa0, sb1);
+  }
+  {
+    col_scales = next_col_scales;
+    const int rest = stages - rounds * kRound;
+    if (rest > 0) stage(kRound * rounds, 0, sa0, sb0, sa1, sb2);
+    if (rest > 1) stage(kRound * rounds + 1, 1, sa1, sb1, sa0, sb0);
+    if (rest > 2) stage(kRound * rounds + 2, 2, sa0, sb2, sa1, sb1);
+    if (rest > 3) stage(kRound * rounds + 3, 3, sa1, sb0, sa0, sb2);
+    if (rest > 4) stage(kRound * rounds + 4, 4, sa0, sb1, sa1, sb0);
+  }
+  if (grp == 0) tile_barrier();  // every wave passes the same number of barriers
+  // no load may still be writing this workgroup's LDS, and no wave reading it
+  __builtin_amdgcn_s_waitcnt(vmcnt_wait(0));
+  tile_barrier();
+  store_tile(a, t, acc, sb0, sb1, sa1);
+}
+
+// A ring of kSlots stages in LDS, of which one is multiplied while the others'
+// loads run; the waves meet once a stage.  For the widened codes the vector ALU
+// has nearly as much to do as the matrix cores (16 conversions a fragment, 4
+// multiply-adds for each 4 matrix instructions), and overlaps with them freely.
+template <bool kWide>
+struct FragmentOf {
+  using Type = i32x8;
+  static __device__ __forceinline__ Type make(const i32x4 (&r)[2]) { return join(r[0], r[1]); }
+};
+template <>
+struct FragmentOf<true> {
+  using Type = WideCodes;
+  static __device__ __forceinline__ Type make(const i32x4 (&r)[2]) { return widen(r[0], r[1]); }
+};
+
+template <Form kForm, bool kWide, int kTileM, int kTileN, int kWavesM, int kWavesN, int kSlots, bool kTail>
+__global__ __launch_bounds__(kWave* kWavesM* kWavesN) void ring_f8_kernel(GemmF8Args a) {
+  using T = TileWave<kForm, kTileM, kTileN, kWavesM, kWavesN>;
+  using F = FragmentOf<kWide>;
+  constexpr int kMI = T::kMI, kNI = T::kNI;
+  static_assert(kSlots == 3 || kSlots == 4, "the slots declared below");
+  __shared__ __attribute__((aligned(1024))) uint8_t sa0[kTileM * kSK];
+  __shared__ __attribute__((aligned(1024))) uint8_t sa1[kTileM * kSK];
+  __shared__ __attribute__((aligned(1024))) uint8_t sa2[kTileM * kSK];
+  __shared__ __attribute__((aligned(1024))) uint8_t sa3[kSlots == 4 ? kTileM * kSK : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t sb0[kTileN * kSK];
+  __shared__ __attribute__((aligned(1024))) uint8_t sb1[kTileN * kSK];
+  __shared__ __attribute__((aligned(1024))) uint8_t sb2[kTileN * kSK];
+  __shared__ __attribute__((aligned(1024))) uint8_t sb3[kSlots == 4 ? kTileN * kSK : 16];
+  constexpr int kScaleFloats = (kTileM + kWave - 1) / kWave * kWave + kWave;
+  __shared__ float ss0[kScaleFloats], ss1[kScaleFloats], ss2[kScaleFloats], ss3[kSlots == 4 ? kScaleFloats : 1];
+  T t;
+  if (!t.set(a)) return;  // the whole workgroup
+  const int stages = t.stages;
+  f32x4 acc[kMI][kNI];
+#pragma unroll
+  for (int i = 0; i < kMI; ++i)
+#pragma unroll
+    for (int j = 0; j < kNI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  // A stage's scales lie in its slot, brought by one load of each wave: the
+  // first waves have 64 rows each, the others all the same one or two of the
+  // weights (a tile's columns lie in one block).  Loaded into registers by each
+  // wave for itself, the rows' with a vector and the weights' with a scalar load,
+  // they cost 1000 rows, k 2048, n 7168 7 and 14 of 75 us.
+  constexpr int kLoads = T::kLoadsA + T::kLoadsB + 1, kRowWaves = (kTileM + kWave - 1) / kWave;
+  static_assert(kRowWaves < T::kTileWaves, "a wave for the weights' scales");
+  const float* scale_src;
+  if (t.wave < kRowWaves) {
+    scale_src = reinterpret_cast<const float*>(
+        a.token_scale + static_cast<int64_t>(tile_row(t.row0, t.row_end, min(t.wave * kWave + t.lane, kTileM - 1))) * a.ts_stride);
+  } else {
+    scale_src = t.lane % T::kHalves == 0 ? t.ws[0] : t.ws[T::kHalves - 1];
+  }
+  const int scale_at = t.wave < kRowWaves ? t.wave * kWave : kRowWaves * kWave;
+  const auto issue = [&](int S, uint8_t* to_a, uint8_t* to_b, float* to_s) {
+    t.template issue<kTail>(S, t.base_b, t.src_b, to_b);
+    t.template issue<kTail>(S, t.base_a, t.src_a, to_a);
+    __builtin_amdgcn_global_load_lds(scale_src + min(S, stages - 1), (MOE_LDS void*)(to_s + scale_at), 4, 0, 0);
+  };
+  issue(0, sa0, sb0, ss0);
+  issue(1, sa1, sb1, ss1);
+  if constexpr (kSlots == 4) issue(2, sa2, sb2, ss2);
+  __builtin_amdgcn_s_waitcnt(vmcnt_wait((kSlots - 2) * kLoads));
+  tile_barrier();
+  auto stage = [&](int S, const uint8_t* ca, const uint8_t* cb, const float* cs, uint8_t* fill_a, uint8_t* fill_b,
+                   float* fill_s) {
+    issue(S + kSlots - 1, fill_a, fill_b, fill_s);  // into the slot of stage S - 1
+    i32x4 ra[kMI][2], rb[2][2];
+#pragma unroll
+    for (int i = 0; i < kMI; ++i) t.read_a(ca, i, ra[i]);
+    t.read_b(cb, 0, rb[0]);
+    float row[kMI], ws[T::kHalves];
+#pragma unroll
+    for (int i = 0; i < kMI; ++i) row[i] = cs[t.wm * T::kWaveM + i * 16 + t.l16];
+#pragma unroll
+    for (int h = 0; h < T::kHalves; ++h) ws[h] = cs[kRowWaves * kWave + h];
+    typename F::Type af[kMI];
+#pragma unroll
+    for (int i = 0; i < kMI; ++i) {
+      if constexpr (kTail) t.cut_tail(S, ra[i]);
+      af[i] = F::make(ra[i]);
+    }
+    // The next fragment is read, and the last one's sums join, while a fragment
+    // is multiplied.
+    f32x4 p[2][kMI];
+    const auto join_sums = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < kMI; ++i) {
+        const float s = row[i] * ws[j / (kNI / T::kHalves)];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(p[j % 2][i][q], s, acc[i][j][q]);
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < kNI; ++j) {
+      if (j + 1 < kNI) t.read_b(cb, j + 1, rb[(j + 1) % 2]);
+      const typename F::Type bf = F::make(rb[j % 2]);
+      if constexpr (kWide) {
+#pragma unroll
+        for (int i = 0; i < kMI; ++i) p[j % 2][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int i = 0; i < kMI; ++i)
+            p[j % 2][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf.v[q], af[i].v[q], p[j % 2][i], 0, 0, 0);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kMI; ++i) p[j % 2][i] = block_sum(bf, af[i]);
+      }
+      if (j > 0) join_sums(j - 1);
+    }
+    join_sums(kNI - 1);
+    // this wave's loads of stage S + 1, and its reads of stage S
+    __builtin_amdgcn_s_waitcnt(vmcnt_wait((kSlots - 2) * kLoads));
+    __builtin_amdgcn_s_waitcnt(kLgkmWait0);
+    tile_barrier();
+  };
+  const int rounds = stages / kSlots, rest = stages - rounds * kSlots;
+  int S = 0;
+  if constexpr (kSlots == 3) {
+    for (int r = 0; r < rounds; ++r, S += 3) {
+      stage(S, sa0, sb0, ss0, sa2, sb2, ss2);
+      stage(S + 1, sa1, sb1, ss1, sa0, sb0, ss0);
+      stage(S + 2, sa2, sb2, ss2, sa1, sb1, ss1);
+    }
+    if (rest > 0) stage(S, sa0, sb0, ss0, sa2, sb2, ss2);
+    if (rest > 1) stage(S + 1, sa1, sb1, ss1, sa0, sb0, ss0);
+  } else {
+    for (int r = 0; r < rounds; ++r, S += 4) {
+      stage(S, sa0, sb0, ss0, sa3, sb3, ss3);
+      stage(S + 1, sa1, sb1, ss1, sa0, sb0, ss0);
+      stage(S + 2, sa2, sb2, ss2, sa1, sb1, ss1);
+      stage(S + 3, sa3, sb3, ss3, sa2, sb2, ss2);
+    }
+    if (rest > 0) stage(S, sa0, sb0, ss0, sa3, sb3, ss3);
+    if (rest > 1) stage(S + 1, sa1, sb1, ss1, sa0, sb0, ss0);
+    if (rest > 2) stage(S + 2, sa2, sb2, ss2, sa1, sb1, ss1);
+  }
+  // no load may still be writing this workgroup's LDS
+  __builtin_amdgcn_s_waitcnt(vmcnt_wait(0));
+  tile_barrier();
+  store_tile(a, t, acc, sb0, sb1, sa1);
+}
+
 int64_t tile_blocks(int32_t rows, int32_t groups, int32_t n, int tile_m, int tile_n) {
   return (row_slots(rows, groups, tile_m) * ((static_cast<int64_t>(n) + tile_n - 1) / tile_n) + 7) / 8 * 8;
 }
 
-template <Form kForm, bool kWide, int kTileM, int kTileN, int kWavesM>
+constexpr int tile_cols(Form form, int tile_n) {
+  return form == Form::kGated || form == Form::kAct ? tile_n / 2 : tile_n;
+}
+
+template <Form kForm, int kTileM, int kTileN, int kWavesM, int kWavesN>
 hipError_t launch_tile(const GemmF8Args& a, hipStream_t stream) {
-  constexpr int kCols = kForm == Form::kGated ? kTileN / 2 : kTileN;
-  const dim3 grid(static_cast<uint32_t>(tile_blocks(a.rows, a.groups, a.n, kTileM, kCols))), block(kWave * kTileWaves);
-  if (a.k % kSK != 0) tile_f8_kernel<kForm, kWide, kTileM, kTileN, kWavesM, true><<<grid, block, 0, stream>>>(a);
-  else tile_f8_kernel<kForm, kWide, kTileM, kTileN, kWavesM, false><<<grid, block, 0, stream>>>(a);
+  const dim3 grid(static_cast<uint32_t>(tile_blocks(a.rows, a.groups, a.n, kTileM, tile_cols(kForm, kTileN))));
+  const dim3 block(kWave * kWavesM * kWavesN);
+  if (a.k % kSK != 0) tile_f8_kernel<kForm, kTileM, kTileN, kWavesM, kWavesN, true><<<grid, block, 0, stream>>>(a);
+  else tile_f8_kernel<kForm, kTileM, kTileN, kWavesM, kWavesN, false><<<grid, block, 0, stream>>>(a);
+  return hipGetLastError();
+}
+template <Form kForm, bool kWide, int kTileM, int kTileN, int kWavesM, int kWavesN, int kSlots>
+hipError_t launch_ring(const GemmF8Args& a, hipStream_t stream) {
+  const dim3 grid(static_cast<uint32_t>(tile_blocks(a.rows, a.groups, a.n, kTileM, tile_cols(kForm, kTileN))));
+  const dim3 block(kWave * kWavesM * kWavesN);
+  if (a.k % kSK != 0)
+    ring_f8_kernel<kForm, kWide, kTileM, kTileN, kWavesM, kWavesN, kSlots, true><<<grid, block, 0, stream>>>(a);
+  else
+    ring_f8_kernel<kForm, kWide, kTileM, kTileN, kWavesM, kWavesN, kSlots, false><<<grid, block, 0, stream>>>(a);
   return hipGetLastError();
 }
 
 // One case for each kernel of select::gemm_f8_kind.
 template <Form kForm>
 hipError_t launch_form(const GemmF8Args& a, hipStream_t stream) {
+  constexpr bool kWide = kForm == Form::kF32;
   switch (select::gemm_f8_kind(a.rows, a.groups, a.n)) {
-    case select::GemmF8Kind::kStream32: return launch_stream<kForm, 2, 4, 256>(a, stream);
-    case select::GemmF8Kind::kTile64: return launch_tile<kForm, true, 64, 128, 2>(a, stream);
-    case select::GemmF8Kind::kTile128: return launch_tile<kForm, true, 128, 128, 2>(a, stream);
+    case select::GemmF8Kind::kSplit16: return launch_stream<kForm, 1, 1, 1, 256, 4>(a, stream);
+    case select::GemmF8Kind::kTile32: return launch_ring<kForm, kWide, 32, 128, 1, 2, 3>(a, stream);
+    case select::GemmF8Kind::kTile64: return launch_ring<kForm, kWide, 64, 128, 2, 2, 3>(a, stream);
     case select::GemmF8Kind::kTile256:
-      if constexpr (kForm == Form::kF32) return launch_tile<kForm, true, 256, 128, 4>(a, stream);
-      else return launch_tile<kForm, false, 256, 256, 4>(a, stream);
+      if constexpr (kWide) return launch_ring<kForm, true, 256, 128, 4, 2, 3>(a, stream);
+      else return launch_tile<kForm, 256, 256, 4, 2>(a, stream);
   }
   return hipErrorInvalidValue;
 }
-hipError_t launch_gated(const GemmF8Args& a, hipStream_t stream) {
-  switch (select::gemm_f8_gated_kind(a.rows, a.groups, a.n)) {
-    case select::GemmF8Kind::kStream32: return launch_stream<Form::kGated, 2, 8, 256>(a, stream);
-    case select::GemmF8Kind::kTile64: return launch_tile<Form::kGated, true, 64, 256, 2>(a, stream);
-    case select::GemmF8Kind::kTile128: return launch_tile<Form::kGated, true, 128, 256, 2>(a, stream);
+hipError_t launch_act(const GemmF8Args& a, hipStream_t stream) {
+  switch (select::gemm_f8_act_kind(a.rows, a.groups, a.n)) {
+    case select::GemmF8Kind::kSplit16: return launch_stream<Form::kAct, 1, 1, 1, 256, 4>(a, stream);
+    case select::GemmF8Kind::kTile32: return launch_ring<Form::kAct, true, 32, 128, 1, 2, 3>(a, stream);
+    case select::GemmF8Kind::kTile64: return launch_ring<Form::kAct, true, 64, 128, 2, 2, 3>(a, stream);
     default: return hipErrorInvalidValue;
   }
 }
 
 }  // namespace
 
+// The workspace's rows of activations, quantised: 16 lanes a block of 128
+// columns, four blocks a wave.  Rows that no expert owns are not read.
+__global__ __launch_bounds__(256) void quant_act_f8_kernel(GemmF8Args a, const float* act, int64_t items) {
+  const int lane = threadIdx.x % kWave;
+  const int quads = (f8_blocks(a.n) + 3) / 4;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + uniform(threadIdx.x / kWave);
+  if (item >= items) return;
+  const int64_t row = item / quads;
+  uint32_t owned = 0;  // rows of the experts, whose sum may pass 2^32: a sum that saturates is past `rows`
+  for (int g = lane; g < a.groups; g += kWave) owned = add_sat(owned, static_cast<uint32_t>(max(a.group_count[g], 0)));
+  for (int d = 1; d < kWave; d *= 2) owned = add_sat(owned, static_cast<uint32_t>(__shfl_xor(static_cast<int>(owned), d)));
+  if (row >= owned) return;
+  const int block = static_cast<int>(item % quads) * 4 + lane / 16, col = block * kF8Block + lane % 16 * 8;
+  const bool has = col < a.n;  // n is a multiple of 16
+  float f[8], m = 0.0f;
+  const f32x4* src = reinterpret_cast<const f32x4*>(act + row * a.n + (has ? col : 0));
+  const f32x4 u = src[0], v = src[1];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    f[q] = q < 4 ? u[q % 4] : v[q % 4];
+    m = __builtin_fmaxf(m, __builtin_fabsf(f[q]));
+  }
+  float scale, factor;
+  f8_scale(token_max<16>(has ? m : 0.0f), scale, factor);
+  if (!has) return;
+  uint8_t* dst = static_cast<uint8_t*>(a.out) + row * a.out_row_bytes;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) f[q] *= factor;
+  *reinterpret_cast<u32x2*>(dst + col) = u32x2{f8_pack4(f[0], f[1], f[2], f[3]), f8_pack4(f[4], f[5], f[6], f[7])};
+  if (lane % 16 == 0) *reinterpret_cast<float*>(dst + a.out_scale_off + block * 4) = scale;
+}
+
 bool grouped_gemm_f8_fits(int32_t rows, int32_t groups, int32_t n, Form form) {
-  constexpr int64_t kTileBlocks = kMaxLaunchThreads / (kTileWaves * kWave);
+  const auto split = [&]() { return stream_blocks(rows, groups, n, 16, 16) <= kMaxLaunchThreads / (4 * kWave); };
+  const auto tile = [&](int tile_m, int tile_n, int waves) {
+    return tile_blocks(rows, groups, n, tile_m, tile_n) <= kMaxLaunchThreads / (waves * kWave);
+  };
   if (form == Form::kGated) {
-    switch (select::gemm_f8_gated_kind(rows, groups, n)) {
-      case select::GemmF8Kind::kStream32: return stream_blocks(rows, groups, n, 32, 128) <= kMaxLaunchThreads / (8 * kWave);
-      case select::GemmF8Kind::kTile64: return tile_blocks(rows, groups, n, 64, 128) <= kTileBlocks;
-      case select::GemmF8Kind::kTile128: return tile_blocks(rows, groups, n, 128, 128) <= kTileBlocks;
+    if (!select::gemm_f8_act(rows, groups, n)) return tile(128, 128, 8);
+    switch (select::gemm_f8_act_kind(rows, groups, n)) {
+      case select::GemmF8Kind::kSplit16: return split();
+      case select::GemmF8Kind::kTile32: return tile(32, 64, 2);
+      case select::GemmF8Kind::kTile64: return tile(64, 64, 4);
       default: return false;
     }
   }
   switch (select::gemm_f8_kind(rows, groups, n)) {
-    case select::GemmF8Kind::kStream32: return stream_blocks(rows, groups, n, 32, 64) <= kMaxLaunchThreads / (4 * kWave);
-    case select::GemmF8Kind::kTile64: return tile_blocks(rows, groups, n, 64, 128) <= kTileBlocks;
-    case select::GemmF8Kind::kTile128: return tile_blocks(rows, groups, n, 128, 128) <= kTileBlocks;
-    case select::GemmF8Kind::kTile256:
-      return tile_blocks(rows, groups, n, 256, form == Form::kF32 ? 128 : 256) <= kTileBlocks;
+    case select::GemmF8Kind::kSplit16: return split();
+    case select::GemmF8Kind::kTile32: return tile(32, 128, 2);
+    case select::GemmF8Kind::kTile64: return tile(64, 128, 4);
+    case select::GemmF8Kind::kTile256: return tile(256, form == Form::kF32 ? 128 : 256, 8);
   }
   return false;
 }
@@ -723,9 +925,17 @@ hipError_t launch_grouped_gemm_f8(GemmF8Args a, Form form, hipStream_t stream) {
     case Form::kBf16: return launch_form<Form::kBf16>(a, stream);
     case Form::kFp16: return launch_form<Form::kFp16>(a, stream);
     case Form::kF32: return launch_form<Form::kF32>(a, stream);
-    case Form::kGated: return launch_gated(a, stream);
+    default: break;
   }
-  return hipErrorInvalidValue;
+  if (!select::gemm_f8_act(a.rows, a.groups, a.n)) return launch_ring<Form::kGated, true, 128, 256, 2, 4, 3>(a, stream);
+  GemmF8Args first = a;
+  first.out = a.workspace;
+  const hipError_t e = launch_act(first, stream);
+  if (e != hipSuccess) return e;
+  const int64_t items = static_cast<int64_t>(a.rows) * ((f8_blocks(a.n) + 3) / 4);
+  quant_act_f8_kernel<<<dim3(static_cast<uint32_t>((items + 3) / 4)), dim3(4 * kWave), 0, stream>>>(
+      a, static_cast<const float*>(a.workspace), items);
+  return hipGetLastError();
 }
 
 }  // namespace moe

@@ -7,24 +7,33 @@
 namespace moe {
 namespace select {
 
-enum class GemmF8Kind { kStream32, kTile64, kTile128, kTile256 };
+enum class GemmF8Kind { kSplit16, kTile32, kTile64, kTile256 };
 
 // Workgroups to expect: every other expert ends inside a tile.
 constexpr int64_t gemm_f8_workgroups(int32_t rows, int32_t groups, int32_t n, int tile_m, int tile_n) {
   return (rows / tile_m + (int64_t(groups) + 1) / 2) * ((int64_t(n) + tile_n - 1) / tile_n);
 }
+// The workgroups of 16 columns (a quarter of k to each of their four waves).
+constexpr int64_t gemm_f8_split_workgroups(int32_t rows, int32_t groups, int32_t n) {
+  return (rows / 16 + int64_t(rows < groups ? rows : groups)) * ((int64_t(n) + 15) / 16);
+}
 constexpr GemmF8Kind gemm_f8_kind(int32_t rows, int32_t groups, int32_t n) {
   const int64_t mean = (int64_t(rows) + groups - 1) / groups;
-  if (mean <= 16) return GemmF8Kind::kStream32;
+  if (gemm_f8_split_workgroups(rows, groups, n) <= 1024) return GemmF8Kind::kSplit16;
+  if (mean <= 16) return GemmF8Kind::kTile32;
   if (mean > 128 && gemm_f8_workgroups(rows, groups, n, 256, 256) >= 128) return GemmF8Kind::kTile256;
-  if (mean > 48 && gemm_f8_workgroups(rows, groups, n, 128, 128) >= 128) return GemmF8Kind::kTile128;
-  return gemm_f8_workgroups(rows, groups, n, 64, 128) >= 128 ? GemmF8Kind::kTile64 : GemmF8Kind::kStream32;
+  return GemmF8Kind::kTile64;
 }
-constexpr GemmF8Kind gemm_f8_gated_kind(int32_t rows, int32_t groups, int32_t n) {
+
+constexpr int32_t kF8ActRows = 4096;
+constexpr bool gemm_f8_act(int32_t rows, int32_t groups, int32_t n) {
   const int64_t mean = (int64_t(rows) + groups - 1) / groups;
-  if (mean <= 16) return GemmF8Kind::kStream32;
-  if (mean > 96 && gemm_f8_workgroups(rows, groups, n, 128, 128) >= 128) return GemmF8Kind::kTile128;
-  return gemm_f8_workgroups(rows, groups, n, 64, 128) >= 128 ? GemmF8Kind::kTile64 : GemmF8Kind::kStream32;
+  return rows <= kF8ActRows && (mean <= 128 || gemm_f8_workgroups(rows, groups, n, 128, 128) < 192);
+}
+constexpr GemmF8Kind gemm_f8_act_kind(int32_t rows, int32_t groups, int32_t n) {
+  const int64_t mean = (int64_t(rows) + groups - 1) / groups;
+  if (gemm_f8_split_workgroups(rows, groups, n) <= 768) return GemmF8Kind::kSplit16;
+  return mean <= 16 ? GemmF8Kind::kTile32 : GemmF8Kind::kTile64;
 }
 
 }  // namespace select

@@ -3,15 +3,14 @@
 # name: (rows, n, counts) as the rule picks them (csrc/select_f8.h); counts that end inside tiles, experts without
 # rows, and n that ends inside a block of 128 columns
 PLAIN = {
-    "stream32": (200, 900, [40, 0, 33, 1, 60, 2, 3, 31, 0, 0, 9, 8, 1, 0]),
+    "split16": (50, 700, [0, 3, 5, 17, 0, 1, 2, 4, 0, 0, 9, 8, 1, 0]),
+    "tile32": (200, 900, [40, 0, 33, 1, 60, 2, 3, 31, 0, 0, 9, 8, 1, 0]),
     "tile64": (900, 648, [64, 0, 65, 1, 190, 2, 63, 31] + [22] * 22),
-    "tile128": (1800, 700, [128, 0, 129, 1, 400, 2, 127, 31] + [80] * 12),
     "tile256": (5200, 1603, [256, 2600, 0, 2300]),
 }
-GATED = {
-    "stream32": (200, 912, [40, 0, 33, 1, 60, 2, 3, 31, 0, 0, 9, 8, 1, 0]),
+GATED = {  # (the rows that go through the workspace, and those that do not)
+    "split16": (50, 464, [0, 3, 5, 17, 0, 1, 2, 4, 0, 0, 9, 8, 1, 0]),
+    "tile32": (200, 912, [40, 0, 33, 1, 60, 2, 3, 31, 0, 0, 9, 8, 1, 0]),
     "tile64": (900, 656, [64, 0, 65, 1, 190, 2, 63, 31] + [22] * 22),
-    "tile128": (1800, 912, [128, 0, 129, 1, 400, 2, 127, 31] + [80] * 12),
+    "whole": (4200, 400, [256, 2100, 0, 1800]),
 }
-# kernels whose 16-bit results come from the 8-bit matrix instruction
-CUT = ("tile256",)
