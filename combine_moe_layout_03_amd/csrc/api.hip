@@ -741,7 +741,7 @@ int moe_rms_norm_backward_workspace_bytes(int32_t bs, int32_t hidden, size_t* by
   if (bs < 0) return MOE_ERR_BAD_SHAPE;
   int st = check_hidden(hidden);
   if (st) return st;
-  *bytes = static_cast<size_t>(moe::select::norm_backward_parts(bs)) * static_cast<size_t>(hidden) * 4u;
+  *bytes = static_cast<size_t>(moe::select::norm_backward_parts(bs, hidden)) * static_cast<size_t>(hidden) * 4u;
   return MOE_OK;
 }
 

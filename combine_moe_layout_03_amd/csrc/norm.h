@@ -35,7 +35,7 @@ struct NormBackwardArgs {
   int32_t bs, hidden;
   void* grad_x;          // [bs][hidden] of sum's type
   float* grad_weight;    // [hidden] or null
-  float* partial;        // [norm_backward_parts(bs)][hidden] where grad_weight is given
+  float* partial;        // [norm_backward_parts(bs, hidden)][hidden] where grad_weight is given
 };
 hipError_t launch_rms_norm_backward(const NormBackwardArgs& a, Out type, Out grad_type, hipStream_t stream);
 

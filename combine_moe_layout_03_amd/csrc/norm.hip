@@ -17,19 +17,19 @@
 namespace moe {
 namespace {
 
-constexpr int kMaxWaves = 16;
-// Of a workgroup (select::norm_shape keeps to it; more of them would leave a lane too few registers).
-constexpr int max_waves(int chunks) { return chunks == 1 ? kMaxWaves : 8; }
+constexpr int kMaxWaves = 8;  // of a workgroup (select::norm_shape keeps to it)
+static_assert(select::norm_shape(MOE_MAX_HIDDEN).waves <= kMaxWaves && select::norm_shape(8192).waves <= kMaxWaves);
 
 // Eight elements as they lie in memory.
 template <Out kType>
 struct Chunk {
   u32x4 w[kType == Out::kF32 ? 2 : 1];
+  template <bool kNt>
   __device__ __forceinline__ void load(const void* base, int64_t elem) {
     const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(base) +
                                                     elem * (kType == Out::kF32 ? 4 : 2));
-    w[0] = p[0];
-    if constexpr (kType == Out::kF32) w[1] = p[1];
+    w[0] = kNt ? __builtin_nontemporal_load(p) : p[0];
+    if constexpr (kType == Out::kF32) w[1] = kNt ? __builtin_nontemporal_load(p + 1) : p[1];
   }
   __device__ __forceinline__ void get(float (&f)[8]) const {
 #pragma unroll
@@ -49,10 +49,15 @@ struct Chunk {
       get(f);
     }
   }
+  // Non-temporally: the rows read would else be pushed out of the caches by the
+  // rows written (h 7168, bf16, us, non-temporally and not, plus a copy of the
+  // results by the next kernel: 512 tokens 6.8 + 6.8, 7.9 + 5.9; 2048: 20.7 +
+  // 25.1, 28.6 + 16.0; 4096: 49.5 + 35.3, 51.3 + 34.3; the gradient 11.7, 12.5;
+  // 25.7, 28.2; 46.3, 48.2).
   __device__ __forceinline__ void store(void* base, int64_t elem) const {
     u32x4* p = reinterpret_cast<u32x4*>(static_cast<uint8_t*>(base) + elem * (kType == Out::kF32 ? 4 : 2));
-    p[0] = w[0];
-    if constexpr (kType == Out::kF32) p[1] = w[1];
+    __builtin_nontemporal_store(w[0], p);
+    if constexpr (kType == Out::kF32) __builtin_nontemporal_store(w[1], p + 1);
   }
 };
 
@@ -63,6 +68,13 @@ __device__ __forceinline__ void store_rounded(void* base, int64_t elem, float (&
   c.store(base, elem);
 }
 
+// Eight floats where they are read again soon.
+__device__ __forceinline__ void put_floats(float* to, const float (&f)[8]) {
+  f32x4* p = reinterpret_cast<f32x4*>(to);
+  p[0] = f32x4{f[0], f[1], f[2], f[3]};
+  p[1] = f32x4{f[4], f[5], f[6], f[7]};
+}
+
 __device__ __forceinline__ void load_weight(const float* weight, int col, float (&w)[8]) {
   const f32x4_u* p = reinterpret_cast<const f32x4_u*>(weight + col);
   const f32x4 a = p[0], b = p[1];
@@ -70,20 +82,21 @@ __device__ __forceinline__ void load_weight(const float* weight, int col, float 
   for (int q = 0; q < 4; ++q) w[q] = a[q], w[4 + q] = b[q];
 }
 
-// The sum of v over the row's waves, in every lane.
+// The sum of v over the row's waves, in every lane: of the workgroup's waves
+// those from `first` on.
 template <bool kOneWave>
-__device__ __forceinline__ float row_sum(float v, int waves, float* lds) {
+__device__ __forceinline__ float row_sum(float v, int waves, float* lds, int first) {
   v = token_sum<kWave>(v);
   if constexpr (kOneWave) return v;
   if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = v;
   __syncthreads();
   float s = 0.0f;
-  for (int q = 0; q < waves; ++q) s += lds[q];
+  for (int q = 0; q < waves; ++q) s += lds[first + q];
   return s;
 }
 
-template <Out kType, int kChunks, bool kOneWave>
-__global__ __launch_bounds__(kOneWave ? kWave* select::kNormRowsPerGroup : kWave* max_waves(kChunks)) void rms_norm_kernel(
+template <Out kType, int kChunks, bool kOneWave, bool kNt>
+__global__ __launch_bounds__(kOneWave ? kWave* select::kNormRowsPerGroup : kWave* kMaxWaves) void rms_norm_kernel(
     NormArgs a) {
   __shared__ float lds[kMaxWaves];
   const int waves = kOneWave ? 1 : blockDim.x / kWave;
@@ -97,8 +110,8 @@ __global__ __launch_bounds__(kOneWave ? kWave* select::kNormRowsPerGroup : kWave
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {  // (past the row's end its last chunk, which counts for nothing)
     const int c = min(lane + i * lanes, chunks - 1);
-    x[i].load(a.x, row + c * 8);
-    if (a.residual != nullptr) r[i].load(a.residual, row + c * 8);
+    x[i].template load<kNt>(a.x, row + c * 8);
+    if (a.residual != nullptr) r[i].template load<kNt>(a.residual, row + c * 8);
   }
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) load_weight(a.weight, min(lane + i * lanes, chunks - 1) * 8, w[i]);
@@ -120,7 +133,7 @@ __global__ __launch_bounds__(kOneWave ? kWave* select::kNormRowsPerGroup : kWave
       for (int q = 0; q < 8; ++q) squares = __builtin_fmaf(y[i][q], y[i][q], squares);
     }
   }
-  squares = row_sum<kOneWave>(squares, waves, lds);
+  squares = row_sum<kOneWave>(squares, waves, lds, 0);
   const float rstd = 1.0f / __builtin_sqrtf(squares / static_cast<float>(a.hidden) + a.eps);
   if (a.rstd != nullptr && lane == 0) a.rstd[t] = rstd;
 #pragma unroll
@@ -156,14 +169,19 @@ __global__ __launch_bounds__(kOneWave ? kWave* select::kNormRowsPerGroup : kWave
 
 // The gradient.  With xh = s rstd and gw = g w
 //   dx = rstd (gw - xh mean(gw xh)) + dsum,  dw = sum over the tokens of g xh
-// A workgroup takes every parts-th row; a lane has the same columns of each, so
-// its part of dw stays in registers, is written once and summed by the second
-// kernel, in a fixed order.
-template <Out kType, Out kGrad, int kChunks, bool kOneWave>
-__global__ __launch_bounds__(kOneWave ? kWave : kWave* max_waves(kChunks)) void rms_norm_backward_kernel(NormBackwardArgs a) {
+// A workgroup takes kRows rows at a time (as many as eight waves hold), and of
+// the batch every parts-th such set.  A lane has the same columns of each row,
+// so its part of dw stays in registers; the rows' parts are joined in LDS,
+// written once, and summed by the second kernel, all in a fixed order.  The
+// rows' chunks are loaded while the rows before them are summed (not where a
+// lane has four chunks of each: the registers spill).
+template <Out kType, Out kGrad, int kChunks, bool kOneWave, bool kNt>
+__global__ __launch_bounds__(kWave* kMaxWaves) void rms_norm_backward_kernel(NormBackwardArgs a, int waves) {
   __shared__ float lds[2][kMaxWaves];
-  const int waves = kOneWave ? 1 : blockDim.x / kWave;
-  const int lane = threadIdx.x, lanes = waves * kWave;
+  __shared__ __attribute__((aligned(16))) float joined[select::kNormJoinedHidden];
+  if constexpr (kOneWave) waves = 1;
+  const int lanes = waves * kWave, rows = blockDim.x / lanes;
+  const int lane = threadIdx.x % lanes, group = uniform(threadIdx.x / lanes);
   const int chunks = a.hidden / 8;
   float w[kChunks][8], dw[kChunks][8];
 #pragma unroll
@@ -172,70 +190,106 @@ __global__ __launch_bounds__(kOneWave ? kWave : kWave* max_waves(kChunks)) void 
 #pragma unroll
     for (int q = 0; q < 8; ++q) dw[i][q] = 0.0f;
   }
+  struct Row {
+    Chunk<kGrad> g[kChunks];
+    Chunk<kType> s[kChunks], skip[kChunks];
+    float rstd;
+    bool keep;
+  };
+  const auto load = [&](int64_t t, Row& r) {  // (past the batch its last row, which counts for nothing)
+    t = t < a.bs ? t : a.bs - 1;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const int64_t at = t * a.hidden + min(lane + i * lanes, chunks - 1) * 8;
+      r.g[i].template load<kNt>(a.grad_out, at);
+      r.s[i].template load<kNt>(a.sum, at);
+      if (a.grad_sum != nullptr) r.skip[i].template load<kNt>(a.grad_sum, at);
+    }
+    r.rstd = a.rstd[t];
+    r.keep = a.token_mask == nullptr || a.token_mask[t] != 0;  // the same in every lane of a row
+  };
   const float mean = 1.0f / static_cast<float>(a.hidden);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * rows;
   int turn = 0;
-  for (int64_t t = blockIdx.x; t < a.bs; t += gridDim.x) {
-    const int64_t row = t * a.hidden;
-    if (a.token_mask != nullptr && a.token_mask[t] == 0) {  // the same in every lane
-      float zero[8] = {};
-#pragma unroll
-      for (int i = 0; i < kChunks; ++i)
-        if (lane + i * lanes < chunks) store_rounded<kType>(a.grad_x, row + (lane + i * lanes) * 8, zero);
-      continue;
-    }
-    Chunk<kGrad> gc[kChunks];
-    Chunk<kType> sc[kChunks], skip[kChunks];
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      const int c = min(lane + i * lanes, chunks - 1);
-      gc[i].load(a.grad_out, row + c * 8);
-      sc[i].load(a.sum, row + c * 8);
-      if (a.grad_sum != nullptr) skip[i].load(a.grad_sum, row + c * 8);
-    }
-    const float rstd = a.rstd[t];
+  Row next;
+  if constexpr (kChunks <= 2) load(static_cast<int64_t>(blockIdx.x) * rows + group, next);
+  for (int64_t first = static_cast<int64_t>(blockIdx.x) * rows; first < a.bs; first += step) {
+    const int64_t t = first + group;
+    if constexpr (kChunks > 2) load(t, next);
+    const Row now = next;
+    if constexpr (kChunks <= 2) load(t + step, next);
+    const bool counts = now.keep && t < a.bs;
     float g[kChunks][8], xh[kChunks][8], dot = 0.0f;
+    if (counts) {
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      gc[i].get(g[i]);
-      sc[i].get(xh[i]);
-      const bool mine = lane + i * lanes < chunks;
+      for (int i = 0; i < kChunks; ++i) {
+        now.g[i].get(g[i]);
+        now.s[i].get(xh[i]);
+        const bool mine = lane + i * lanes < chunks;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        xh[i][q] *= rstd;
-        dw[i][q] = __builtin_fmaf(g[i][q], xh[i][q], dw[i][q]);
-        g[i][q] *= w[i][q];
-        if (mine) dot = __builtin_fmaf(g[i][q], xh[i][q], dot);
+        for (int q = 0; q < 8; ++q) {
+          xh[i][q] *= now.rstd;
+          dw[i][q] = __builtin_fmaf(g[i][q], xh[i][q], dw[i][q]);
+          g[i][q] *= w[i][q];
+          if (mine) dot = __builtin_fmaf(g[i][q], xh[i][q], dot);
+        }
       }
     }
-    dot = row_sum<kOneWave>(dot, waves, lds[turn]) * mean;
+    // the row's waves: `waves` of the workgroup's from group * waves on
+    dot = row_sum<kOneWave>(dot, waves, lds[turn], group * waves) * mean;
     turn ^= 1;  // the other sums may still be read
+    if (t >= a.bs) continue;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
       float f[8], s[8] = {};
-      if (a.grad_sum != nullptr) skip[i].get(s);
+      if (a.grad_sum != nullptr) now.skip[i].get(s);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) f[q] = (g[i][q] - xh[i][q] * dot) * rstd + s[q];
-      if (lane + i * lanes < chunks) store_rounded<kType>(a.grad_x, row + (lane + i * lanes) * 8, f);
+      for (int q = 0; q < 8; ++q) f[q] = counts ? (g[i][q] - xh[i][q] * dot) * now.rstd + s[q] : 0.0f;
+      if (lane + i * lanes < chunks) store_rounded<kType>(a.grad_x, t * a.hidden + (lane + i * lanes) * 8, f);
     }
   }
   if (a.grad_weight == nullptr) return;
+  for (int r = 1; r < rows; ++r) {  // the first row's lanes add the others'
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+      if (group == r && lane + i * lanes < chunks) put_floats(joined + (lane + i * lanes) * 8, dw[i]);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      if (group != 0 || lane + i * lanes >= chunks) continue;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) dw[i][q] += joined[(lane + i * lanes) * 8 + q];
+    }
+  }
+  if (group != 0) return;
   float* part = a.partial + static_cast<int64_t>(blockIdx.x) * a.hidden;
 #pragma unroll
   for (int i = 0; i < kChunks; ++i)
-    if (lane + i * lanes < chunks) store_rounded<Out::kF32>(part, (lane + i * lanes) * 8, dw[i]);
+    if (lane + i * lanes < chunks) put_floats(part + (lane + i * lanes) * 8, dw[i]);
 }
 
 // Sums the parts: a workgroup has 64 columns, a wave every kSumWaves-th part of
-// them, and the waves' sums are added in order.
-constexpr int kSumWaves = 8;
+// them, kSumDeep loads at a time, and the waves' sums are added in order.
+constexpr int kSumWaves = 16, kSumDeep = 8;
 __global__ __launch_bounds__(kWave* kSumWaves) void rms_norm_weight_sum_kernel(const float* partial, int32_t parts,
                                                                               int32_t hidden, float* grad_weight) {
   __shared__ float lds[kSumWaves][kWave];
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int col = blockIdx.x * kWave + lane;
+  const float* src = partial + min(col, hidden - 1);
   float s = 0.0f;
-  if (col < hidden)
-    for (int p = wave; p < parts; p += kSumWaves) s += partial[static_cast<int64_t>(p) * hidden + col];
+  for (int p0 = wave; p0 < parts; p0 += kSumWaves * kSumDeep) {
+    float v[kSumDeep];
+#pragma unroll
+    for (int q = 0; q < kSumDeep; ++q) {
+      const int p = p0 + q * kSumWaves;
+      v[q] = src[static_cast<int64_t>(min(p, parts - 1)) * hidden];
+      if (p >= parts) v[q] = 0.0f;
+    }
+#pragma unroll
+    for (int q = 0; q < kSumDeep; ++q) s += v[q];
+  }
   lds[wave][lane] = s;
   __syncthreads();
   if (wave != 0 || col >= hidden) return;
@@ -244,26 +298,27 @@ __global__ __launch_bounds__(kWave* kSumWaves) void rms_norm_weight_sum_kernel(c
   grad_weight[col] = s;
 }
 
-// f(chunks, one wave) with the shape as compile-time constants.
+// f(chunks, one wave, non-temporal loads) with the shape as compile-time
+// constants.
+template <int kChunks, bool kOneWave, bool kNt, typename F>
+hipError_t call_shape(F f) {
+  return f(std::integral_constant<int, kChunks>{}, std::bool_constant<kOneWave>{}, std::bool_constant<kNt>{});
+}
 template <typename F>
-hipError_t with_norm_shape(select::NormShape s, F f) {
-  const auto chunks = [&](auto one) {
-    switch (s.chunks) {
-      case 1: return f(std::integral_constant<int, 1>{}, one);
-      case 2: return f(std::integral_constant<int, 2>{}, one);
-      case 4: return f(std::integral_constant<int, 4>{}, one);
-    }
-    return hipErrorInvalidValue;
-  };
-  return s.waves == 1 ? chunks(std::true_type{}) : chunks(std::false_type{});
+hipError_t with_norm_shape(select::NormShape s, bool nt, F f) {
+  if (s.chunks == 1) return call_shape<1, true, false>(f);
+  if (s.waves == 1) return call_shape<2, true, false>(f);
+  if (s.chunks == 2) return nt ? call_shape<2, false, true>(f) : call_shape<2, false, false>(f);
+  return nt ? call_shape<4, false, true>(f) : call_shape<4, false, false>(f);
 }
 
 template <Out kType>
 hipError_t launch_norm_type(const NormArgs& a, hipStream_t stream) {
-  const select::NormShape s = select::norm_shape(a.bs, a.hidden);
-  return with_norm_shape(s, [&](auto chunks, auto one) {
+  const select::NormShape s = select::norm_shape(a.hidden);
+  const int64_t read = static_cast<int64_t>(a.bs) * a.hidden * (kType == Out::kF32 ? 4 : 2) * (a.residual != nullptr ? 2 : 1);
+  return with_norm_shape(s, select::norm_nt(read), [&](auto chunks, auto one, auto nt) {
     constexpr int kRows = decltype(one)::value ? select::kNormRowsPerGroup : 1;
-    rms_norm_kernel<kType, decltype(chunks)::value, decltype(one)::value>
+    rms_norm_kernel<kType, decltype(chunks)::value, decltype(one)::value, decltype(nt)::value>
         <<<dim3((a.bs + kRows - 1) / kRows), dim3(kWave * (kRows > 1 ? kRows : s.waves)), 0, stream>>>(a);
     return hipGetLastError();
   });
@@ -271,13 +326,16 @@ hipError_t launch_norm_type(const NormArgs& a, hipStream_t stream) {
 
 template <Out kType, Out kGrad>
 hipError_t launch_backward_types(const NormBackwardArgs& a, hipStream_t stream) {
-  const select::NormShape s = select::norm_backward_shape(a.bs, a.hidden);
-  const int32_t parts = select::norm_backward_parts(a.bs);
-  const hipError_t e = a.bs == 0 ? hipSuccess : with_norm_shape(s, [&](auto chunks, auto one) {
-    rms_norm_backward_kernel<kType, kGrad, decltype(chunks)::value, decltype(one)::value>
-        <<<dim3(parts), dim3(kWave * s.waves), 0, stream>>>(a);
+  const select::NormShape s = select::norm_shape(a.hidden);
+  const int32_t parts = select::norm_backward_parts(a.bs, a.hidden);
+  const int64_t read = static_cast<int64_t>(a.bs) * a.hidden *
+                       ((kType == Out::kF32 ? 4 : 2) * (a.grad_sum != nullptr ? 2 : 1) + (kGrad == Out::kF32 ? 4 : 2));
+  const auto launch = [&](auto chunks, auto one, auto nt) {
+    rms_norm_backward_kernel<kType, kGrad, decltype(chunks)::value, decltype(one)::value, decltype(nt)::value>
+        <<<dim3(parts), dim3(kWave * s.waves * select::norm_backward_rows(s.waves)), 0, stream>>>(a, s.waves);
     return hipGetLastError();
-  });
+  };
+  const hipError_t e = a.bs == 0 ? hipSuccess : with_norm_shape(s, select::norm_nt(read), launch);
   if (e != hipSuccess || a.grad_weight == nullptr) return e;
   rms_norm_weight_sum_kernel<<<dim3((a.hidden + kWave - 1) / kWave), dim3(kWave * kSumWaves), 0, stream>>>(
       a.partial, parts, a.hidden, a.grad_weight);

@@ -589,7 +589,7 @@ int moe_rms_norm(const void* x, const void* residual, moe_dtype type, const floa
 
 /* Bytes of workspace that moe_rms_norm_backward needs to give the weight's
  * gradient (the query-size, caller-allocates convention of page section 6.7):
- * 4 * hidden for each of up to 512 parts of the batch.  Host only. */
+ * 4 * hidden for each of up to 256 parts of the batch.  Host only. */
 int moe_rms_norm_backward_workspace_bytes(int32_t bs, int32_t hidden, size_t* bytes);
 
 /* The norm's gradient (no counterpart on the pages): with g = gradOut, xh = s *
