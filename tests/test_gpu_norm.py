@@ -286,3 +286,27 @@ def test_norm_backward_against_differences():
         # the differences are off by about step^2, the gradients by some 70 roundings of their terms
         bound = 70 * B.U * ((np.abs(g) * w).sum() * 4 + np.abs(host(dw) * e).sum() + np.abs(host(dx) * d).sum()) + 1e-6
         assert abs(slope / (2 * step) - got) <= bound
+
+
+@pytest.mark.parametrize("kind,bs,h", [("bf16", 4100, 7168), ("fp32", 1700, 8208), ("fp16", 900, 16384), ("fp32", 30000, 1040)])
+def test_norm_large_batches(kind, bs, h):
+    """Batches of more than the caches keep (their rows are loaded in another way), some rows of each."""
+    log(f"rms_norm large {kind} {bs} {h}")
+    gen = torch.Generator(device="cuda").manual_seed(h)
+    x, r, g, k = (torch.randn((bs, h), device="cuda", generator=gen).to(B.TYPES[kind]) for _ in range(4))
+    w = torch.rand(h, device="cuda", generator=gen) + 0.5
+    s, out, buf, rstd = run(x, r, w, 1e-6, kind, True, True)
+    assert torch.equal(s, (x.float() + r.float()).to(x.dtype))
+    some = sorted({0, 1, bs // 2, bs - 2, bs - 1} | set(np.random.default_rng(h).integers(0, bs, 20).tolist()))
+    y, want = B.norm(host(s[some]), host(w), 1e-6)
+    assert B.near(host(out[some]), y, kind, B.NORM * np.abs(y)) and (np.abs(host(rstd[some]) - want) <= B.RSTD * want).all()
+    B.check_rows(*B.unpack(buf.view(bs, -1)[some].contiguous(), len(some), h), y, B.NORM * np.abs(y))
+    dx, dw = torch.full_like(s, 7), torch.full((h,), 7.0, device="cuda")
+    ws = torch.full((M.moe_rms_norm_backward_workspace_bytes(bs, h),), 0xFF, dtype=torch.uint8, device="cuda")
+    M.moe_rms_norm_backward(g, s, w, rstd, dx, grad_sum=k, grad_weight=dw, workspace=ws)
+    torch.cuda.synchronize()
+    dxs, err, _, _ = B.norm_backward(host(g[some]), host(s[some]), host(w), host(rstd[some]), host(k[some]))
+    assert B.near(host(dx[some]), dxs, kind, err)
+    terms = g.double() * s.double() * rstd.double()[:, None]
+    bound = (bs + 8) * B.U * terms.abs().sum(dim=0)
+    assert ((dw.double() - terms.sum(dim=0)).abs() <= bound).all()
