@@ -223,11 +223,13 @@ def _recv_code(dtype: torch.dtype) -> int:
     return MOE_E4M3_BLOCKSCALE if dtype is torch.float8_e4m3fn else dtype_code(dtype)
 
 
-def _row_type(x: torch.Tensor) -> Tuple[int, int, int]:
+def _row_type(x: torch.Tensor, quant_int8: bool) -> Tuple[int, int, int]:
     """(bs, hidden, type) of the rows that dispatch takes; e4m3 rows (bytes) are moved as 16-bit ones."""
     bs, hidden = x.shape
     if x.dtype is not torch.uint8:
         return bs, hidden, dtype_code(x.dtype)
+    if quant_int8:
+        raise ValueError("e4m3 rows are dispatched as they are (quant_int8 False)")
     if hidden % 128:
         raise ValueError("e4m3 rows are whole lines of 128 bytes")
     return bs, hidden // 2, MOE_BF16
@@ -316,7 +318,7 @@ def moe_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, send_token_idx: torch.
     False), which are copied whole."""
     if x.dim() != 2 or topk_idx.dim() != 2:
         raise ValueError("x must be [bs, hidden] and topk_idx [bs, topk]")
-    bs, hidden, x_type = _row_type(x)
+    bs, hidden, x_type = _row_type(x, quant_int8)
     topk = topk_idx.shape[1]
     _need(send_token_idx, "send_token_idx", bs * topk)
     _need_routes(expert_num_per_rank, rank_size, put_offset, recv_base)
@@ -376,7 +378,7 @@ def moe_dispatch_src(x: torch.Tensor, topk_idx: torch.Tensor, send_token_idx: to
     """Dispatch of source ``src_rank``; put_offset is [E, num_src]."""
     if x.dim() != 2 or topk_idx.dim() != 2 or put_offset.dim() != 2:
         raise ValueError("x must be [bs, hidden], topk_idx [bs, topk], put_offset [E, num_src]")
-    bs, hidden, x_type = _row_type(x)
+    bs, hidden, x_type = _row_type(x, quant_int8)
     topk = topk_idx.shape[1]
     _need(send_token_idx, "send_token_idx", bs * topk)
     _need_routes(expert_num_per_rank, rank_size, put_offset, recv_base, put_offset.shape[1])
@@ -427,7 +429,7 @@ def moe_layout_notify_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, expert_n
                                workspace: torch.Tensor, stream=None) -> None:
     if x.dim() != 2 or topk_idx.dim() != 2:
         raise ValueError("x must be [bs, hidden] and topk_idx [bs, topk]")
-    bs, hidden, x_type = _row_type(x)
+    bs, hidden, x_type = _row_type(x, quant_int8)
     topk = topk_idx.shape[1]
     _need_layout(bs, topk, expert_num_per_rank, rank_size, token_per_expert, token_per_rank, send_token_idx,
                  bad_id_count)
@@ -688,6 +690,12 @@ def moe_grouped_gemm_deq_i8(a: torch.Tensor, a_row_bytes: int, rows: int, k: int
         _dev(out, "out"), dtype_code(out.dtype), out.nbytes, _stream(stream)))
 
 
+def _on_current_device(t: torch.Tensor, name: str) -> None:
+    """Raise if t lies on another device than the current one, on whose stream the call would run."""
+    if _raw_device is not None and t.get_device() != _raw_device():
+        raise ValueError(f"{name} is on another device than the current one")
+
+
 def _row_matrix(t: torch.Tensor, name: str, shape, dtype=None):
     """The device pointer of an optional matrix of ``shape``."""
     if t is None:
@@ -709,6 +717,7 @@ def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Op
     MOE_E4M3_BLOCKSCALE) bytes each, a scale for each 128 columns).  rstd
     float32 [bs] gets 1 / sqrt(...), for ``moe_rms_norm_backward``."""
     px = _dev(x, "x")
+    _on_current_device(x, "x")
     shape, dtype = x.shape, x.dtype
     if len(shape) != 2:
         raise ValueError("x must be [bs, hidden]")
@@ -741,6 +750,7 @@ def moe_rms_norm_backward(grad_out: torch.Tensor, sum: torch.Tensor, weight: tor
     needs a workspace of moe_rms_norm_backward_workspace_bytes(bs, hidden)
     bytes.  token_mask (uint8 or bool [bs]) takes a token out where it is 0."""
     pg = _dev(grad_out, "grad_out")
+    _on_current_device(grad_out, "grad_out")
     shape, dtype = sum.shape, sum.dtype
     if len(shape) != 2 or grad_out.shape != shape:
         raise ValueError("grad_out and sum must be [bs, hidden]")
@@ -785,6 +795,7 @@ def _gemm_f8_sizes(a, a_row_bytes, rows, k, group_count, w, weight_scale, token_
         raise ValueError("token_scale must be contiguous float32 or bytes")
     if not token_scale.is_cuda:
         raise ValueError("token_scale must be a device tensor")
+    _on_current_device(token_scale, "token_scale")
     if rows > 0 and token_scale.nbytes < (rows - 1) * token_scale_stride + 4 * blocks:
         raise ValueError(f"token_scale holds {token_scale.nbytes} bytes, rows at stride {token_scale_stride} need "
                          f"{(rows - 1) * token_scale_stride + 4 * blocks}")

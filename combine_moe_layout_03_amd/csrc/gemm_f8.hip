@@ -63,7 +63,7 @@ __device__ __forceinline__ void store_columns(const GemmF8Args& a, int64_t row, 
 // kSplit parts of kWaves waves share out the chunks of k, and the first adds
 // the others' sums.
 template <Form kForm, int kMI, int kNW, int kWaves, int kKC, int kSplit>
-__global__ __launch_bounds__(kWave* kWaves* kSplit) void stream_f8_kernel(GemmF8Args a, int64_t slots) {
+__global__ __launch_bounds__(kWave* kWaves* kSplit, 2) void stream_f8_kernel(GemmF8Args a, int64_t slots) {
   constexpr bool kGated = kForm == Form::kAct;
   constexpr int kHalves = kGated ? 2 : 1, kNI = kHalves * kNW;  // fragments of a wave: gate, then up
   constexpr int kThreads = kWave * kWaves, kCols = 16 * kNW * kWaves, kRows = 16 * kMI;
@@ -350,8 +350,13 @@ struct TileWave {
   int piece, k;  // (the piece of load 0)
   // kTileWaves is even: q turns the bit of swizzle() that rows 16 apart differ in.
   __device__ __forceinline__ int piece_of(int q) const { return piece ^ ((q * (kTileWaves / 2) & 1) << 1); }
+  // The tile of 256 x 256 has no registers left for its loads' offsets and makes
+  // them anew each time, of the last row (of weights) that exists and the stride.
+  static constexpr bool kAnew = kTileM * kTileN == 256 * 256;
   const uint8_t *base_a, *base_b;
-  uint32_t src_a[kLoadsA], src_b[kLoadsB];
+  uint32_t src_a[kAnew ? 1 : kLoadsA], src_b[kAnew ? 1 : kLoadsB];
+  int last_a, last_b;
+  uint32_t stride_a;
   const float* ts_row;        // the scales of the wave's row lane % kWaveM
   const float* ws[kHalves];   // of its columns
   // Fragments: pair p, tile t of the weights is row 32 p + 8 (l16 / 4) + 4 t +
@@ -381,13 +386,14 @@ struct TileWave {
     piece = (lane % 8) ^ swizzle(kRowsPerLoad * wave + lane / 8);
     base_a = a.a + row0 * a.a_stride;
     base_b = a.w + (static_cast<int64_t>(rs.group) * kHalves * a.n + col0) * a.k;
+    last_a = row_end - row0 - 1, last_b = a.n - 1 - col0, stride_a = static_cast<uint32_t>(a.a_stride);
 #pragma unroll
-    for (int q = 0; q < kLoadsA; ++q) {
+    for (int q = 0; q < (kAnew ? 0 : kLoadsA); ++q) {
       const int r = kRowsPerLoad * (q * kTileWaves + wave) + lane / 8;
       src_a[q] = static_cast<uint32_t>(tile_row(row0, row_end, r) - row0) * static_cast<uint32_t>(a.a_stride) + piece_of(q) * 16;
     }
 #pragma unroll
-    for (int q = 0; q < kLoadsB; ++q) {
+    for (int q = 0; q < (kAnew ? 0 : kLoadsB); ++q) {
       const int r = kRowsPerLoad * (q * kTileWaves + wave) + lane / 8;
       constexpr int kPart = kWaveN / kHalves;
       const int half = r % kWaveN / kPart, c = r / kWaveN * kPart + r % kPart;
@@ -410,15 +416,30 @@ struct TileWave {
   // Stages past the last one load it again, into slots that are not read; a
   // piece past k reads the row's first piece (its row fragments count as zero).
   template <bool kTail, int kLoads>
-  __device__ __forceinline__ void issue(int s, const uint8_t* base, const uint32_t (&src)[kLoads], uint8_t* buf) const {
+  __device__ __forceinline__ void issue(int s, const uint8_t* base, const uint32_t* src, int last, uint32_t stride,
+                                        uint8_t* buf) const {
     const int k0 = min(s, stages - 1) * kSK;
+    int first = kRowsPerLoad * wave + lane / 8;
+    if constexpr (kAnew) asm volatile("" : "+v"(first));  // else the offsets are made once and kept
 #pragma unroll
     for (int q = 0; q < kLoads; ++q) {
+      uint32_t at;
+      if constexpr (kAnew)
+        at = static_cast<uint32_t>(min(kRowsPerLoad * kTileWaves * q + first, last)) * stride + piece_of(q) * 16;
+      else at = src[q];
       const uint8_t* p;
-      if constexpr (kTail) p = base + (src[q] + static_cast<uint32_t>((k0 + piece_of(q) * 16 < k) ? k0 : -piece_of(q) * 16));
-      else p = base + k0 + src[q];
+      if constexpr (kTail) p = base + (at + static_cast<uint32_t>((k0 + piece_of(q) * 16 < k) ? k0 : -piece_of(q) * 16));
+      else p = base + k0 + at;
       __builtin_amdgcn_global_load_lds(p, (MOE_LDS void*)(buf + (q * kTileWaves + wave) * kRowsPerLoad * kSK), 16, 0, 0);
     }
+  }
+  template <bool kTail>
+  __device__ __forceinline__ void issue_a(int s, uint8_t* buf) const {
+    issue<kTail, kLoadsA>(s, base_a, src_a, last_a, stride_a, buf);
+  }
+  template <bool kTail>
+  __device__ __forceinline__ void issue_b(int s, uint8_t* buf) const {
+    issue<kTail, kLoadsB>(s, base_b, src_b, last_b, static_cast<uint32_t>(k), buf);
   }
   // The two pieces of fragment i of a stage's rows, and j of its weights.
   __device__ __forceinline__ void read_a(const uint8_t* buf, int i, i32x4 (&to)[2]) const {
@@ -586,8 +607,8 @@ __global__ __launch_bounds__(kWave* kWavesM* kWavesN) void tile_f8_kernel(GemmF8
   // Half of a stage's columns.
   auto step = [&](int S, int h, float ts, float w, const uint8_t* ca, const uint8_t* cb, uint8_t* fill_a,
                   uint8_t* fill_b) {
-    if (h == 0) t.template issue<kTail>(S + 1, t.base_a, t.src_a, fill_a);  // into the slot A(S - 1) used
-    else t.template issue<kTail>(S + 2, t.base_b, t.src_b, fill_b);         // into the slot B(S - 1) used
+    if (h == 0) t.template issue_a<kTail>(S + 1, fill_a);  // into the slot A(S - 1) used
+    else t.template issue_b<kTail>(S + 2, fill_b);         // into the slot B(S - 1) used
     i32x4 ra[kMI][2], rb[kStepNI][2];
     if (h == 0) {
 #pragma unroll
@@ -632,9 +653,9 @@ __global__ __launch_bounds__(kWave* kWavesM* kWavesN) void tile_f8_kernel(GemmF8
   next_col_scales = load_col_scales(0);
 #pragma unroll
   for (int u = 0; u < 2; ++u) row_scale[u] = t.ts_row[min(u, stages - 1)];
-  t.template issue<kTail>(0, t.base_b, t.src_b, sb0);
-  t.template issue<kTail>(0, t.base_a, t.src_a, sa0);
-  t.template issue<kTail>(1, t.base_b, t.src_b, sb1);
+  t.template issue_b<kTail>(0, sb0);
+  t.template issue_a<kTail>(0, sa0);
+  t.template issue_b<kTail>(1, sb1);
   __builtin_amdgcn_s_waitcnt(vmcnt_wait(T::kLoadsB));
   tile_barrier();
   const int grp = t.wave / 4;
@@ -666,7 +687,7 @@ __global__ __launch_bounds__(kWave* kWavesM* kWavesN) void tile_f8_kernel(GemmF8
   store_tile(a, t, acc, sb0, sb1, sa1);
 }
 
-// A ring of kSlots stages in LDS, of which one is multiplied while the others'
+// A ring of three stages in LDS, of which one is multiplied while the others'
 // loads run; the waves meet once a stage.  For the widened codes the vector ALU
 // has nearly as much to do as the matrix cores (16 conversions a fragment, 4
 // multiply-adds for each 4 matrix instructions), and overlaps with them freely.
@@ -681,22 +702,19 @@ struct FragmentOf<true> {
   static __device__ __forceinline__ Type make(const i32x4 (&r)[2]) { return widen(r[0], r[1]); }
 };
 
-template <Form kForm, bool kWide, int kTileM, int kTileN, int kWavesM, int kWavesN, int kSlots, bool kTail>
-__global__ __launch_bounds__(kWave* kWavesM* kWavesN) void ring_f8_kernel(GemmF8Args a) {
+template <Form kForm, bool kWide, int kTileM, int kTileN, int kWavesM, int kWavesN, bool kTail>
+__global__ __launch_bounds__(kWave* kWavesM* kWavesN, 2) void ring_f8_kernel(GemmF8Args a) {
   using T = TileWave<kForm, kTileM, kTileN, kWavesM, kWavesN>;
   using F = FragmentOf<kWide>;
-  constexpr int kMI = T::kMI, kNI = T::kNI;
-  static_assert(kSlots == 3 || kSlots == 4, "the slots declared below");
+  constexpr int kMI = T::kMI, kNI = T::kNI, kSlots = 3;
   __shared__ __attribute__((aligned(1024))) uint8_t sa0[kTileM * kSK];
   __shared__ __attribute__((aligned(1024))) uint8_t sa1[kTileM * kSK];
   __shared__ __attribute__((aligned(1024))) uint8_t sa2[kTileM * kSK];
-  __shared__ __attribute__((aligned(1024))) uint8_t sa3[kSlots == 4 ? kTileM * kSK : 16];
   __shared__ __attribute__((aligned(1024))) uint8_t sb0[kTileN * kSK];
   __shared__ __attribute__((aligned(1024))) uint8_t sb1[kTileN * kSK];
   __shared__ __attribute__((aligned(1024))) uint8_t sb2[kTileN * kSK];
-  __shared__ __attribute__((aligned(1024))) uint8_t sb3[kSlots == 4 ? kTileN * kSK : 16];
   constexpr int kScaleFloats = (kTileM + kWave - 1) / kWave * kWave + kWave;
-  __shared__ float ss0[kScaleFloats], ss1[kScaleFloats], ss2[kScaleFloats], ss3[kSlots == 4 ? kScaleFloats : 1];
+  __shared__ float ss0[kScaleFloats], ss1[kScaleFloats], ss2[kScaleFloats];
   T t;
   if (!t.set(a)) return;  // the whole workgroup
   const int stages = t.stages;
@@ -721,13 +739,12 @@ __global__ __launch_bounds__(kWave* kWavesM* kWavesN) void ring_f8_kernel(GemmF8
   }
   const int scale_at = t.wave < kRowWaves ? t.wave * kWave : kRowWaves * kWave;
   const auto issue = [&](int S, uint8_t* to_a, uint8_t* to_b, float* to_s) {
-    t.template issue<kTail>(S, t.base_b, t.src_b, to_b);
-    t.template issue<kTail>(S, t.base_a, t.src_a, to_a);
+    t.template issue_b<kTail>(S, to_b);
+    t.template issue_a<kTail>(S, to_a);
     __builtin_amdgcn_global_load_lds(scale_src + min(S, stages - 1), (MOE_LDS void*)(to_s + scale_at), 4, 0, 0);
   };
   issue(0, sa0, sb0, ss0);
   issue(1, sa1, sb1, ss1);
-  if constexpr (kSlots == 4) issue(2, sa2, sb2, ss2);
   __builtin_amdgcn_s_waitcnt(vmcnt_wait((kSlots - 2) * kLoads));
   tile_barrier();
   auto stage = [&](int S, const uint8_t* ca, const uint8_t* cb, const float* cs, uint8_t* fill_a, uint8_t* fill_b,
@@ -785,25 +802,13 @@ __global__ __launch_bounds__(kWave* kWavesM* kWavesN) void ring_f8_kernel(GemmF8
   };
   const int rounds = stages / kSlots, rest = stages - rounds * kSlots;
   int S = 0;
-  if constexpr (kSlots == 3) {
-    for (int r = 0; r < rounds; ++r, S += 3) {
-      stage(S, sa0, sb0, ss0, sa2, sb2, ss2);
-      stage(S + 1, sa1, sb1, ss1, sa0, sb0, ss0);
-      stage(S + 2, sa2, sb2, ss2, sa1, sb1, ss1);
-    }
-    if (rest > 0) stage(S, sa0, sb0, ss0, sa2, sb2, ss2);
-    if (rest > 1) stage(S + 1, sa1, sb1, ss1, sa0, sb0, ss0);
-  } else {
-    for (int r = 0; r < rounds; ++r, S += 4) {
-      stage(S, sa0, sb0, ss0, sa3, sb3, ss3);
-      stage(S + 1, sa1, sb1, ss1, sa0, sb0, ss0);
-      stage(S + 2, sa2, sb2, ss2, sa1, sb1, ss1);
-      stage(S + 3, sa3, sb3, ss3, sa2, sb2, ss2);
-    }
-    if (rest > 0) stage(S, sa0, sb0, ss0, sa3, sb3, ss3);
-    if (rest > 1) stage(S + 1, sa1, sb1, ss1, sa0, sb0, ss0);
-    if (rest > 2) stage(S + 2, sa2, sb2, ss2, sa1, sb1, ss1);
+  for (int r = 0; r < rounds; ++r, S += 3) {
+    stage(S, sa0, sb0, ss0, sa2, sb2, ss2);
+    stage(S + 1, sa1, sb1, ss1, sa0, sb0, ss0);
+    stage(S + 2, sa2, sb2, ss2, sa1, sb1, ss1);
   }
+  if (rest > 0) stage(S, sa0, sb0, ss0, sa2, sb2, ss2);
+  if (rest > 1) stage(S + 1, sa1, sb1, ss1, sa0, sb0, ss0);
   // no load may still be writing this workgroup's LDS
   __builtin_amdgcn_s_waitcnt(vmcnt_wait(0));
   tile_barrier();
@@ -826,14 +831,14 @@ hipError_t launch_tile(const GemmF8Args& a, hipStream_t stream) {
   else tile_f8_kernel<kForm, kTileM, kTileN, kWavesM, kWavesN, false><<<grid, block, 0, stream>>>(a);
   return hipGetLastError();
 }
-template <Form kForm, bool kWide, int kTileM, int kTileN, int kWavesM, int kWavesN, int kSlots>
+template <Form kForm, bool kWide, int kTileM, int kTileN, int kWavesM, int kWavesN>
 hipError_t launch_ring(const GemmF8Args& a, hipStream_t stream) {
   const dim3 grid(static_cast<uint32_t>(tile_blocks(a.rows, a.groups, a.n, kTileM, tile_cols(kForm, kTileN))));
   const dim3 block(kWave * kWavesM * kWavesN);
   if (a.k % kSK != 0)
-    ring_f8_kernel<kForm, kWide, kTileM, kTileN, kWavesM, kWavesN, kSlots, true><<<grid, block, 0, stream>>>(a);
+    ring_f8_kernel<kForm, kWide, kTileM, kTileN, kWavesM, kWavesN, true><<<grid, block, 0, stream>>>(a);
   else
-    ring_f8_kernel<kForm, kWide, kTileM, kTileN, kWavesM, kWavesN, kSlots, false><<<grid, block, 0, stream>>>(a);
+    ring_f8_kernel<kForm, kWide, kTileM, kTileN, kWavesM, kWavesN, false><<<grid, block, 0, stream>>>(a);
   return hipGetLastError();
 }
 
@@ -843,10 +848,10 @@ hipError_t launch_form(const GemmF8Args& a, hipStream_t stream) {
   constexpr bool kWide = kForm == Form::kF32;
   switch (select::gemm_f8_kind(a.rows, a.groups, a.n)) {
     case select::GemmF8Kind::kSplit16: return launch_stream<kForm, 1, 1, 1, 256, 4>(a, stream);
-    case select::GemmF8Kind::kTile32: return launch_ring<kForm, kWide, 32, 128, 1, 2, 3>(a, stream);
-    case select::GemmF8Kind::kTile64: return launch_ring<kForm, kWide, 64, 128, 2, 2, 3>(a, stream);
+    case select::GemmF8Kind::kTile32: return launch_ring<kForm, kWide, 32, 128, 1, 2>(a, stream);
+    case select::GemmF8Kind::kTile64: return launch_ring<kForm, kWide, 64, 128, 2, 2>(a, stream);
     case select::GemmF8Kind::kTile256:
-      if constexpr (kWide) return launch_ring<kForm, true, 256, 128, 4, 2, 3>(a, stream);
+      if constexpr (kWide) return launch_ring<kForm, true, 256, 128, 4, 2>(a, stream);
       else return launch_tile<kForm, 256, 256, 4, 2>(a, stream);
   }
   return hipErrorInvalidValue;
@@ -854,8 +859,8 @@ hipError_t launch_form(const GemmF8Args& a, hipStream_t stream) {
 hipError_t launch_act(const GemmF8Args& a, hipStream_t stream) {
   switch (select::gemm_f8_act_kind(a.rows, a.groups, a.n)) {
     case select::GemmF8Kind::kSplit16: return launch_stream<Form::kAct, 1, 1, 1, 256, 4>(a, stream);
-    case select::GemmF8Kind::kTile32: return launch_ring<Form::kAct, true, 32, 128, 1, 2, 3>(a, stream);
-    case select::GemmF8Kind::kTile64: return launch_ring<Form::kAct, true, 64, 128, 2, 2, 3>(a, stream);
+    case select::GemmF8Kind::kTile32: return launch_ring<Form::kAct, true, 32, 128, 1, 2>(a, stream);
+    case select::GemmF8Kind::kTile64: return launch_ring<Form::kAct, true, 64, 128, 2, 2>(a, stream);
     default: return hipErrorInvalidValue;
   }
 }
@@ -927,7 +932,7 @@ hipError_t launch_grouped_gemm_f8(GemmF8Args a, Form form, hipStream_t stream) {
     case Form::kF32: return launch_form<Form::kF32>(a, stream);
     default: break;
   }
-  if (!select::gemm_f8_act(a.rows, a.groups, a.n)) return launch_ring<Form::kGated, true, 128, 256, 2, 4, 3>(a, stream);
+  if (!select::gemm_f8_act(a.rows, a.groups, a.n)) return launch_ring<Form::kGated, true, 128, 256, 2, 4>(a, stream);
   GemmF8Args first = a;
   first.out = a.workspace;
   const hipError_t e = launch_act(first, stream);

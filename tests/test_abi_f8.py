@@ -175,5 +175,7 @@ def test_binding_checks():
     with pytest.raises(ValueError, match="token_scale must be a device tensor"):
         M.moe_grouped_gemm_f8(rows, 16, 4, 16, count, codes, scale[:1], scale, x)
     idx = torch.zeros(4, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="as they are"):
+        M.moe_dispatch(torch.zeros(4, 256, dtype=torch.uint8), idx, idx, idx, idx, 1, 1, True, rows)
     with pytest.raises(ValueError, match="whole lines"):
         M.moe_dispatch(torch.zeros(4, 200, dtype=torch.uint8), idx, idx, idx, idx, 1, 1, False, rows)

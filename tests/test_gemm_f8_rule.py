@@ -86,7 +86,7 @@ def test_compiled_instances():
 
     assert found(r"::stream_f8_kernel<\(moe::Form\)(\d), (\d+), (\d+), (\d+), (\d+), (\d+)>") == {
         (f, "1", "1", "1", "256", "4") for f in "0124"}
-    ring = found(r"::ring_f8_kernel<\(moe::Form\)(\d), (\w+), (\d+), (\d+), \d+, \d+, 3, (\w+)>")
+    ring = found(r"::ring_f8_kernel<\(moe::Form\)(\d), (\w+), (\d+), (\d+), \d+, \d+, (\w+)>")
     tails = ("true", "false")
     assert ring == {(f, "true" if f in "24" else "false", m, "128", t) for f in "0124" for m in ("32", "64")
                     for t in tails} | {("2", "true", "256", "128", t) for t in tails} | {
