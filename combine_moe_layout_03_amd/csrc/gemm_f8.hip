@@ -3,24 +3,50 @@
 // For a row m of expert g and a column j
 //   y[m][j] = sum over the blocks b of k of (ts[m][b] ws[g][j / 128][b]) p_b,
 //   p_b = sum over i in block b of a[m][i] w[g][j][i]
-// A block's products are summed from zero by the bf16 matrix instructions (the
-// codes widened in registers) and added to the binary32 accumulator times the
-// block's scale by one multiply-add.  The 8-bit instructions (16x16x128 f8f6f4
-// and 16x16x32 fp8) are not as exact: in each eight consecutive products they
-// cut what lies below 2^-13 of the largest (measured: 2^3 is kept beside 2^16,
-// 2^2 is not), an error of 1.4e-5 of normal rows' results.
+// A block's products are summed from zero by matrix instructions and added to
+// the binary32 accumulator, times the block's scale, by one multiply-add.  The
+// plain form rounds y; the gated form takes 2n columns, gate and up, and
+// quantises g / (1 + e^-g) u in blocks of 128 columns (block_rows.h).
 //
-// The plain form rounds y; the gated form takes 2n columns, gate and up, and
-// quantises u g / (1 + e^-g) in blocks of 128 columns (block_rows.h).  A block
-// is the work of one workgroup, so nothing but the 8-bit rows leaves the chip.
+// Two matrix instructions, by what the sums become.  Where they are kept in 32
+// bits (fp32 results, and the scales of 8-bit rows), the codes are widened to
+// bf16 in registers: every product is exact then and the sums are binary32's
+// (1.4e-7 of normal rows' results at k 7168).  The 8-bit instructions (16x16x128
+// f8f6f4 at twice that rate, and 16x16x32 fp8) are not as exact: of each eight
+// consecutive products they cut what lies below 2^-13 of the largest (beside
+// 2^16, 2^3 is kept and 2^2 lost), 1.4e-5 of normal rows' results.  They serve
+// the tiles whose results are rounded to 16 bits, whose half step is 3.9e-3
+// (bf16) or 4.9e-4 (fp16).
 //
 // The weights are the first operand and the rows the second: a lane then holds
 // four consecutive columns of one row, and one scale serves all four.
 //
-// stream_f8_kernel: a workgroup takes kMI x 16 rows; the rows lie in LDS in
-// chunks of kKC bytes of k, two buffers; a wave owns 16 columns (16 gate and 16
-// up) and loads their weights straight into registers, two chunks ahead, each
-// byte once.
+// Kernels (select_f8.h has the rule; us, at the fastest copy's 6.17 TB/s and a
+// large 8-bit or bf16 library product's 3.0 and 1.25 PFLOP/s):
+//
+// split_f8_kernel, for the few workgroups of a small call: 16 rows and 16
+// columns (and as many up columns), a quarter of k to each of four waves; the
+// rows in LDS, the weights straight into registers two chunks ahead.  64 rows, k
+// and n 2048, one expert: 7.7, where a tile takes 9.1.
+//
+// ring_f8_kernel, tiles of 32 and 64 rows by 128 rows of weights: three stages of
+// 128 of k in LDS, filled by LDS-destination loads whole cache lines at a time,
+// with the stage's scales in its slot.  Bound by the weights' bytes where experts
+// have few rows (24 rows over 16 experts, k 2048, n 7168: 44 = 5.4 TB/s, floor
+// 38), by latency where they have tens: 1000 such rows take 60 (floor 41), of
+// which the last, partly filled round of workgroups is a third.  Deeper rings (four
+// stages, one workgroup a CU: 64), two stages and three workgroups a CU (64),
+// eight waves instead of four (59), 128 rows (80) and 256 columns were not
+// faster.  The gated form's widening makes the vector ALU as busy as the matrix
+// cores: 1000 rows, k 7168, n 2048, 130 (floor 77).
+// As 128 x 256 it also takes the gated product of many rows, a block of 128
+// columns to a workgroup, so that nothing but 8-bit rows leaves the chip: 32768
+// rows 1.73 ms = 1.11 PFLOP/s, 0.9 of a large bf16 product.
+//
+// tile_f8_kernel, 256 x 256 by the 8-bit instruction: 32768 rows, k 2048, n 7168,
+// 523 = 1.84 PFLOP/s.  A stage keeps the matrix cores and LDS busy for 2048
+// cycles each; of a tile's 33 us, 8 find its rows, load its first stages and store
+// its results with nothing else on the CU.
 #include "block_rows.h"
 #include "device_util.h"
 #include "gemm.h"
@@ -57,64 +83,57 @@ __device__ __forceinline__ void store_columns(const GemmF8Args& a, int64_t row, 
   }
 }
 
-// ---- few rows for each expert -----------------------------------------------------
+// ---- few workgroups ----------------------------------------------------------------
 
-// kMI x 16 rows; a wave has kNW x 16 columns (and as many again with a gate);
-// kSplit parts of kWaves waves share out the chunks of k, and the first adds
-// the others' sums.
-template <Form kForm, int kMI, int kNW, int kWaves, int kKC, int kSplit>
-__global__ __launch_bounds__(kWave* kWaves* kSplit, 2) void stream_f8_kernel(GemmF8Args a, int64_t slots) {
-  constexpr bool kGated = kForm == Form::kAct;
-  constexpr int kHalves = kGated ? 2 : 1, kNI = kHalves * kNW;  // fragments of a wave: gate, then up
-  constexpr int kThreads = kWave * kWaves, kCols = 16 * kNW * kWaves, kRows = 16 * kMI;
-  constexpr int kRowPieces = kKC / 16, kSteps = kKC / kF8Block, kPieces = kRows * kRowPieces;
-  constexpr int kCopies = (kPieces + kThreads - 1) / kThreads;  // pieces of a chunk's rows that a thread brings
-  constexpr int kScales = kRows * kSteps;                       // of a chunk, for each half
-  static_assert(kRowPieces % 8 == 0 && (kPieces % kThreads == 0 || kCopies == 1), "whole chunks");
-  static_assert(kScales <= kThreads && kF8Block % kCols == 0, "a scale a thread, one block of columns a workgroup");
-  constexpr int kRowsBytes = kRows * kKC;
-  // two buffers of every part's rows; later the sums of all parts but the first
-  constexpr int kSumsBytes = (kSplit - 1) * kThreads * kMI * kNI * 16;
-  __shared__ __attribute__((aligned(1024)))
-  uint8_t rows[2 * kSplit * kRowsBytes > kSumsBytes ? 2 * kSplit * kRowsBytes : kSumsBytes];
-  __shared__ float scales[2][kSplit][kHalves][kScales];
-  const int tid = threadIdx.x % kThreads, lane = tid % kWave, wave = uniform(tid / kWave);
-  const int part = kSplit == 1 ? 0 : uniform(threadIdx.x / kThreads);
-  uint8_t* const sa0 = rows + part * kRowsBytes;
-  uint8_t* const sa1 = sa0 + kSplit * kRowsBytes;
+// 16 rows and 16 columns (of the gate and of the up half).  Four waves share out
+// the chunks of kSplitK of k, each with rows in LDS of its own; a lane loads its
+// weights, two chunks ahead, straight into registers.  The first wave adds the
+// others' sums.
+constexpr int kSplitRows = 16, kSplitWaves = 4, kSplitK = 256;
+
+template <Form kForm>
+__global__ __launch_bounds__(kWave* kSplitWaves, 2) void split_f8_kernel(GemmF8Args a, int64_t slots) {
+  constexpr int kHalves = kForm == Form::kAct ? 2 : 1;  // gate and up
+  constexpr int kSteps = kSplitK / kF8Block, kRowPieces = kSplitK / 16;
+  constexpr int kCopies = kSplitRows * kRowPieces / kWave;  // pieces of a chunk's rows that a lane brings
+  constexpr int kScales = kSplitRows * kSteps;              // of a chunk, for each half
+  static_assert(kRowPieces == 16 && kScales <= kWave && kF8Block % 16 == 0, "a scale a lane, one block of columns");
+  constexpr int kRowsBytes = kSplitRows * kSplitK;
+  __shared__ __attribute__((aligned(1024))) uint8_t rows[2][kSplitWaves][kRowsBytes];
+  __shared__ float scales[2][kSplitWaves][kHalves][kScales];
+  __shared__ f32x4 sums[kSplitWaves - 1][kHalves][kWave];
+  const int lane = threadIdx.x % kWave, part = uniform(threadIdx.x / kWave);
   // workgroups of one block of columns lie on one XCD, an expert's slots next to each other
   const int64_t x = blockIdx.x % 8, y = blockIdx.x / 8;
   const int64_t slot = y % slots, block = y / slots * 8 + x;
-  if (block * kCols >= a.n) return;
+  if (block * 16 >= a.n) return;
   RowSlot rs;
-  if (!find_row_slot<kRows>(a.group_count, a.groups, a.rows, slot, lane, &rs)) return;
+  if (!find_row_slot<kSplitRows>(a.group_count, a.groups, a.rows, slot, lane, &rs)) return;
 
-  const int col0 = static_cast<int>(block) * kCols + wave * 16 * kNW;
+  const int col0 = static_cast<int>(block) * 16;
   const int piece = lane / 16 * 16, l16 = lane % 16;
   const int kb = f8_blocks(a.k), nb = f8_blocks(a.n);
-  const uint8_t* pb[kNI];
+  const uint8_t* pb[kHalves];
   const float* ws[kHalves];
 #pragma unroll
   for (int h = 0; h < kHalves; ++h) {
     const int64_t half = static_cast<int64_t>(rs.group) * kHalves + h;
-#pragma unroll
-    for (int j = 0; j < kNW; ++j) pb[h * kNW + j] = a.w + (half * a.n + min(col0 + j * 16 + l16, a.n - 1)) * a.k;
-    ws[h] = a.weight_scale + (half * nb + static_cast<int>(block) * kCols / kF8Block) * kb;
+    pb[h] = a.w + (half * a.n + min(col0 + l16, a.n - 1)) * a.k;
+    ws[h] = a.weight_scale + (half * nb + col0 / kF8Block) * kb;
   }
   const uint8_t* pa[kCopies];
-  int ka[kCopies], la[kCopies];
+  int la[kCopies];
+  const int ka = lane % kRowPieces * 16;
 #pragma unroll
   for (int q = 0; q < kCopies; ++q) {
-    const int p = q * kThreads + tid, r = p / kRowPieces, c = p % kRowPieces;
-    pa[q] = a.a + tile_row(rs.row0, rs.row_end, min(r, kRows - 1)) * a.a_stride;
-    ka[q] = c * 16;
-    la[q] = r * kKC + (c ^ (r % (kRowPieces < 16 ? kRowPieces : 16))) * 16;
+    const int r = (q * kWave + lane) / kRowPieces;
+    pa[q] = a.a + tile_row(rs.row0, rs.row_end, r) * a.a_stride;
+    la[q] = r * kSplitK + ((lane % kRowPieces) ^ r) * 16;  // 16 rows' pieces fall into all banks
   }
-  // scale tid of a chunk: step tid / kRows, row tid % kRows
-  const int sr = tid % kRows, sb = tid / kRows;
+  // scale `lane` of a chunk: step lane / 16, row lane % 16
   const float* pts = reinterpret_cast<const float*>(
-      a.token_scale + static_cast<int64_t>(tile_row(rs.row0, rs.row_end, sr)) * a.ts_stride);
-  const int rounds = (a.k + kSplit * kKC - 1) / (kSplit * kKC);
+      a.token_scale + static_cast<int64_t>(tile_row(rs.row0, rs.row_end, l16)) * a.ts_stride);
+  const int rounds = (a.k + kSplitWaves * kSplitK - 1) / (kSplitWaves * kSplitK);
   // Past k the rows' codes count as zero, and so do their scales; the weights
   // there are some of the same column's.
   struct Codes {
@@ -125,68 +144,57 @@ __global__ __launch_bounds__(kWave* kWaves* kSplit, 2) void stream_f8_kernel(Gem
     float s[kHalves];
   };
   auto load_a = [&](int round, Rows& to) {
-    const int chunk = round * kSplit + part;
+    const int chunk = round * kSplitWaves + part, at = chunk * kSplitK + ka;
 #pragma unroll
     for (int q = 0; q < kCopies; ++q) {
-      const int at = chunk * kKC + ka[q];
       to.v[q] = *reinterpret_cast<const i32x4*>(pa[q] + (at < a.k ? at : 0));
       if (at >= a.k) to.v[q] = i32x4{0, 0, 0, 0};
     }
-    const int b = chunk * kSteps + sb;
-    const bool have = tid < kScales && b < kb;
+    const int b = chunk * kSteps + lane / kSplitRows;
+    const bool have = lane < kScales && b < kb;
     const float ts = have ? pts[b] : 0.0f;
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) to.s[h] = have ? ts * ws[h][b] : 0.0f;
   };
   auto put_a = [&](int buf, const Rows& from) {
 #pragma unroll
-    for (int q = 0; q < kCopies; ++q)
-      if (kPieces % kThreads == 0 || tid < kPieces) *reinterpret_cast<i32x4*>((buf ? sa1 : sa0) + la[q]) = from.v[q];
+    for (int q = 0; q < kCopies; ++q) *reinterpret_cast<i32x4*>(rows[buf][part] + la[q]) = from.v[q];
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
-      if (tid < kScales) scales[buf][part][h][tid] = from.s[h];
+      if (lane < kScales) scales[buf][part][h][lane] = from.s[h];
   };
-  auto load_b = [&](int round, Codes (&v)[kSteps][kNI]) {
-    const int chunk = round * kSplit + part;
+  auto load_b = [&](int round, Codes (&v)[kSteps][kHalves]) {
+    const int chunk = round * kSplitWaves + part;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      const int at = chunk * kKC + s * kF8Block + piece;
+      const int at = chunk * kSplitK + s * kF8Block + piece;
 #pragma unroll
-      for (int j = 0; j < kNI; ++j)
-        v[s][j] = Codes{*reinterpret_cast<const i32x4*>(pb[j] + (at < a.k ? at : 0)),
-                        *reinterpret_cast<const i32x4*>(pb[j] + (at + 64 < a.k ? at + 64 : 0))};
+      for (int h = 0; h < kHalves; ++h)
+        v[s][h] = Codes{*reinterpret_cast<const i32x4*>(pb[h] + (at < a.k ? at : 0)),
+                        *reinterpret_cast<const i32x4*>(pb[h] + (at + 64 < a.k ? at + 64 : 0))};
     }
   };
-  f32x4 acc[kMI][kNI];
+  f32x4 acc[kHalves];
 #pragma unroll
-  for (int i = 0; i < kMI; ++i)
-#pragma unroll
-    for (int j = 0; j < kNI; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  auto multiply = [&](int buf, const Codes (&b)[kSteps][kNI]) {
+  for (int h = 0; h < kHalves; ++h) acc[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto multiply = [&](int buf, const Codes (&b)[kSteps][kHalves]) {
+    const uint8_t* row = rows[buf][part] + l16 * kSplitK;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      WideCodes w[kNI];
+      const WideCodes f = widen(*reinterpret_cast<const i32x4*>(row + ((s * 8 + lane / 16) ^ l16) * 16),
+                                *reinterpret_cast<const i32x4*>(row + ((s * 8 + 4 + lane / 16) ^ l16) * 16));
 #pragma unroll
-      for (int j = 0; j < kNI; ++j) w[j] = widen(b[s][j].a, b[s][j].b);
+      for (int h = 0; h < kHalves; ++h) {
+        const f32x4 p = block_sum(widen(b[s][h].a, b[s][h].b), f);
+        const float scale = scales[buf][part][h][s * kSplitRows + l16];
 #pragma unroll
-      for (int i = 0; i < kMI; ++i) {
-        const int r = i * 16 + l16, turn = r % (kRowPieces < 16 ? kRowPieces : 16);
-        const uint8_t* row = (buf ? sa1 : sa0) + r * kKC;
-        const WideCodes f = widen(*reinterpret_cast<const i32x4*>(row + ((s * 8 + lane / 16) ^ turn) * 16),
-                                  *reinterpret_cast<const i32x4*>(row + ((s * 8 + 4 + lane / 16) ^ turn) * 16));
-#pragma unroll
-        for (int j = 0; j < kNI; ++j) {
-          const f32x4 p = block_sum(w[j], f);
-          const float scale = scales[buf][part][j / kNW][s * kRows + r];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) acc[i][j][q] = __builtin_fmaf(p[q], scale, acc[i][j][q]);
-        }
+        for (int q = 0; q < 4; ++q) acc[h][q] = __builtin_fmaf(p[q], scale, acc[h][q]);
       }
     }
   };
 
   Rows a0, a1;
-  Codes b0[kSteps][kNI], b1[kSteps][kNI];
+  Codes b0[kSteps][kHalves], b1[kSteps][kHalves];
   load_a(0, a0);
   load_b(0, b0);
   if (rounds > 1) {
@@ -194,8 +202,8 @@ __global__ __launch_bounds__(kWave* kWaves* kSplit, 2) void stream_f8_kernel(Gem
     load_b(1, b1);
   }
   put_a(0, a0);
-  __syncthreads();
-  // A buffer is written again only after the barrier that follows its readers.
+  wave_lds_sync();
+  // A wave's buffers are its own; it writes one again only after its reads of it.
   for (int c = 0;; c += 2) {
     multiply(0, b0);
     if (c + 1 >= rounds) break;
@@ -204,7 +212,7 @@ __global__ __launch_bounds__(kWave* kWaves* kSplit, 2) void stream_f8_kernel(Gem
       load_b(c + 2, b0);
     }
     put_a(1, a1);
-    __syncthreads();
+    wave_lds_sync();
     multiply(1, b1);
     if (c + 2 >= rounds) break;
     if (c + 3 < rounds) {
@@ -212,55 +220,34 @@ __global__ __launch_bounds__(kWave* kWaves* kSplit, 2) void stream_f8_kernel(Gem
       load_b(c + 3, b1);
     }
     put_a(0, a0);
-    __syncthreads();
+    wave_lds_sync();
   }
-  if constexpr (kSplit > 1) {  // the first part adds the others' sums
-    f32x4* const sums = reinterpret_cast<f32x4*>(rows);
-    __syncthreads();
-    if (part > 0) {
+  if (part > 0) {
 #pragma unroll
-      for (int i = 0; i < kMI; ++i)
-#pragma unroll
-        for (int j = 0; j < kNI; ++j) sums[((part - 1) * kMI * kNI + i * kNI + j) * kThreads + tid] = acc[i][j];
-    }
-    __syncthreads();
-    if (part == 0) {
-#pragma unroll
-      for (int p = 1; p < kSplit; ++p)
-#pragma unroll
-        for (int i = 0; i < kMI; ++i)
-#pragma unroll
-          for (int j = 0; j < kNI; ++j) acc[i][j] += sums[((p - 1) * kMI * kNI + i * kNI + j) * kThreads + tid];
-    } else {
-      return;
-    }
+    for (int h = 0; h < kHalves; ++h) sums[part - 1][h][lane] = acc[h];
   }
-
+  __syncthreads();
+  if (part > 0) return;
+#pragma unroll
+  for (int p = 0; p < kSplitWaves - 1; ++p)
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) acc[h] += sums[p][h][lane];
+  if constexpr (kHalves == 2) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[0][q] = gated(acc[0][q], acc[1][q]);
+  }
   const int col = col0 + lane / 16 * 4;
-#pragma unroll
-  for (int j = 0; j < kNW; ++j) {
-    if (col + j * 16 >= a.n) continue;
-#pragma unroll
-    for (int i = 0; i < kMI; ++i) {
-      const int r = i * 16 + l16;
-      if constexpr (kGated) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i][j][q] = gated(acc[i][j][q], acc[i][kNW + j][q]);
-      }
-      if (tile_has_row(rs.row0, rs.row_end, r)) store_columns<kForm>(a, rs.row0 + r, col + j * 16, acc[i][j]);
-    }
-  }
+  if (col < a.n && tile_has_row(rs.row0, rs.row_end, l16)) store_columns<kForm>(a, rs.row0 + l16, col, acc[0]);
 }
 
-int64_t stream_blocks(int32_t rows, int32_t groups, int32_t n, int tile_m, int tile_n) {
-  return row_slots(rows, groups, tile_m) * (((static_cast<int64_t>(n) + tile_n - 1) / tile_n + 7) / 8 * 8);
+int64_t split_blocks(int32_t rows, int32_t groups, int32_t n) {
+  return row_slots(rows, groups, kSplitRows) * (((static_cast<int64_t>(n) + 15) / 16 + 7) / 8 * 8);
 }
 
-template <Form kForm, int kMI, int kNW, int kWaves, int kKC, int kSplit>
-hipError_t launch_stream(const GemmF8Args& a, hipStream_t stream) {
-  const dim3 grid(static_cast<uint32_t>(stream_blocks(a.rows, a.groups, a.n, kMI * 16, 16 * kNW * kWaves)));
-  stream_f8_kernel<kForm, kMI, kNW, kWaves, kKC, kSplit>
-      <<<grid, dim3(kWave * kWaves * kSplit), 0, stream>>>(a, row_slots(a.rows, a.groups, kMI * 16));
+template <Form kForm>
+hipError_t launch_split(const GemmF8Args& a, hipStream_t stream) {
+  split_f8_kernel<kForm><<<dim3(static_cast<uint32_t>(split_blocks(a.rows, a.groups, a.n))), dim3(kWave * kSplitWaves), 0,
+                           stream>>>(a, row_slots(a.rows, a.groups, kSplitRows));
   return hipGetLastError();
 }
 
@@ -846,8 +833,8 @@ hipError_t launch_ring(const GemmF8Args& a, hipStream_t stream) {
 template <Form kForm>
 hipError_t launch_form(const GemmF8Args& a, hipStream_t stream) {
   constexpr bool kWide = kForm == Form::kF32;
-  switch (select::gemm_f8_kind(a.rows, a.groups, a.n)) {
-    case select::GemmF8Kind::kSplit16: return launch_stream<kForm, 1, 1, 1, 256, 4>(a, stream);
+  switch (select::gemm_f8_kind(a.rows, a.groups, a.n, kWide)) {
+    case select::GemmF8Kind::kSplit16: return launch_split<kForm>(a, stream);
     case select::GemmF8Kind::kTile32: return launch_ring<kForm, kWide, 32, 128, 1, 2>(a, stream);
     case select::GemmF8Kind::kTile64: return launch_ring<kForm, kWide, 64, 128, 2, 2>(a, stream);
     case select::GemmF8Kind::kTile256:
@@ -858,7 +845,7 @@ hipError_t launch_form(const GemmF8Args& a, hipStream_t stream) {
 }
 hipError_t launch_act(const GemmF8Args& a, hipStream_t stream) {
   switch (select::gemm_f8_act_kind(a.rows, a.groups, a.n)) {
-    case select::GemmF8Kind::kSplit16: return launch_stream<Form::kAct, 1, 1, 1, 256, 4>(a, stream);
+    case select::GemmF8Kind::kSplit16: return launch_split<Form::kAct>(a, stream);
     case select::GemmF8Kind::kTile32: return launch_ring<Form::kAct, true, 32, 128, 1, 2>(a, stream);
     case select::GemmF8Kind::kTile64: return launch_ring<Form::kAct, true, 64, 128, 2, 2>(a, stream);
     default: return hipErrorInvalidValue;
@@ -900,7 +887,7 @@ __global__ __launch_bounds__(256) void quant_act_f8_kernel(GemmF8Args a, const f
 }
 
 bool grouped_gemm_f8_fits(int32_t rows, int32_t groups, int32_t n, Form form) {
-  const auto split = [&]() { return stream_blocks(rows, groups, n, 16, 16) <= kMaxLaunchThreads / (4 * kWave); };
+  const auto split = [&]() { return split_blocks(rows, groups, n) <= kMaxLaunchThreads / (kSplitWaves * kWave); };
   const auto tile = [&](int tile_m, int tile_n, int waves) {
     return tile_blocks(rows, groups, n, tile_m, tile_n) <= kMaxLaunchThreads / (waves * kWave);
   };
@@ -913,7 +900,7 @@ bool grouped_gemm_f8_fits(int32_t rows, int32_t groups, int32_t n, Form form) {
       default: return false;
     }
   }
-  switch (select::gemm_f8_kind(rows, groups, n)) {
+  switch (select::gemm_f8_kind(rows, groups, n, form == Form::kF32)) {
     case select::GemmF8Kind::kSplit16: return split();
     case select::GemmF8Kind::kTile32: return tile(32, 128, 2);
     case select::GemmF8Kind::kTile64: return tile(64, 128, 4);

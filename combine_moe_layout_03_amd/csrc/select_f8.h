@@ -7,6 +7,26 @@
 namespace moe {
 namespace select {
 
+// The rows an expert has on average (when all have some, and the counts add up
+// to the call's rows: the host does not know less) decide how many rows a tile
+// takes, measured at 16 experts whose counts fall as rank^-1/2 (us, bf16
+// results; tile32, tile64, tile256):
+//   k 2048, n 7168, 16 rows: 40, 41, 63       k 7168, n 2048, 24 rows: 42, 42, 77
+//   200: 45, 46, 67                           200: 43, 43, 78
+//   400: 54, 49, 68                           768: 57, 68, 85
+//   1500: 91, 74, 76                          3000: 153, 114, 101
+//   3000: 143, 108, 101
+//   6000: 244, 179, 140
+// The widened products (fp32 results) have a tile of 256 x 128 in the place of
+// tile256, and fewer workgroups than about 256 of 256 x 256 are slower with it
+// (tile64, tile256: 32768 rows, k 2048, n 7168: 1158, 1012; 16384, k and n 2048, 4
+// experts, 528 workgroups: 168, 159; 8000, k 4096, n 1024, 8 experts, 140: 92,
+// 110; 8-bit products 60, 47).
+//
+// Where all workgroups of 16 columns fit on the chip at once (four a CU), those
+// are the fastest (split16, and the best of the others; us): 2 rows, 8 experts, k
+// 5904, n 213: 7.8, 23; 30, 5, 5488, 1546: 13.8, 22; 1000, 1, 7168, 128: 14.3, 23;
+// 64, 1, 2048, 2048: 7.7, 9.1; but 128, 2, 4096, 2048 (1280 of them): 18.9, 14.7.
 enum class GemmF8Kind { kSplit16, kTile32, kTile64, kTile256 };
 
 // Workgroups to expect: every other expert ends inside a tile.
@@ -17,23 +37,35 @@ constexpr int64_t gemm_f8_workgroups(int32_t rows, int32_t groups, int32_t n, in
 constexpr int64_t gemm_f8_split_workgroups(int32_t rows, int32_t groups, int32_t n) {
   return (rows / 16 + int64_t(rows < groups ? rows : groups)) * ((int64_t(n) + 15) / 16);
 }
-constexpr GemmF8Kind gemm_f8_kind(int32_t rows, int32_t groups, int32_t n) {
-  const int64_t mean = (int64_t(rows) + groups - 1) / groups;
+constexpr int64_t gemm_f8_mean(int32_t rows, int32_t groups) { return (int64_t(rows) + groups - 1) / groups; }
+constexpr GemmF8Kind gemm_f8_kind(int32_t rows, int32_t groups, int32_t n, bool wide) {
+  const int64_t mean = gemm_f8_mean(rows, groups);
   if (gemm_f8_split_workgroups(rows, groups, n) <= 1024) return GemmF8Kind::kSplit16;
   if (mean <= 16) return GemmF8Kind::kTile32;
-  if (mean > 128 && gemm_f8_workgroups(rows, groups, n, 256, 256) >= 128) return GemmF8Kind::kTile256;
+  if (mean > 128 && gemm_f8_workgroups(rows, groups, n, 256, 256) >= (wide ? 256 : 128)) return GemmF8Kind::kTile256;
   return GemmF8Kind::kTile64;
 }
 
+// The gated product of few rows passes its activations through a workspace, as
+// floats, to a kernel that quantises them: its workgroups need not hold whole
+// blocks of 128 columns then, and fill the chip (8 rows, 8 experts, k 7168, n
+// 2048: 47 us, and 71 with 128 columns a workgroup).  With more rows for each
+// expert, and workgroups enough, a workgroup of 128 x 128 quantises its own (3000
+// rows, 16 experts: 230 us, and 264 through the workspace; 1500: 193, 165; 4000,
+// 4 experts, k and n 512: 19, 15).
 constexpr int32_t kF8ActRows = 4096;
 constexpr bool gemm_f8_act(int32_t rows, int32_t groups, int32_t n) {
-  const int64_t mean = (int64_t(rows) + groups - 1) / groups;
-  return rows <= kF8ActRows && (mean <= 128 || gemm_f8_workgroups(rows, groups, n, 128, 128) < 192);
+  return rows <= kF8ActRows &&
+         (gemm_f8_mean(rows, groups) <= 128 || gemm_f8_workgroups(rows, groups, n, 128, 128) < 192);
 }
+// As above (k 7168, n 2048, 16 experts, us; tile32, tile64: 24 rows 84, 92; 200:
+// 87, 93; 400: 121, 95; 768: 125, 124; 1500: 199, 165), with two reads of weights
+// for each column split16 up to fewer workgroups (30 rows, 5 experts, k 5488, n
+// 1536, 576 of them: 22, and 38 with tile32; 8 rows, 8 experts, k 7168, n 2048,
+// 1024 of them: 53, 47).
 constexpr GemmF8Kind gemm_f8_act_kind(int32_t rows, int32_t groups, int32_t n) {
-  const int64_t mean = (int64_t(rows) + groups - 1) / groups;
   if (gemm_f8_split_workgroups(rows, groups, n) <= 768) return GemmF8Kind::kSplit16;
-  return mean <= 16 ? GemmF8Kind::kTile32 : GemmF8Kind::kTile64;
+  return gemm_f8_mean(rows, groups) <= 16 ? GemmF8Kind::kTile32 : GemmF8Kind::kTile64;
 }
 
 }  // namespace select

@@ -8,6 +8,7 @@ PLAIN = {
     "tile64": (900, 648, [64, 0, 65, 1, 190, 2, 63, 31] + [22] * 22),
     "tile256": (5200, 1603, [256, 2600, 0, 2300]),
 }
+WIDE = dict(PLAIN, tile256=(5200, 3001, [256, 2600, 0, 2300]))  # fp32 results
 GATED = {  # (the rows that go through the workspace, and those that do not)
     "split16": (50, 464, [0, 3, 5, 17, 0, 1, 2, 4, 0, 0, 9, 8, 1, 0]),
     "tile32": (200, 912, [40, 0, 33, 1, 60, 2, 3, 31, 0, 0, 9, 8, 1, 0]),

@@ -20,7 +20,8 @@ int main() {
   char what;
   int a, b, c;
   while (std::scanf(" %c %d %d %d", &what, &a, &b, &c) == 4) {
-    if (what == 'p') std::printf("%d\n", static_cast<int>(gemm_f8_kind(a, b, c)));
+    if (what == 'p') std::printf("%d\n", static_cast<int>(gemm_f8_kind(a, b, c, false)));
+    if (what == 'w') std::printf("%d\n", static_cast<int>(gemm_f8_kind(a, b, c, true)));
     if (what == 'g') std::printf("%d\n", gemm_f8_act(a, b, c) ? static_cast<int>(gemm_f8_act_kind(a, b, c)) : 9);
     if (what == 'n') {
       const NormShape s = norm_shape(b);
@@ -48,8 +49,10 @@ def kinds(what, shapes):
 
 def test_every_kernel_has_a_gpu_case():
     assert kinds("p", [(r, len(c), n) for r, n, c in IC.PLAIN.values()]) == list(IC.PLAIN)
+    assert kinds("w", [(r, len(c), n) for r, n, c in IC.WIDE.values()]) == list(IC.WIDE)
     assert kinds("g", [(r, len(c), n) for r, n, c in IC.GATED.values()]) == list(IC.GATED)
     assert set(IC.PLAIN) == {"split16", "tile32", "tile64", "tile256"}
+    assert set(IC.WIDE) == set(IC.PLAIN)
     assert set(IC.GATED) == {"split16", "tile32", "tile64", "whole"}
 
 
@@ -60,6 +63,8 @@ def test_rules_at_their_borders():
                        (big, 1, 1)]) == [
         "split16", "split16", "tile64", "tile32", "tile32", "tile64", "tile64", "tile256", "tile64", "tile256", "tile32",
         "tile256"]
+    assert kinds("w", [(129 * 16, 16, 7168), (8000, 8, 1024), (16384, 4, 2048), (big, 65536, 65536)]) == [
+        "tile256", "tile64", "tile256", "tile256"]
     assert kinds("g", [(1, 1, 16), (8, 8, 2048), (8, 8, 1536), (256, 16, 2048), (257, 16, 2048), (4096, 64, 2048),
                        (4096, 16, 2048), (4096, 1, 64), (4097, 1, 16), (big, 65536, 32768)]) == [
         "split16", "tile32", "split16", "tile32", "tile64", "tile64", "whole", "tile64", "whole", "whole"]
@@ -84,8 +89,7 @@ def test_compiled_instances():
     def found(pattern):
         return {m.groups() for m in (re.search(pattern, s) for s in names) if m}
 
-    assert found(r"::stream_f8_kernel<\(moe::Form\)(\d), (\d+), (\d+), (\d+), (\d+), (\d+)>") == {
-        (f, "1", "1", "1", "256", "4") for f in "0124"}
+    assert found(r"::split_f8_kernel<\(moe::Form\)(\d)>") == {(f,) for f in "0124"}
     ring = found(r"::ring_f8_kernel<\(moe::Form\)(\d), (\w+), (\d+), (\d+), \d+, \d+, (\w+)>")
     tails = ("true", "false")
     assert ring == {(f, "true" if f in "24" else "false", m, "128", t) for f in "0124" for m in ("32", "64")
