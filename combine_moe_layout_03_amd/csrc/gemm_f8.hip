@@ -329,7 +329,7 @@ struct TileWave {
                     kWaveN / kHalves % 32 == 0,
                 "a wave's columns share a scale, and fall into pairs of fragments");
 
-  int lane, wave, wm, wn, l16, row0, row_end, col0, stages;
+  int lane, wave, wm, wn, l16, row0, row_end, col0, stages, start;
   // Load q of a wave fills the stage rows from 8 (q kTileWaves + wave); lane l
   // fetches the piece that belongs at position l % 8 of row l / 8.  A wave's stage rows of weights are its gate rows, then its up
   // rows.  Offsets from the tile's first row fit in 32 bits: 256 rows of at most
@@ -340,6 +340,7 @@ struct TileWave {
   // The tile of 256 x 256 has no registers left for its loads' offsets and makes
   // them anew each time, of the last row (of weights) that exists and the stride.
   static constexpr bool kAnew = kTileM * kTileN == 256 * 256;
+  static constexpr bool kTurned = kTileM <= 64;  // (larger tiles are not bound by their loads)
   const uint8_t *base_a, *base_b;
   uint32_t src_a[kAnew ? 1 : kLoadsA], src_b[kAnew ? 1 : kLoadsB];
   int last_a, last_b;
@@ -370,6 +371,12 @@ struct TileWave {
     col0 = static_cast<int>(col_tile) * kCols;
     wm = wave / kWavesN, wn = wave % kWavesN, l16 = lane % 16;
     stages = f8_blocks(a.k), k = a.k;
+    // Where along k the stages begin.  Rows that lie a multiple of 4096 bytes apart
+    // fall into few memory channels, and workgroups in step would all ask the same
+    // ones (16 experts, us, all from 0 and each expert from a place of its own: k
+    // and n 4096, 24 rows 65.1 and 46.0, 1000 rows 70.8, 67.4; k 8192, n 2048, 24
+    // rows 60.8, 45.3; gated, k 4096, n 2048, 24 rows 69.4, 50.6).
+    start = !kTurned || a.k % 4096 != 0 ? 0 : static_cast<int>(rs.group * int64_t(5) % stages);
     piece = (lane % 8) ^ swizzle(kRowsPerLoad * wave + lane / 8);
     base_a = a.a + row0 * a.a_stride;
     base_b = a.w + (static_cast<int64_t>(rs.group) * kHalves * a.n + col0) * a.k;
@@ -400,12 +407,17 @@ struct TileWave {
     return true;
   }
 
+  // The block of k of stage s; stages past the last one repeat it.
+  __device__ __forceinline__ int block_of(int s) const {
+    s = min(s, stages - 1);
+    return !kTurned || s + start < stages ? s + start : s + start - stages;
+  }
   // Stages past the last one load it again, into slots that are not read; a
   // piece past k reads the row's first piece (its row fragments count as zero).
   template <bool kTail, int kLoads>
   __device__ __forceinline__ void issue(int s, const uint8_t* base, const uint32_t* src, int last, uint32_t stride,
                                         uint8_t* buf) const {
-    const int k0 = min(s, stages - 1) * kSK;
+    const int k0 = block_of(s) * kSK;
     int first = kRowsPerLoad * wave + lane / 8;
     if constexpr (kAnew) asm volatile("" : "+v"(first));  // else the offsets are made once and kept
 #pragma unroll
@@ -728,7 +740,7 @@ __global__ __launch_bounds__(kWave* kWavesM* kWavesN, 2) void ring_f8_kernel(Gem
   const auto issue = [&](int S, uint8_t* to_a, uint8_t* to_b, float* to_s) {
     t.template issue_b<kTail>(S, to_b);
     t.template issue_a<kTail>(S, to_a);
-    __builtin_amdgcn_global_load_lds(scale_src + min(S, stages - 1), (MOE_LDS void*)(to_s + scale_at), 4, 0, 0);
+    __builtin_amdgcn_global_load_lds(scale_src + t.block_of(S), (MOE_LDS void*)(to_s + scale_at), 4, 0, 0);
   };
   issue(0, sa0, sb0, ss0);
   issue(1, sa1, sb1, ss1);

@@ -178,6 +178,16 @@ def test_gemm_swiglu_f8_every_kernel(name, k):
     check_gated(np.random.default_rng(k), rows, k, n, counts)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp32", "gated"])
+@pytest.mark.parametrize("rows,k,n,counts", [(30, 4096, 4128, [17, 13]), (200, 4096, 1200, [90, 110]), (200, 8192, 1200, [3, 190])])
+def test_gemm_f8_turned_k(rows, k, n, counts, kind):
+    """A k of whole 4096s, which the experts walk from places of their own."""
+    if kind == "gated":
+        check_gated(np.random.default_rng(k), rows, k, n // 2 // 16 * 16 if rows < 100 else n, counts)
+    else:
+        check_plain(np.random.default_rng(k), rows, k, n - 5, counts, kind)
+
+
 @pytest.mark.parametrize("rows,k,n,counts", [(20, 208, 96, [9, 11]), (300, 400, 256, [150, 150]), (900, 528, 304, [900])])
 def test_gemm_f8_dense_rows_and_scales(rows, k, n, counts):
     check_plain(np.random.default_rng(n), rows, k, n, counts, "bf16", packed=False)
