@@ -267,21 +267,15 @@ constexpr int kLgkmWait0 = 0xc07f;
 // both the 16 rows fall into all 16 groups of banks.
 __device__ __forceinline__ int swizzle(int r) { return ((r >> 1) & 7) ^ (((r >> 4) & 1) << 1); }
 
-// Lane l's value is that of row l of a wave's 64 rows (of l % 32 with 32): in
-// every lane, for each fragment i, the value of row 16 i + l % 16.
-template <int kMI>
-__device__ __forceinline__ void spread_rows(float v, float (&to)[kMI]) {
-  static_assert(kMI == 2 || kMI == 4, "32 or 64 rows");
+// Lane l's value is that of row l of a wave's 64 rows: in every lane, for each
+// fragment i, the value of row 16 i + l % 16.
+__device__ __forceinline__ void spread_rows(float v, float (&to)[4]) {
   const uint32_t b = __float_as_uint(v);
   const auto h = __builtin_amdgcn_permlane16_swap(b, b, false, false);  // rows 0 0 2 2 and 1 1 3 3
-  if constexpr (kMI == 2) {
-    to[0] = __uint_as_float(h[0]), to[1] = __uint_as_float(h[1]);
-  } else {
-    const auto even = __builtin_amdgcn_permlane32_swap(h[0], h[0], false, false);
-    const auto odd = __builtin_amdgcn_permlane32_swap(h[1], h[1], false, false);
-    to[0] = __uint_as_float(even[0]), to[1] = __uint_as_float(odd[0]);
-    to[2] = __uint_as_float(even[1]), to[3] = __uint_as_float(odd[1]);
-  }
+  const auto even = __builtin_amdgcn_permlane32_swap(h[0], h[0], false, false);
+  const auto odd = __builtin_amdgcn_permlane32_swap(h[1], h[1], false, false);
+  to[0] = __uint_as_float(even[0]), to[1] = __uint_as_float(odd[0]);
+  to[2] = __uint_as_float(even[1]), to[3] = __uint_as_float(odd[1]);
 }
 
 // 16 bytes of consecutive columns of one row, as far as the row goes.
@@ -616,7 +610,7 @@ __global__ __launch_bounds__(kWave* kWavesM* kWavesN) void tile_f8_kernel(GemmF8
 #pragma unroll
     for (int n = 0; n < kStepNI; ++n) t.read_b(cb, h * kStepNI + n, rb[n]);
     float s[kMI];
-    spread_rows<kMI>(ts, s);
+    spread_rows(ts, s);
 #pragma unroll
     for (int i = 0; i < kMI; ++i) s[i] *= w;
     // this wave's loads of A(S + 1) and B(S + 1); those of B(S + 2) may still run

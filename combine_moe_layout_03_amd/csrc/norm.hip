@@ -7,6 +7,14 @@
 // A row's chunks of 8 elements lie in the registers of its lanes from the load
 // to the stores, so every element is read and written once.  16 neighbouring
 // lanes hold the 128 columns of an 8-bit block.
+//
+// Bound by the rows' bytes.  4096 tokens, h 7168, bf16, with the sum, the result
+// and the 8-bit rows written: 47.2 us for 265 MB = 5.6 TB/s (43.0 at the fastest
+// copy's 6.17).  The gradient of the same tokens, 235 MB: 43.0 us and 4.7 for
+// the weight's parts (38.1).  A row stays in one workgroup, since its mean is
+// needed before its first store; what hides a row's two barriers is the other
+// rows of the CU, and in the gradient, whose workgroups walk many rows, the next
+// row's loads.
 #include "block_rows.h"
 #include "device_util.h"
 #include "norm.h"

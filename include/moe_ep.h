@@ -653,9 +653,8 @@ int moe_rms_norm_backward(const void* gradOut, moe_dtype gradOutType, const void
  * tokenScaleStride as above (else MOE_ERR_BAD_SHAPE); k % 16 == 0, k <=
  * MOE_GEMM_MAX_K, n <= MOE_GEMM_MAX_N, groups <= MOE_GEMM_MAX_GROUPS,
  * aRowBytes <= 2^23, and a launch of fewer than 2^32 threads (else
- * MOE_ERR_UNSUPPORTED); aRowBytes a
- * multiple of 16 (else MOE_ERR_BAD_ALIGN).  rows == 0 enqueues nothing.  One
- * launch, no workspace. */
+ * MOE_ERR_UNSUPPORTED); aRowBytes a multiple of 16 (else MOE_ERR_BAD_ALIGN).
+ * rows == 0 enqueues nothing.  One launch, no workspace. */
 int moe_grouped_gemm_f8(const void* a, int64_t aRowBytes, int32_t rows, int32_t k, const int32_t* groupCount,
                         int32_t groups, const void* w, int32_t n, const float* weightScale,
                         const void* tokenScale, int64_t tokenScaleStride, void* out, moe_dtype outType,
@@ -681,7 +680,8 @@ int moe_gemm_swiglu_quant_f8_workspace_bytes(int32_t rows, int32_t n, size_t* by
  * workspace  device, 16-byte aligned, of
  *            moe_gemm_swiglu_quant_f8_workspace_bytes(rows, n) bytes (may be
  *            NULL where that is 0); contents on return unspecified.
- * Requires as moe_grouped_gemm_f8, n % 16 == 0 and 2n <= MOE_GEMM_MAX_N. */
+ * Requires as moe_grouped_gemm_f8, n % 16 == 0 and 2n <= MOE_GEMM_MAX_N.  One
+ * launch where the workspace is of 0 bytes, else two. */
 int moe_grouped_gemm_swiglu_quant_f8(const void* a, int64_t aRowBytes, int32_t rows, int32_t k,
                                      const int32_t* groupCount, int32_t groups, const void* w, int32_t n,
                                      const float* weightScale, const void* tokenScale,

@@ -87,7 +87,7 @@ def gated(**kw):
 BOTH = [
     (dict(rows=-1), 2), (dict(k=0), 2), (dict(n=0), 2), (dict(g=0), 2), (dict(ab=2032), 2), (dict(st=60), 2),
     (dict(st=0), 2), (dict(st=-64), 2), (dict(st=66), 2), (dict(k=2040), 7), (dict(k=65552, ab=65552), 7),
-    (dict(g=65537), 7), (dict(ab=2184), 3), (dict(a=None), 1), (dict(gc=None), 1), (dict(w=None), 1),
+    (dict(g=65537), 7), (dict(ab=2 ** 23 + 16), 7), (dict(ab=2184), 3), (dict(a=None), 1), (dict(gc=None), 1), (dict(w=None), 1),
     (dict(ws=None), 1), (dict(ts=None), 1), (dict(out=None), 1), (dict(a=P + 8), 3), (dict(w=P + 8), 3),
     (dict(gc=P + 2), 3), (dict(ws=P + 2), 3), (dict(ts=P + 2), 3),
 ]
