@@ -62,7 +62,8 @@
 namespace moe {
 namespace {
 
-// u g / (1 + e^-g); e^-g overflows to infinity only where the quotient is 0.
+// u g / (1 + e^-g).  Below g = -88.7 e^-g is infinite and the quotient, of at most
+// 2.7e-37, becomes 0.
 __device__ __forceinline__ float gated(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
 // Four consecutive columns of one row, as far as the row goes.
@@ -325,8 +326,8 @@ struct TileWave {
 
   int lane, wave, wm, wn, l16, row0, row_end, col0, stages, start;
   // Load q of a wave fills the stage rows from 8 (q kTileWaves + wave); lane l
-  // fetches the piece that belongs at position l % 8 of row l / 8.  A wave's stage rows of weights are its gate rows, then its up
-  // rows.  Offsets from the tile's first row fit in 32 bits: 256 rows of at most
+  // fetches the piece that belongs at position l % 8 of row l / 8.  A wave's stage
+  // rows of weights are its gate rows, then its up rows.  Offsets from the tile's first row fit in 32 bits: 256 rows of at most
   // kF8MaxRowBytes, and weights of at most 2^16 columns by 2^16 with 256 more.
   int piece, k;  // (the piece of load 0)
   // kTileWaves is even: q turns the bit of swizzle() that rows 16 apart differ in.
@@ -378,7 +379,7 @@ struct TileWave {
 #pragma unroll
     for (int q = 0; q < (kAnew ? 0 : kLoadsA); ++q) {
       const int r = kRowsPerLoad * (q * kTileWaves + wave) + lane / 8;
-      src_a[q] = static_cast<uint32_t>(tile_row(row0, row_end, r) - row0) * static_cast<uint32_t>(a.a_stride) + piece_of(q) * 16;
+      src_a[q] = static_cast<uint32_t>(tile_row(row0, row_end, r) - row0) * stride_a + piece_of(q) * 16;
     }
 #pragma unroll
     for (int q = 0; q < (kAnew ? 0 : kLoadsB); ++q) {

@@ -681,7 +681,7 @@ int moe_gemm_swiglu_quant_f8_workspace_bytes(int32_t rows, int32_t n, size_t* by
  *            moe_gemm_swiglu_quant_f8_workspace_bytes(rows, n) bytes (may be
  *            NULL where that is 0); contents on return unspecified.
  * Requires as moe_grouped_gemm_f8, n % 16 == 0 and 2n <= MOE_GEMM_MAX_N.  One
- * launch where the workspace is of 0 bytes, else two. */
+ * launch, or two where the activations pass through the workspace. */
 int moe_grouped_gemm_swiglu_quant_f8(const void* a, int64_t aRowBytes, int32_t rows, int32_t k,
                                      const int32_t* groupCount, int32_t groups, const void* w, int32_t n,
                                      const float* weightScale, const void* tokenScale,
