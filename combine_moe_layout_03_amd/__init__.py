@@ -812,7 +812,13 @@ def moe_grouped_gemm_f8(a: torch.Tensor, a_row_bytes: int, rows: int, k: int, gr
     row m, a float for each 128 of k, are read from byte m * token_scale_stride
     of ``token_scale`` on (float32 [rows, ceil(k / 128)], the default stride, or
     e4m3 rows at their scales' byte, see ``block_scales_of``); out [rows, n] of
-    bf16, fp16 or fp32 (rows of no expert are not written)."""
+    bf16, fp16 or fp32 (rows of no expert are not written).
+
+    A float32 out is summed in binary32 from exact products.  A 16-bit out, but
+    in the smallest calls, comes from a matrix instruction that drops, of each
+    eight products next to each other, what lies below 2^-13 of the largest: some
+    1.4e-5 of the result of normal rows before its rounding, at most 8.5e-4 of
+    the largest product of each eight, which counts where large products cancel."""
     if token_scale_stride is None:
         token_scale_stride = (k + 127) // 128 * 4
     groups, n = _gemm_f8_sizes(a, a_row_bytes, rows, k, group_count, w, weight_scale, token_scale, token_scale_stride,

@@ -630,9 +630,14 @@ int moe_rms_norm_backward(const void* gradOut, moe_dtype gradOutType, const void
  *   p_b       = sum over i in block b of a[m][i] * w[g][j][i]
  * in binary32, rounded half-even to outType.  For a 16-bit outType p_b may lose,
  * of each eight consecutive products (i from a multiple of 8 on), what lies below
- * 2^-13 of the largest: that is what the 8-bit matrix instruction does, an error
- * of some 1.4e-5 of the result of normally distributed rows, where bf16's half
- * step is 3.9e-3 and fp16's 4.9e-4.  The result does not depend on scheduling.
+ * 2^-13 of the largest: that is what the 8-bit matrix instruction does.  Before
+ * the rounding that is some 1.4e-5 of the result of normally distributed rows
+ * (bf16's half step is 3.9e-3, fp16's 4.9e-4), and for any rows at most 7 * 2^-13
+ * = 8.5e-4 of the largest product of each eight, summed over the eights: where
+ * large products cancel, that can be more than what is left of them.  Calls with
+ * few rows and columns keep every product, so a row may get other last bits in a
+ * call of another size.  MOE_FP32 keeps every product in every call.  The result
+ * does not depend on scheduling.
  *
  * a, aRowBytes, rows, k, groupCount, groups: as moe_grouped_gemm_i8, with e4m3
  *            codes (moe_dispatch's and moe_grouped_gemm_swiglu_quant_f8's rows
