@@ -845,7 +845,8 @@ def moe_grouped_gemm_swiglu_quant_f8(a: torch.Tensor, a_row_bytes: int, rows: in
     rows), weight_scale float32 [groups, 2 * ceil(n / 128), ceil(k / 128)], out
     a uint8 buffer of e4m3 rows (moe_recv_row_bytes(n, MOE_E4M3_BLOCKSCALE)
     bytes each; rows of no expert are not written), and workspace a device
-    buffer of moe_gemm_swiglu_quant_f8_workspace_bytes(rows, n) bytes."""
+    buffer of moe_gemm_swiglu_quant_f8_workspace_bytes(rows, n) bytes (None
+    where a call of that many rows for each expert does not use it)."""
     if token_scale_stride is None:
         token_scale_stride = (k + 127) // 128 * 4
     groups, n = _gemm_f8_sizes(a, a_row_bytes, rows, k, group_count, w, weight_scale, token_scale, token_scale_stride,

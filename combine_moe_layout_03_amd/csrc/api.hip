@@ -854,8 +854,11 @@ int moe_grouped_gemm_swiglu_quant_f8(const void* a, int64_t a_row_bytes, int32_t
   if (!aligned(out, 16) || !aligned(workspace, 16)) return MOE_ERR_BAD_ALIGN;
   const size_t rb = e4m3_row_bytes(n);
   if (out_bytes / rb < static_cast<size_t>(rows)) return MOE_ERR_BUFFER_TOO_SMALL;
+  // The size query does not know the experts: it answers for any number of them.
   size_t need = 0;
-  if ((st = moe_gemm_swiglu_quant_f8_workspace_bytes(rows, n, &need))) return st;
+  if (moe::select::gemm_f8_act(rows, groups, n) &&
+      (st = moe_gemm_swiglu_quant_f8_workspace_bytes(rows, n, &need)))
+    return st;
   if (need > 0 && !workspace) return MOE_ERR_NULL_PTR;
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (!moe::grouped_gemm_f8_fits(rows, groups, n, moe::Form::kGated)) return MOE_ERR_UNSUPPORTED;

@@ -666,8 +666,9 @@ int moe_grouped_gemm_f8(const void* a, int64_t aRowBytes, int32_t rows, int32_t 
                         size_t outBytes, void* stream);
 
 /* Bytes of workspace that moe_grouped_gemm_swiglu_quant_f8 needs for `rows`
- * rows and n activation columns (page section 6.7's convention); at most 4 * n
- * for each of up to 4096 rows, and 0 for some sizes.  Host only. */
+ * rows and n activation columns (page section 6.7's convention), whatever the
+ * number of experts: 4 * n for each of up to 4096 rows, and 0 for more rows.
+ * Host only. */
 int moe_gemm_swiglu_quant_f8_workspace_bytes(int32_t rows, int32_t n, size_t* bytes);
 
 /* The first expert product in 8-bit floats with its gate (the pages' int8 form
@@ -683,8 +684,10 @@ int moe_gemm_swiglu_quant_f8_workspace_bytes(int32_t rows, int32_t n, size_t* by
  *            MOE_E4M3_BLOCKSCALE): e4m3 rows.  Rows that no expert owns are
  *            not written.  Activations must be finite in binary32.
  * workspace  device, 16-byte aligned, of
- *            moe_gemm_swiglu_quant_f8_workspace_bytes(rows, n) bytes (may be
- *            NULL where that is 0); contents on return unspecified.
+ *            moe_gemm_swiglu_quant_f8_workspace_bytes(rows, n) bytes; contents
+ *            on return unspecified.  Not used, and may be NULL, where that is 0
+ *            and where rows > 128 * groups and (rows / 128 + (groups + 1) / 2) *
+ *            ceil(n / 128) >= 192 (whole divisions).
  * Requires as moe_grouped_gemm_f8, n % 16 == 0 and 2n <= MOE_GEMM_MAX_N.  One
  * launch, or two where the activations pass through the workspace. */
 int moe_grouped_gemm_swiglu_quant_f8(const void* a, int64_t aRowBytes, int32_t rows, int32_t k,
