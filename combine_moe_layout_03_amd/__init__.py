@@ -232,7 +232,19 @@ def _row_type(x: torch.Tensor, quant_int8: bool) -> Tuple[int, int, int]:
         raise ValueError("e4m3 rows are dispatched as they are (quant_int8 False)")
     if hidden % 128:
         raise ValueError("e4m3 rows are whole lines of 128 bytes")
+    if hidden > moe_recv_row_bytes(MOE_MAX_HIDDEN, MOE_E4M3_BLOCKSCALE):
+        raise ValueError(f"no e4m3 row has {hidden} bytes")
     return bs, hidden // 2, MOE_BF16
+
+
+def _need_rows(x: torch.Tensor, recv_type: int, row_bytes: int) -> None:
+    """Raise unless a receive buffer of e4m3 rows gets e4m3 rows of its own width, and another buffer none: the
+    library moves them at the width that x has."""
+    if recv_type != MOE_E4M3_BLOCKSCALE:
+        if x.dtype is torch.uint8:
+            raise ValueError("x holds bytes: the receive buffer is not one of e4m3 rows (x_dtype float8_e4m3fn)")
+    elif x.dtype is not torch.uint8 or x.dim() != 2 or x.shape[1] != row_bytes:
+        raise ValueError(f"the receive buffer takes e4m3 rows, uint8 [bs, {row_bytes}]")
 
 
 def moe_recv_row_bytes(hidden: int, recv_type: int) -> int:
@@ -314,8 +326,8 @@ def moe_notify(token_per_expert: torch.Tensor, expert_num_per_rank: int, rank_si
 def moe_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, send_token_idx: torch.Tensor,
                  put_offset: torch.Tensor, recv_base: torch.Tensor, expert_num_per_rank: int,
                  rank_size: int, quant_int8: bool, recv_x: torch.Tensor, stream=None) -> None:
-    """x [bs, hidden] of bf16 or fp16; or e4m3 rows, uint8 [bs, row bytes] (``moe_rms_norm``'s rows; quant_int8
-    False), which are copied whole."""
+    """x [bs, hidden] of bf16 or fp16; or e4m3 rows, uint8 [bs, row bytes] (``moe_rms_norm``'s rows, codes with their
+    scales; quant_int8 False), which are copied whole, to receive rows of the same bytes."""
     if x.dim() != 2 or topk_idx.dim() != 2:
         raise ValueError("x must be [bs, hidden] and topk_idx [bs, topk]")
     bs, hidden, x_type = _row_type(x, quant_int8)
@@ -917,6 +929,7 @@ class EpBuffers:
                    self.recv_base, self.recv_token_per_expert, stream)
 
     def dispatch(self, x, topk_idx, stream=None):
+        _need_rows(x, self.recv_type, self.row_bytes)
         moe_dispatch(x, topk_idx, self.send_token_idx, self.put_offset, self.recv_base, self.epr,
                      self.ranks, self.quant_int8, self.recv_x, stream)
 
@@ -925,6 +938,7 @@ class EpBuffers:
                     self.put_offset, self.recv_base, self.epr, self.ranks, self.out, stream)
 
     def layout_notify_dispatch(self, x, topk_idx, stream=None):
+        _need_rows(x, self.recv_type, self.row_bytes)
         moe_layout_notify_dispatch(x, topk_idx, self.epr, self.ranks, self.quant_int8, self.token_per_expert,
                                    self.token_per_rank, self.send_token_idx, self.bad_id_count,
                                    self.put_offset, self.recv_count, self.recv_base,
@@ -990,6 +1004,7 @@ class EpMultiBuffers:
                          self.recv_base, self.recv_token_per_expert, stream)
 
     def dispatch(self, src: int, x, topk_idx, stream=None):
+        _need_rows(x, self.recv_type, self.row_bytes)
         moe_dispatch_src(x, topk_idx, self.send_token_idx[src], self.put_offset, self.recv_base, self.epr,
                          self.ranks, src, self.quant_int8, self.recv_x, stream)
 
