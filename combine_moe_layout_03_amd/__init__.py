@@ -5,7 +5,8 @@ The functions below carry the names of the C entry points declared in
 include/moe_ep.h and only marshal arguments: they check that tensors are
 CUDA (HIP) tensors of the right dtype and contiguity, pass their device
 pointers and torch's current stream to the C call, and raise ``MoeEpError``
-on a non-zero status.  Every step of the path runs in the library's HIP
+on a non-zero status.  The norm and the products in 8-bit floats also refuse
+tensors of another device than the current one.  Every step of the path runs in the library's HIP
 kernels; there is no fallback.  Importing this module fails loudly if the
 library has not been built (``python combine_moe_layout_03_amd/build.py`` or
 ``__graft_entry__.build()``).
@@ -17,6 +18,7 @@ need for one shape, so a caller can run the pipeline without allocating.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -163,18 +165,35 @@ def _stream(stream) -> Optional[int]:
     return int(stream)
 
 
-def _dev(t: Optional[torch.Tensor], name: str, dtype=None, optional: bool = False):
+@functools.lru_cache(maxsize=None)
+def _several_devices() -> bool:
+    return torch.cuda.device_count() > 1
+
+
+def _here() -> Optional[int]:
+    """The current device, on whose stream a call runs, and None where there is no other (asking each tensor takes 55 ns
+    more than asking whether it is a device's)."""
+    if not _several_devices():
+        return None
+    return torch.cuda.current_device() if _raw_device is None else _raw_device()
+
+
+def _dev(t: Optional[torch.Tensor], name: str, dtype=None, optional: bool = False, here: Optional[int] = None):
+    """t's device pointer; with ``here`` the tensor has to lie on that device."""
     if t is None:
         if optional:
             return None
         raise ValueError(f"{name} is required")
     try:
-        if t.is_cuda and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+        if (t.is_cuda if here is None else t.get_device() == here) and (
+                dtype is None or t.dtype is dtype) and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:  # no tensor
         pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
+    if here is not None and t.get_device() != here:
+        raise ValueError(f"{name} is on another device than the current one")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     raise ValueError(f"{name} must be contiguous")
@@ -702,17 +721,11 @@ def moe_grouped_gemm_deq_i8(a: torch.Tensor, a_row_bytes: int, rows: int, k: int
         _dev(out, "out"), dtype_code(out.dtype), out.nbytes, _stream(stream)))
 
 
-def _on_current_device(t: torch.Tensor, name: str) -> None:
-    """Raise if t lies on another device than the current one, on whose stream the call would run."""
-    if _raw_device is not None and t.get_device() != _raw_device():
-        raise ValueError(f"{name} is on another device than the current one")
-
-
-def _row_matrix(t: torch.Tensor, name: str, shape, dtype=None):
+def _row_matrix(t: torch.Tensor, name: str, shape, dtype, here):
     """The device pointer of an optional matrix of ``shape``."""
     if t is None:
         return None
-    p = _dev(t, name, dtype)
+    p = _dev(t, name, dtype, here=here)
     if t.shape != shape:
         raise ValueError(f"{name} must be [bs, hidden]")
     return p
@@ -728,8 +741,8 @@ def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Op
     ``rows``, a uint8 buffer of bs e4m3 rows (moe_recv_row_bytes(hidden,
     MOE_E4M3_BLOCKSCALE) bytes each, a scale for each 128 columns).  rstd
     float32 [bs] gets 1 / sqrt(...), for ``moe_rms_norm_backward``."""
-    px = _dev(x, "x")
-    _on_current_device(x, "x")
+    here = _here()
+    px = _dev(x, "x", here=here)
     shape, dtype = x.shape, x.dtype
     if len(shape) != 2:
         raise ValueError("x must be [bs, hidden]")
@@ -738,10 +751,11 @@ def moe_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: Op
         raise ValueError("weight must hold hidden floats")
     _need(rstd, "rstd", bs)
     _check("moe_rms_norm", _lib.moe_rms_norm(
-        px, _row_matrix(residual, "residual", shape, dtype), dtype_code(dtype), _dev(weight, "weight", torch.float32),
-        eps, bs, hidden, _row_matrix(sum, "sum", shape, dtype), _row_matrix(out, "out", shape),
-        0 if out is None else dtype_code(out.dtype), _dev(rows, "rows", torch.uint8, optional=True),
-        0 if rows is None else rows.nbytes, _dev(rstd, "rstd", torch.float32, optional=True), _stream(stream)))
+        px, _row_matrix(residual, "residual", shape, dtype, here), dtype_code(dtype),
+        _dev(weight, "weight", torch.float32, here=here), eps, bs, hidden,
+        _row_matrix(sum, "sum", shape, dtype, here), _row_matrix(out, "out", shape, None, here),
+        0 if out is None else dtype_code(out.dtype), _dev(rows, "rows", torch.uint8, True, here),
+        0 if rows is None else rows.nbytes, _dev(rstd, "rstd", torch.float32, True, here), _stream(stream)))
 
 
 def moe_rms_norm_backward_workspace_bytes(bs: int, hidden: int) -> int:
@@ -761,8 +775,8 @@ def moe_rms_norm_backward(grad_out: torch.Tensor, sum: torch.Tensor, weight: tor
     the sum past the norm, is added) and grad_weight float32 [hidden], which
     needs a workspace of moe_rms_norm_backward_workspace_bytes(bs, hidden)
     bytes.  token_mask (uint8 or bool [bs]) takes a token out where it is 0."""
-    pg = _dev(grad_out, "grad_out")
-    _on_current_device(grad_out, "grad_out")
+    here = _here()
+    pg = _dev(grad_out, "grad_out", here=here)
     shape, dtype = sum.shape, sum.dtype
     if len(shape) != 2 or grad_out.shape != shape:
         raise ValueError("grad_out and sum must be [bs, hidden]")
@@ -779,17 +793,19 @@ def moe_rms_norm_backward(grad_out: torch.Tensor, sum: torch.Tensor, weight: tor
     if grad_x is None:
         raise ValueError("grad_x is required")
     _check("moe_rms_norm_backward", _lib.moe_rms_norm_backward(
-        pg, dtype_code(grad_out.dtype), _row_matrix(grad_sum, "grad_sum", shape, dtype), _dev(sum, "sum"),
-        dtype_code(dtype), _dev(weight, "weight", torch.float32), _dev(rstd, "rstd", torch.float32),
-        _dev(token_mask, "token_mask", optional=True), bs, hidden, _row_matrix(grad_x, "grad_x", shape, dtype),
-        _dev(grad_weight, "grad_weight", torch.float32, optional=True), _dev(workspace, "workspace", optional=True),
+        pg, dtype_code(grad_out.dtype), _row_matrix(grad_sum, "grad_sum", shape, dtype, here),
+        _dev(sum, "sum", here=here), dtype_code(dtype), _dev(weight, "weight", torch.float32, here=here),
+        _dev(rstd, "rstd", torch.float32, here=here), _dev(token_mask, "token_mask", None, True, here), bs, hidden,
+        _row_matrix(grad_x, "grad_x", shape, dtype, here),
+        _dev(grad_weight, "grad_weight", torch.float32, True, here), _dev(workspace, "workspace", None, True, here),
         0 if workspace is None else workspace.nbytes, _stream(stream)))
 
 
 _CODE_TYPES = (torch.float8_e4m3fn, torch.uint8, torch.int8)  # e4m3 codes, or the bytes that hold them
 
 
-def _gemm_f8_sizes(a, a_row_bytes, rows, k, group_count, w, weight_scale, token_scale, token_scale_stride, halves):
+def _gemm_f8_sizes(a, a_row_bytes, rows, k, group_count, w, weight_scale, token_scale, token_scale_stride, halves,
+                   here):
     shape = w.shape
     if len(shape) != 3 or shape[2] != k or w.dtype not in _CODE_TYPES or shape[1] % halves:
         raise ValueError("w must be e4m3 [groups, n, k]" if halves == 1 else "w must be e4m3 [groups, 2n, k]")
@@ -805,9 +821,7 @@ def _gemm_f8_sizes(a, a_row_bytes, rows, k, group_count, w, weight_scale, token_
         raise ValueError("a is smaller than (rows - 1) * a_row_bytes + k bytes")
     if token_scale.dtype not in _SCALE_TYPES or not token_scale.is_contiguous():
         raise ValueError("token_scale must be contiguous float32 or bytes")
-    if not token_scale.is_cuda:
-        raise ValueError("token_scale must be a device tensor")
-    _on_current_device(token_scale, "token_scale")
+    _dev(token_scale, "token_scale", here=here)
     if rows > 0 and token_scale.nbytes < (rows - 1) * token_scale_stride + 4 * blocks:
         raise ValueError(f"token_scale holds {token_scale.nbytes} bytes, rows at stride {token_scale_stride} need "
                          f"{(rows - 1) * token_scale_stride + 4 * blocks}")
@@ -833,12 +847,14 @@ def moe_grouped_gemm_f8(a: torch.Tensor, a_row_bytes: int, rows: int, k: int, gr
     the largest product of each eight, which counts where large products cancel."""
     if token_scale_stride is None:
         token_scale_stride = (k + 127) // 128 * 4
+    here = _here()
     groups, n = _gemm_f8_sizes(a, a_row_bytes, rows, k, group_count, w, weight_scale, token_scale, token_scale_stride,
-                               1)
+                               1, here)
     _check("moe_grouped_gemm_f8", _lib.moe_grouped_gemm_f8(
-        _dev(a, "a"), a_row_bytes, rows, k, _dev(group_count, "group_count", torch.int32), groups, _dev(w, "w"), n,
-        _dev(weight_scale, "weight_scale", torch.float32), token_scale.data_ptr(), token_scale_stride,
-        _dev(out, "out"), dtype_code(out.dtype), out.nbytes, _stream(stream)))
+        _dev(a, "a", here=here), a_row_bytes, rows, k, _dev(group_count, "group_count", torch.int32, here=here), groups,
+        _dev(w, "w", here=here), n, _dev(weight_scale, "weight_scale", torch.float32, here=here),
+        token_scale.data_ptr(), token_scale_stride,
+        _dev(out, "out", here=here), dtype_code(out.dtype), out.nbytes, _stream(stream)))
 
 
 def moe_gemm_swiglu_quant_f8_workspace_bytes(rows: int, n: int) -> int:
@@ -861,12 +877,14 @@ def moe_grouped_gemm_swiglu_quant_f8(a: torch.Tensor, a_row_bytes: int, rows: in
     where a call of that many rows for each expert does not use it)."""
     if token_scale_stride is None:
         token_scale_stride = (k + 127) // 128 * 4
+    here = _here()
     groups, n = _gemm_f8_sizes(a, a_row_bytes, rows, k, group_count, w, weight_scale, token_scale, token_scale_stride,
-                               2)
+                               2, here)
     _check("moe_grouped_gemm_swiglu_quant_f8", _lib.moe_grouped_gemm_swiglu_quant_f8(
-        _dev(a, "a"), a_row_bytes, rows, k, _dev(group_count, "group_count", torch.int32), groups, _dev(w, "w"), n,
-        _dev(weight_scale, "weight_scale", torch.float32), token_scale.data_ptr(), token_scale_stride,
-        _dev(out, "out"), out.nbytes, _dev(workspace, "workspace", optional=True),
+        _dev(a, "a", here=here), a_row_bytes, rows, k, _dev(group_count, "group_count", torch.int32, here=here), groups,
+        _dev(w, "w", here=here), n, _dev(weight_scale, "weight_scale", torch.float32, here=here),
+        token_scale.data_ptr(), token_scale_stride,
+        _dev(out, "out", here=here), out.nbytes, _dev(workspace, "workspace", None, True, here),
         0 if workspace is None else workspace.nbytes, _stream(stream)))
 
 
