@@ -136,7 +136,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 // Accesses at any element's address (a row of an odd length starts anywhere).
 typedef f32x4 f32x4_u __attribute__((aligned(4)));
-typedef f32x2 f32x2_u __attribute__((aligned(4)));
 typedef u32x2 u32x2_u __attribute__((aligned(2)));
 typedef u32x4 u32x4_u __attribute__((aligned(2)));
 
