@@ -88,6 +88,7 @@
 #include "device_util.h"
 #include "launch.h"
 #include "gemm.h"
+#include "lds_stage.h"
 #include "quant.h"
 #include "swiglu.h"
 
@@ -98,7 +99,6 @@ namespace {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-#define MOE_LDS __attribute__((address_space(3)))
 
 constexpr int kSK = kGemmStageK;               // bytes of k per stage
 constexpr int kPieces = kSK / 16;              // 16-byte pieces of a row per stage
@@ -143,11 +143,6 @@ __device__ void find_slot(const GemmArgs& a, int64_t slot, int lane, TileSlot* o
     if (tile_base > slot) break;
   }
 }
-
-// s_waitcnt with vmcnt(n) (expcnt and lgkmcnt left at their maxima).
-constexpr int vmcnt_wait(int n) { return 0x0f70 | (n & 15) | ((n >> 4) << 14); }
-// s_waitcnt with lgkmcnt(0) (vmcnt and expcnt left at their maxima).
-constexpr int kLgkmWait0 = 0xc07f;
 
 // Row slots of one launch: enough for any counts, rounded up to whole pairs
 // of XCD blocks when the XCD-aware order applies.
@@ -276,13 +271,6 @@ __global__ __launch_bounds__(kWave * WM * WN) void grouped_gemm_kernel(GemmArgs 
 #pragma unroll
     for (int j = 0; j < kNI; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
 
-  auto barrier = [&]() {
-    __builtin_amdgcn_sched_barrier(0);
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_s_barrier();
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_sched_barrier(0);
-  };
   // Step h (k bytes [64 h, 64 h + 64)) of stage S, its A rows in `ca` and B
   // rows in `cb`: the memory phase, a barrier, the compute phase, a barrier.
   auto step = [&](int S, int h, const uint8_t* ca, const uint8_t* cb, uint8_t* fill_a, uint8_t* fill_b) {
@@ -303,13 +291,13 @@ __global__ __launch_bounds__(kWave * WM * WN) void grouped_gemm_kernel(GemmArgs 
     // this wave's loads of A(S + 1) and B(S + 1); those of B(S + 2) may still run
     if (h == 1) __builtin_amdgcn_s_waitcnt(vmcnt_wait(kLoadsB));
     __builtin_amdgcn_s_waitcnt(kLgkmWait0);  // the fragments are in registers
-    barrier();
+    tile_barrier();
 #pragma unroll
     for (int i = 0; i < kMI; ++i)
 #pragma unroll
       for (int q = 0; q < kNI; ++q)
         acc[i][q] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af[i], bf[q], acc[i][q], 0, 0, 0);
-    barrier();
+    tile_barrier();
   };
   // Stage S: A in sa[S % 2] (refilling sa[(S + 1) % 2]), B in sb[S % 3]
   // (refilling sb[(S + 2) % 3]).
@@ -321,9 +309,9 @@ __global__ __launch_bounds__(kWave * WM * WN) void grouped_gemm_kernel(GemmArgs 
   issue_a(0, sa0);
   issue_b(1, sb1);
   __builtin_amdgcn_s_waitcnt(vmcnt_wait(kLoadsB));  // this wave's loads of stage 0
-  barrier();
+  tile_barrier();
   const int grp = wave / 4;
-  if (grp == 1) barrier();  // the second group runs half a step behind
+  if (grp == 1) tile_barrier();  // the second group runs half a step behind
   // Whole rounds of the rotation (its period is six stages), then the rest.
   const int rounds = stages / 6;
   for (int r = 0; r < rounds; ++r) {
@@ -342,7 +330,7 @@ __global__ __launch_bounds__(kWave * WM * WN) void grouped_gemm_kernel(GemmArgs 
     if (rest > 3) stage(6 * rounds + 3, sa1, sb0, sa0, sb2);
     if (rest > 4) stage(6 * rounds + 4, sa0, sb1, sa1, sb0);
   }
-  if (grp == 0) barrier();  // every wave passes the same number of barriers
+  if (grp == 0) tile_barrier();  // every wave passes the same number of barriers
   // no load may still be writing this workgroup's LDS when it exits
   __builtin_amdgcn_s_waitcnt(vmcnt_wait(0));
 
@@ -389,7 +377,7 @@ __global__ __launch_bounds__(kWave * WM * WN) void grouped_gemm_kernel(GemmArgs 
         const int rs = min(row_base + ii * 16 + r, row_end - 1);
         ts[ii][r] = *reinterpret_cast<const float*>(a.token_scale + static_cast<int64_t>(rs) * a.ts_stride);
       }
-    barrier();
+    tile_barrier();
     uint8_t* const pool = wave < 2 ? sa0 : wave < 4 ? sa1 : wave < 6 ? sb0 : sb1;
     uint8_t* const mine = pool + (wave % 2) * (kHalf * kNI * kWave * 16);
     const uint8_t* const theirs = pool + ((wave % 2) ^ 1) * (kHalf * kNI * kWave * 16);
@@ -403,7 +391,7 @@ __global__ __launch_bounds__(kWave * WM * WN) void grouped_gemm_kernel(GemmArgs 
 #pragma unroll
         for (int j = 0; j < kNI; ++j)
           *reinterpret_cast<i32x4*>(mine + ((ii * kNI + j) * kWave + lane) * 16) = acc[kGive + ii][j];
-      barrier();
+      tile_barrier();
 #pragma unroll
       for (int ii = 0; ii < kHalf; ++ii) {
         float y[kNI][4];

@@ -52,6 +52,7 @@
 #include "device_util.h"
 #include "gemm.h"
 #include "layer.h"
+#include "lds_stage.h"
 #include "router_util.h"
 #include "row_range.h"
 #include "row_slots.h"
@@ -62,7 +63,6 @@ namespace moe {
 namespace {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-#define MOE_LDS __attribute__((address_space(3)))
 
 // Stores below are at any element's address: one unaligned store of 16 bytes
 // costs far less than eight stores.
@@ -294,15 +294,6 @@ constexpr int kTileWaves = 8;
 constexpr int kSK = 128;         // bytes of k per stage
 constexpr int kGroupCols = 1024;  // columns of a group of column tiles
 
-constexpr int vmcnt_wait(int n) { return 0x0f70 | (n & 15) | ((n >> 4) << 14); }
-constexpr int kLgkmWait0 = 0xc07f;
-
-// Position of a 16-byte piece in a stage row: piece p of row r sits at p ^
-// swizzle(r).  The fragments read 16 rows at one piece, rows 16 i + (0 .. 15)
-// of the rows and 32 p + {0-3, 8-11, 16-19, 24-27} (+ 4) of the weights; for
-// both the 16 rows fall into all 16 groups of banks.
-__device__ __forceinline__ int swizzle(int r) { return ((r >> 1) & 7) ^ (((r >> 4) & 1) << 1); }
-
 template <Out kOut, int kTileM, int kTileN, int kWavesM, bool kTail>
 __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) {
   constexpr int kWavesN = kTileWaves / kWavesM;
@@ -415,13 +406,6 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) 
 #pragma unroll
     for (int j = 0; j < kNI; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
 
-  auto barrier = [&]() {
-    __builtin_amdgcn_sched_barrier(0);
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_s_barrier();
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_sched_barrier(0);
-  };
   auto step = [&](int S, int h, const uint8_t* ca, const uint8_t* cb, uint8_t* fill_a, uint8_t* fill_b) {
     if (h == 0) issue_a(S + 1, fill_a);  // into the slot A(S - 1) used
     else issue_b(S + 2, fill_b);         // into the slot B(S - 1) used
@@ -442,13 +426,13 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) 
     // this wave's loads of A(S + 1) and B(S + 1); those of B(S + 2) may still run
     if (h == 1) __builtin_amdgcn_s_waitcnt(vmcnt_wait(kLoadsB));
     __builtin_amdgcn_s_waitcnt(kLgkmWait0);
-    barrier();
+    tile_barrier();
 #pragma unroll
     for (int i = 0; i < kMI; ++i)
 #pragma unroll
       for (int j = 0; j < kNI; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[j], af[i], acc[i][j], 0, 0, 0);
-    barrier();
+    tile_barrier();
   };
   auto stage = [&](int S, const uint8_t* ca, const uint8_t* cb, uint8_t* fill_a, uint8_t* fill_b) {
     step(S, 0, ca, cb, fill_a, fill_b);
@@ -458,9 +442,9 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) 
   issue_a(0, sa0);
   issue_b(1, sb1);
   __builtin_amdgcn_s_waitcnt(vmcnt_wait(kLoadsB));
-  barrier();
+  tile_barrier();
   const int grp = wave / 4;
-  if (grp == 1) barrier();  // the second group runs half a step behind
+  if (grp == 1) tile_barrier();  // the second group runs half a step behind
   const int rounds = stages / 6;
   for (int r = 0; r < rounds; ++r) {
     stage(6 * r, sa0, sb0, sa1, sb2);
@@ -478,7 +462,7 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) 
     if (rest > 3) stage(6 * rounds + 3, sa1, sb0, sa0, sb2);
     if (rest > 4) stage(6 * rounds + 4, sa0, sb1, sa1, sb0);
   }
-  if (grp == 0) barrier();  // every wave passes the same number of barriers
+  if (grp == 0) tile_barrier();  // every wave passes the same number of barriers
   // no load may still be writing this workgroup's LDS
   __builtin_amdgcn_s_waitcnt(vmcnt_wait(0));
 
@@ -487,7 +471,7 @@ __global__ __launch_bounds__(kWave* kTileWaves) void tile_kernel(GemmDeqArgs a) 
   // rows (whole cache lines; stored from the products' layout, 64 bytes of each
   // of 16 rows, 32768 rows took 495 us instead of 469).  The weights' slots are
   // free once every wave's loads have landed and its reads are done.
-  barrier();
+  tile_barrier();
   constexpr int kPieceCols = kOut == Out::kF32 ? 4 : 8;  // columns of a 16-byte piece
   constexpr int kRowPieces = kWaveN / kPieceCols, kWaveBytes = 16 * kRowPieces * 16;
   constexpr int kSlotWaves = kTileN * kSK / kWaveBytes < kTileWaves ? kTileN * kSK / kWaveBytes : kTileWaves;

@@ -53,6 +53,7 @@
 #include "device_util.h"
 #include "gemm.h"
 #include "gemm_f8.h"
+#include "lds_stage.h"
 #include "router_util.h"
 #include "row_range.h"
 #include "row_slots.h"
@@ -260,16 +261,6 @@ constexpr int kSK = kF8Block;     // bytes of k per stage: one block
 constexpr int kRound = 6;         // stages of a round: the slots' places come round again
 constexpr int kGroupCols = 1024;  // rows of weights of a group of column tiles
 
-constexpr int vmcnt_wait(int n) { return 0x0f70 | (n & 15) | ((n >> 4) << 14); }
-constexpr int kLgkmWait0 = 0xc07f;
-#define MOE_LDS __attribute__((address_space(3)))
-
-// Position of a 16-byte piece in a stage row: piece p of row r sits at p ^
-// swizzle(r).  The fragments read 16 rows at one piece, rows 16 i + (0 .. 15)
-// of the rows and 32 p + {0-3, 8-11, 16-19, 24-27} (+ 4) of the weights; for
-// both the 16 rows fall into all 16 groups of banks.
-__device__ __forceinline__ int swizzle(int r) { return ((r >> 1) & 7) ^ (((r >> 4) & 1) << 1); }
-
 // Lane l's value is that of row l of a wave's 64 rows: in every lane, for each
 // fragment i, the value of row 16 i + l % 16.
 __device__ __forceinline__ void spread_rows(float v, float (&to)[4]) {
@@ -456,14 +447,6 @@ struct TileWave {
     for (int q = 0; q < 2; ++q) a[q] &= s * kSK + (4 * q + lane / 16) * 16 < k ? -1 : 0;
   }
 };
-
-__device__ __forceinline__ void tile_barrier() {
-  __builtin_amdgcn_sched_barrier(0);
-  __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  __builtin_amdgcn_s_barrier();
-  __atomic_signal_fence(__ATOMIC_SEQ_CST);
-  __builtin_amdgcn_sched_barrier(0);
-}
 
 // A tile's results.  They pass through LDS, so that a store's lanes lie along
 // rows (whole cache lines): `lds0` and `lds1` of kTileN stage rows each, and
