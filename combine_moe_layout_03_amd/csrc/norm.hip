@@ -58,10 +58,14 @@ struct Chunk {
     }
   }
   // Non-temporally: the rows read would else be pushed out of the caches by the
-  // rows written (h 7168, bf16, us, non-temporally and not, plus a copy of the
-  // results by the next kernel: 512 tokens 6.8 + 6.8, 7.9 + 5.9; 2048: 20.7 +
-  // 25.1, 28.6 + 16.0; 4096: 49.5 + 35.3, 51.3 + 34.3; the gradient 11.7, 12.5;
-  // 25.7, 28.2; 46.3, 48.2).
+  // rows written.  The call gains, the kernel that reads the result next loses (h
+  // 7168, bf16, us, non-temporally and not, in captured runs; the call, the call
+  // and a router's product with 256 experts behind it, and copies of both results
+  // in its place): 1 token 3.3, 3.3; 10.9, 11.0; 7.3, 6.8.  64: 3.7, 3.7; 14.5, 12.5;
+  // 8.2, 8.2.  512: 6.8, 8.4; 24.1, 21.6; 18.1, 15.6.  2048: 26.5, 29.0; 52.8, 48.1;
+  // 50.9, 46.0.  4096: 47.7, 45.2; 79.5, 72.3; 92.9, 93.0.  8192: 89.6, 99.1; 155,
+  // 177; 184, 197.  The gradient and a copy of it: 512 17.0, 16.7; 2048 39.9, 37.7;
+  // 4096 68.1, 64.6; 8192 123, 135.
   __device__ __forceinline__ void store(void* base, int64_t elem) const {
     u32x4* p = reinterpret_cast<u32x4*>(static_cast<uint8_t*>(base) + elem * (kType == Out::kF32 ? 4 : 2));
     __builtin_nontemporal_store(w[0], p);
