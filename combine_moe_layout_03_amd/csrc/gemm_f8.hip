@@ -17,8 +17,8 @@
 // 2^16, 2^3 is kept and 2^2 lost), 1.4e-5 of normal rows' results and at most 7 *
 // 2^-13 of the largest of the eight.  They serve the tiles whose results are
 // rounded to 16 bits, whose half step is 3.9e-3 (bf16) or 4.9e-4 (fp16): widened,
-// 32768 rows, k 2048, n 7168 take 1012 us instead of 523.  split_f8_kernel, which
-// waits for its loads, widens for every type.
+// 32768 rows, k 2048, n 7168 take 1050 us instead of 528, 1000 rows 67 and 63.
+// split_f8_kernel, which waits for its loads, widens for every type.
 //
 // The weights are the first operand and the rows the second: a lane then holds
 // four consecutive columns of one row, and one scale serves all four.
@@ -43,10 +43,10 @@
 // cores: 1000 rows, k 7168, n 2048, 130 (floor 77).
 // As 128 x 256 it also takes the gated product of many rows, a block of 128
 // columns to a workgroup, so that nothing but 8-bit rows leaves the chip: 32768
-// rows 1.73 ms = 1.11 PFLOP/s, 0.9 of a large bf16 product.
+// rows 1.69-1.82 ms over boxes = 1.1 PFLOP/s, 0.9 of a large bf16 product.
 //
 // tile_f8_kernel, 256 x 256 by the 8-bit instruction: 32768 rows, k 2048, n 7168,
-// 523 = 1.84 PFLOP/s.  A stage keeps the matrix cores and LDS busy for 2048
+// 523-546 over boxes = 1.8 PFLOP/s.  A stage keeps the matrix cores and LDS busy for 2048
 // cycles each; of a tile's 33 us, 8 find its rows, load its first stages and store
 // its results with nothing else on the CU.
 #include "block_rows.h"

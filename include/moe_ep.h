@@ -52,7 +52,7 @@ extern "C" {
 typedef enum {
   MOE_BF16 = 0,          /* bfloat16 */
   MOE_FP16 = 1,          /* IEEE binary16 */
-  MOE_FP32 = 2,          /* IEEE binary32 (combine output only) */
+  MOE_FP32 = 2,          /* IEEE binary32 */
   MOE_INT8_ROWSCALE = 3, /* int8 codes + float inverse scale per row (receive buffer) */
   MOE_E4M3_BLOCKSCALE = 4 /* e4m3 codes + float scale per 128 columns of a row */
 } moe_dtype;
