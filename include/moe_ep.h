@@ -673,7 +673,7 @@ int moe_gemm_swiglu_quant_f8_workspace_bytes(int32_t rows, int32_t n, size_t* by
 
 /* The first expert product in 8-bit floats with its gate (the pages' int8 form
  * is section 4.8.1's): with y as moe_grouped_gemm_f8 defines out before its
- * rounding, for the n gate columns and the n up columns,
+ * rounding, every product kept, for the n gate columns and the n up columns,
  *   act[m][j] = (y[m][j] / (1 + e^-y[m][j])) * y[m][n + j]
  * quantised like moe_rms_norm's rows, in blocks of 128 columns.
  * Arguments as moe_grouped_gemm_f8, but for
